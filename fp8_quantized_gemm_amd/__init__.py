@@ -19,10 +19,15 @@ LIB_PATH = os.path.join(_PKG, "libbsq.so")
 BSQ_OK, BSQ_EINVAL, BSQ_EUNSUPPORTED, BSQ_EHIP = 0, 1, 2, 3
 FORMATS = {"nvfp4": 0, "mxfp4": 1, "mxfp8": 2, "fp8": 3}
 ROUNDING = {"rne": 0, "sr": 1}
+GATES = {None: 0, "channel": 1, "row": 2, "full": 3}
+SCORING = {"softmax": 0, "sigmoid": 1}
 ABI_SYMBOLS = ("nvfp4_quantize", "mx_quantize", "quantize_transpose", "quantize_transpose_amax",
                "fp8_quantize_transpose", "swiglu_amax", "swiglu_backward_amax",
                "master_weight_update", "nvfp4_expand", "bs_gemm", "bs_gemm_noalloc",
-               "bs_gemm_nvfp4_bx", "bsq_status_string")
+               "bs_gemm_nvfp4_bx", "block_norm", "block_norm_backward_workspace",
+               "block_norm_backward", "moe_rows", "moe_route_workspace", "moe_route",
+               "moe_route_backward", "moe_gather", "moe_combine", "moe_combine_backward",
+               "bs_gemm_grouped", "bs_gemm_grouped_wgrad", "bsq_status_string")
 
 
 class BsqError(RuntimeError):
@@ -58,6 +63,20 @@ def lib():
         L.bs_gemm_noalloc.argtypes = [I, I64, I64, I64, P, P, P, P, P, P, P, I64, P]
         L.nvfp4_expand.argtypes = [P, P, I64, I64, P, P]
         L.bs_gemm_nvfp4_bx.argtypes = [I64, I64, I64, P, P, P, P, P, P, I64, P]
+        F = ctypes.c_float
+        L.block_norm.argtypes = [P, I, P, I64, I64, P, I, P, F, P, F, P, P, P, P, P, P]
+        L.block_norm_backward_workspace.argtypes = [I64, I64, P]
+        L.block_norm_backward.argtypes = [P, I, P, P, P, I64, I64, P, I, P, F, P, P, P, P, P, P, P, P,
+                                          P, I64, P]
+        L.moe_rows.argtypes = [I64, I, I, I, P]
+        L.moe_route_workspace.argtypes = [I64, I, I, P]
+        L.moe_route.argtypes = [P, I, I64, I, I, P, I, I, F, I, I64, P, P, P, P, P, P, I64, P]
+        L.moe_route_backward.argtypes = [P, I, I64, I, I, P, P, I, I, F, P, P]
+        L.moe_gather.argtypes = [P, I64, I64, I, P, I64, P, P]
+        L.moe_combine.argtypes = [P, I64, I64, P, P, I64, I, P, P]
+        L.moe_combine_backward.argtypes = [P, P, I64, I64, I, P, P, P, I64, P, P, P]
+        L.bs_gemm_grouped.argtypes = [I, I, P, I64, I64, I64, P, P, P, P, P, P, I, P, I64, P]
+        L.bs_gemm_grouped_wgrad.argtypes = [I, I, P, I64, I64, I64, P, P, P, P, P, P, P, P]
         for fn in ABI_SYMBOLS[:-1]:
             getattr(L, fn).restype = I
         L.bsq_status_string.argtypes = [I]
@@ -415,4 +434,298 @@ def bs_gemm_nvfp4_bx(a_codes, a_scales, a_amax, b_x, b_amax, out=None):
     st = lib().bs_gemm_nvfp4_bx(M, N, int(K), _ptr(a_codes), _ptr(a_scales), _ptr(a_amax), _ptr(b_x),
                                 _ptr(b_amax), _ptr(out), ldc, _stream(dev))
     _check("bs_gemm_nvfp4_bx", st)
+    return out
+
+
+# ---------------------------------------------------------------- norms, gate and residual
+
+def _check_stream(x, what="x"):
+    """A 2-D bfloat16 or float32 CUDA tensor (a residual stream), made contiguous."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2
+            and x.dtype in (torch.bfloat16, torch.float32)):
+        raise ValueError(f"{what} must be a 2-D bfloat16 or float32 CUDA tensor")
+    return x.contiguous()
+
+
+def _check_like(t, what, shape, dtype, device):
+    """None, or a contiguous copy of a tensor that must have this shape, type and device."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape)
+            and t.device == device):
+        raise ValueError(f"{what} must be a {dtype} {list(shape)} tensor on {device}")
+    return t.contiguous()
+
+
+def _check_gate(gate, R, C, device):
+    """(kind, contiguous gate) of a block_norm gate: float32 [C] per channel, float32
+    [R, 1] per row, bfloat16 [R, C] per element."""
+    if gate is None:
+        return 0, None
+    if isinstance(gate, torch.Tensor) and gate.device == device:
+        if gate.dtype == torch.float32 and tuple(gate.shape) == (C,):
+            return GATES["channel"], gate.contiguous()
+        if gate.dtype == torch.float32 and tuple(gate.shape) == (R, 1):
+            return GATES["row"], gate.contiguous()
+        if gate.dtype == torch.bfloat16 and tuple(gate.shape) == (R, C):
+            return GATES["full"], gate.contiguous()
+    raise ValueError(f"gate must be float32 [{C}], float32 [{R}, 1] or bfloat16 [{R}, {C}] on {device}")
+
+
+def block_norm(x, o=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-6, amax=False):
+    """The step between two blocks: r = alpha * x + gate * norm(o) * w_post and
+    h = norm(r) * w_pre, x [R, C] bfloat16 or float32, o [R, C] bfloat16.
+
+    o None: h = norm(x) only.  w_post None: o is not normalised.  w_pre None: no
+    h.  gate: None, float32 [C] or [R, 1], or bfloat16 [R, C].  Returns dict(r (x's
+    type), h (bfloat16), rstd_post, rstd_pre (float32 [R]), amax (float32 [1],
+    max|h|, with amax=True)); entries that do not apply are None."""
+    x = _check_stream(x)
+    (R, C), dev = x.shape, x.device
+    o = _check_like(o, "o", (R, C), torch.bfloat16, dev)
+    w_pre = _check_like(w_pre, "w_pre", (C,), torch.float32, dev)
+    w_post = _check_like(w_post, "w_post", (C,), torch.float32, dev)
+    kind, gate = _check_gate(gate, R, C, dev)
+    r = torch.empty_like(x) if o is not None else None
+    h = torch.empty((R, C), dtype=torch.bfloat16, device=dev) if w_pre is not None else None
+    f32 = lambda n: torch.empty(n, dtype=torch.float32, device=dev)
+    rq = f32(R) if w_post is not None else None
+    rp = f32(R) if w_pre is not None else None
+    am = f32(1) if amax and w_pre is not None else None
+    st = lib().block_norm(_ptr(x), int(x.dtype == torch.float32), _ptr(o), R, C, _ptr(w_post), kind,
+                          _ptr(gate), float(alpha), _ptr(w_pre), float(eps), _ptr(r), _ptr(h), _ptr(rq),
+                          _ptr(rp), _ptr(am), _stream(dev))
+    _check("block_norm", st)
+    return dict(r=r, h=h, rstd_post=rq, rstd_pre=rp, amax=am)
+
+
+def block_norm_backward(r, o=None, d_r=None, d_h=None, w_pre=None, w_post=None, gate=None,
+                        rstd_pre=None, rstd_post=None, alpha=1.0):
+    """Gradient of block_norm from d_r [R, C] (r's type, or None) and d_h [R, C]
+    (bfloat16; with w_pre), given the forward's r (its x when there was no o), o
+    and rstd.
+
+    Returns dict(d_x (r's type), d_o (bfloat16), d_gate (the gate's shape and
+    type), d_w_pre, d_w_post (float32 [C])); entries that do not apply are None."""
+    r = _check_stream(r, "r")
+    (R, C), dev = r.shape, r.device
+    o = _check_like(o, "o", (R, C), torch.bfloat16, dev)
+    d_r = _check_like(d_r, "d_r", (R, C), r.dtype, dev)
+    d_h = _check_like(d_h, "d_h", (R, C), torch.bfloat16, dev)
+    w_pre = _check_like(w_pre, "w_pre", (C,), torch.float32, dev)
+    w_post = _check_like(w_post, "w_post", (C,), torch.float32, dev)
+    rstd_pre = _check_like(rstd_pre, "rstd_pre", (R,), torch.float32, dev)
+    rstd_post = _check_like(rstd_post, "rstd_post", (R,), torch.float32, dev)
+    kind, gate = _check_gate(gate, R, C, dev)
+    need = ctypes.c_int64(0)
+    _check("block_norm_backward_workspace",
+           lib().block_norm_backward_workspace(R, C, ctypes.byref(need)))
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    d_x = torch.empty_like(r)
+    d_o = torch.empty_like(o) if o is not None else None
+    d_g = torch.empty_like(gate) if gate is not None else None
+    d_wp = torch.empty_like(w_pre) if w_pre is not None else None
+    d_wq = torch.empty_like(w_post) if w_post is not None else None
+    st = lib().block_norm_backward(_ptr(r), int(r.dtype == torch.float32), _ptr(o), _ptr(d_r), _ptr(d_h),
+                                   R, C, _ptr(w_post), kind, _ptr(gate), float(alpha), _ptr(w_pre),
+                                   _ptr(rstd_post), _ptr(rstd_pre), _ptr(d_x), _ptr(d_o), _ptr(d_g),
+                                   _ptr(d_wp), _ptr(d_wq), _ptr(ws), need.value, _stream(dev))
+    _check("block_norm_backward", st)
+    return dict(d_x=d_x, d_o=d_o, d_gate=d_g, d_w_pre=d_wp, d_w_post=d_wq)
+
+
+# ---------------------------------------------------------------- expert routing
+
+def _scoring(name):
+    if name not in SCORING:
+        raise ValueError(f"unknown scoring {name!r}")
+    return SCORING[name]
+
+
+def moe_rows(tokens, experts, k, align=1):
+    """Rows of the expert-ordered buffers of moe_route for these sizes."""
+    n = ctypes.c_int64(0)
+    _check("moe_rows", lib().moe_rows(int(tokens), int(experts), int(k), int(align), ctypes.byref(n)))
+    return n.value
+
+
+def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1):
+    """Top-k routing of logits [T, E] (bfloat16 or float32; -inf masks an expert).
+
+    Returns dict(experts int32 [T, k] (-1: no candidate left), weights float32 [T,
+    k], offsets int32 [E + 1] (rows of each expert's padded group), row_of int32
+    [T, k] (row of the assignment, -1: none), src int32 [moe_rows] (token * k +
+    slot of the row, -1: padding))."""
+    logits = _check_stream(logits, "logits")
+    (T, E), dev, k = logits.shape, logits.device, int(k)
+    bias = _check_like(bias, "bias", (E,), torch.float32, dev)
+    sc, need = _scoring(scoring), ctypes.c_int64(0)
+    rows = moe_rows(T, E, k, align)
+    _check("moe_route_workspace", lib().moe_route_workspace(T, E, k, ctypes.byref(need)))
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
+    ids, row_of, off, src = i32(T, k), i32(T, k), i32(E + 1), i32(rows)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    ws = i32(need.value // 4)
+    st = lib().moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
+                         1 if normalize else 0, float(scale), int(align), rows, _ptr(ids), _ptr(w), _ptr(off),
+                         _ptr(row_of), _ptr(src), _ptr(ws), need.value, _stream(dev))
+    _check("moe_route", st)
+    return dict(experts=ids, weights=w, offsets=off, row_of=row_of, src=src)
+
+
+def moe_route_backward(logits, experts, d_weights, scoring="softmax", normalize=True, scale=1.0):
+    """d_logits [T, E] (logits' type) from d_weights [T, k] and moe_route's experts."""
+    logits = _check_stream(logits, "logits")
+    (T, E), dev = logits.shape, logits.device
+    if not (isinstance(experts, torch.Tensor) and experts.dim() == 2):
+        raise ValueError("experts must be moe_route's int32 [T, k] tensor")
+    k = experts.shape[1]
+    experts = _check_like(experts, "experts", (T, k), torch.int32, dev)
+    if d_weights is None:
+        raise ValueError("d_weights is required")
+    d_weights = _check_like(d_weights, "d_weights", (T, k), torch.float32, dev)
+    d = torch.empty_like(logits)
+    st = lib().moe_route_backward(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(experts),
+                                  _ptr(d_weights), _scoring(scoring), 1 if normalize else 0, float(scale),
+                                  _ptr(d), _stream(dev))
+    _check("moe_route_backward", st)
+    return d
+
+
+def _check_index(t, what, dim, device):
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.dim() == dim and t.device == device):
+        raise ValueError(f"{what} must be a {dim}-D int32 tensor on {device}")
+    return t.contiguous()
+
+
+def moe_gather(x, src, k, out=None):
+    """Token rows x [T, C] (bfloat16) in expert order [rows, C]: row p is token src[p]
+    // k, zeros where src[p] < 0."""
+    x = _check_input(x)
+    T, C = x.shape
+    src = _check_index(src, "src", 1, x.device)
+    if out is None:
+        out = torch.empty((src.shape[0], C), dtype=torch.bfloat16, device=x.device)
+    else:
+        _check_out(out, src.shape[0], C, torch.bfloat16)
+    _check_device(x, src, out)
+    _check("moe_gather", lib().moe_gather(_ptr(x), T, C, int(k), _ptr(src), src.shape[0], _ptr(out),
+                                          _stream(x.device)))
+    return out
+
+
+def moe_combine(y, row_of, weights=None, out=None):
+    """[T, C] bfloat16: sum over the slots of weights [T, k] (None: 1) times the rows
+    row_of [T, k] of y [rows, C]."""
+    y = _check_input(y)
+    R, C = y.shape
+    row_of = _check_index(row_of, "row_of", 2, y.device)
+    T, k = row_of.shape
+    weights = _check_like(weights, "weights", (T, k), torch.float32, y.device)
+    if out is None:
+        out = torch.empty((T, C), dtype=torch.bfloat16, device=y.device)
+    else:
+        _check_out(out, T, C, torch.bfloat16)
+    _check_device(y, row_of, out)
+    _check("moe_combine", lib().moe_combine(_ptr(y), R, C, _ptr(row_of), _ptr(weights), T, k, _ptr(out),
+                                            _stream(y.device)))
+    return out
+
+
+def moe_combine_backward(d_out, y, src, row_of, weights):
+    """(d_y [rows, C] bfloat16, d_weights float32 [T, k]) of moe_combine from d_out [T, C]."""
+    d_out, y = _check_input(d_out), _check_input(y)
+    (R, C), dev = y.shape, y.device
+    row_of = _check_index(row_of, "row_of", 2, dev)
+    T, k = row_of.shape
+    d_out = _check_like(d_out, "d_out", (T, C), torch.bfloat16, dev)
+    src = _check_index(src, "src", 1, dev)
+    if src.shape[0] != R:
+        raise ValueError(f"src must have y's {R} rows")
+    if weights is None:
+        raise ValueError("weights are required")
+    weights = _check_like(weights, "weights", (T, k), torch.float32, dev)
+    d_y = torch.empty_like(y)
+    d_w = torch.empty_like(weights)
+    _check("moe_combine_backward",
+           lib().moe_combine_backward(_ptr(d_out), _ptr(y), T, C, k, _ptr(src), _ptr(row_of), _ptr(weights), R,
+                                      _ptr(d_y), _ptr(d_w), _stream(dev)))
+    return d_y, d_w
+
+
+# ---------------------------------------------------------------- expert-grouped products
+
+GROUPED_FORMATS = ("nvfp4", "mxfp4", "mxfp8")
+
+
+def _check_offsets(offsets):
+    if not (isinstance(offsets, torch.Tensor) and offsets.dtype == torch.int32 and offsets.dim() == 1
+            and offsets.numel() >= 2):
+        raise ValueError("offsets must be a 1-D int32 tensor of experts + 1 elements")
+    return offsets.numel() - 1
+
+
+def bs_gemm_grouped(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=None, b_amax=None, out=None):
+    """C [R, N] bf16: rows offsets[e] .. offsets[e + 1] - 1 of A [R, K] times B[e] [N, K]
+    transposed, zeros in the rows past the last group.  b_codes [E, N, K / per
+    byte], b_scales [E, N, K / block]; nvfp4: a_amax [1], b_amax [1] or [E]."""
+    if fmt not in GROUPED_FORMATS:
+        raise ValueError(f"unknown grouped format {fmt!r}")
+    E = _check_offsets(offsets)
+    if not (isinstance(b_codes, torch.Tensor) and b_codes.dim() == 3 and b_codes.shape[0] == E
+            and isinstance(b_scales, torch.Tensor) and b_scales.dim() == 3 and b_scales.shape[0] == E
+            and isinstance(a_codes, torch.Tensor) and a_codes.dim() == 2):
+        raise ValueError(f"A must be [rows, K], B [{E}, N, K] codes and scales")
+    _check_device(a_codes, a_scales, b_codes, b_scales, offsets, a_amax, b_amax, out=out)
+    K = a_codes.shape[1] * (1 if fmt == "mxfp8" else 2)
+    _check_operand("A", a_codes, a_scales, K, fmt)
+    _check_operand("B", b_codes.flatten(0, 1), b_scales.flatten(0, 1), K, fmt)
+    if fmt == "nvfp4" and (a_amax is None or b_amax is None):
+        raise ValueError("nvfp4 needs both per-tensor amaxes")
+    _check_amax(a_amax, b_amax)
+    bn = 1
+    if b_amax is not None and fmt == "nvfp4":
+        bn = b_amax.numel()
+        if bn not in (1, E):
+            raise ValueError(f"b_amax must have 1 or {E} elements")
+    M, N = a_codes.shape[0], b_codes.shape[1]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_codes.device)
+    else:
+        _check_out(out, M, N, torch.bfloat16)
+    st = lib().bs_gemm_grouped(FORMATS[fmt], E, _ptr(offsets), M, N, K, _ptr(a_codes), _ptr(a_scales),
+                               _ptr(a_amax), _ptr(b_codes), _ptr(b_scales), _ptr(b_amax), bn, _ptr(out),
+                               max(out.stride(0), N), _stream(out.device))
+    _check("bs_gemm_grouped", st)
+    return out
+
+
+def bs_gemm_grouped_wgrad(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=None, b_amax=None,
+                          out=None):
+    """C [E, M, N] bf16: A [M, R] times B [N, R] transposed over the rows of each group
+    (codes quantized along the rows, R the expert-ordered rows; offsets multiples
+    of the format's scale block)."""
+    if fmt not in GROUPED_FORMATS:
+        raise ValueError(f"unknown grouped format {fmt!r}")
+    E = _check_offsets(offsets)
+    if not (isinstance(a_codes, torch.Tensor) and a_codes.dim() == 2
+            and isinstance(b_codes, torch.Tensor) and b_codes.dim() == 2):
+        raise ValueError("A must be [M, rows], B [N, rows]")
+    _check_device(a_codes, a_scales, b_codes, b_scales, offsets, a_amax, b_amax)
+    R = a_codes.shape[1] * (1 if fmt == "mxfp8" else 2)
+    _check_operand("A", a_codes, a_scales, R, fmt)
+    _check_operand("B", b_codes, b_scales, R, fmt)
+    if fmt == "nvfp4" and (a_amax is None or b_amax is None):
+        raise ValueError("nvfp4 needs both per-tensor amaxes")
+    _check_amax(a_amax, b_amax)
+    M, N = a_codes.shape[0], b_codes.shape[0]
+    if out is None:
+        out = torch.empty((E, M, N), dtype=torch.bfloat16, device=a_codes.device)
+    elif not (out.dtype == torch.bfloat16 and tuple(out.shape) == (E, M, N)):
+        raise ValueError(f"out must be a bfloat16 [{E}, {M}, {N}] tensor")
+    _check_device(a_codes, out)
+    st = lib().bs_gemm_grouped_wgrad(FORMATS[fmt], E, _ptr(offsets), M, N, R, _ptr(a_codes), _ptr(a_scales),
+                                     _ptr(a_amax), _ptr(b_codes), _ptr(b_scales), _ptr(b_amax), _ptr(out),
+                                     _stream(out.device))
+    _check("bs_gemm_grouped_wgrad", st)
     return out

@@ -121,6 +121,61 @@ bsq_status swiglu_common(const void* y, const void* dh, int64_t rows, int64_t f,
                                        amax_row, amax_col, s));
 }
 
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+// Alignment of an element of a BF16 (false) or FP32 (true) array.
+bool aligned_elem(const void* p, bool f32) { return f32 ? aligned4(p) : aligned2(p); }
+
+bool valid_dtype(bsq_dtype t) { return t == BSQ_BF16 || t == BSQ_F32; }
+
+// Checks shared by block_norm and its backward; 0 = fine.
+bsq_status norm_checks(int64_t rows, int64_t cols, bsq_dtype type, const void* o, const float* w_post,
+                       bsq_gate kind, const void* gate, const float* w_pre) {
+  if (rows < 0 || cols < 1 || too_many(rows, cols) || !valid_dtype(type)) return BSQ_EINVAL;
+  if (kind < BSQ_GATE_NONE || kind > BSQ_GATE_FULL) return BSQ_EINVAL;
+  if (cols > 16384) return BSQ_EUNSUPPORTED;
+  if (!aligned4(w_post) || !aligned4(w_pre) || !aligned2(o)) return BSQ_EINVAL;
+  if (rows == 0) return BSQ_OK;                            // empty tensors have null pointers
+  if (!o && (w_post || kind != BSQ_GATE_NONE)) return BSQ_EINVAL;
+  if (!o && !w_pre) return BSQ_EINVAL;                     // nothing to compute
+  if ((kind != BSQ_GATE_NONE) != (gate != nullptr)) return BSQ_EINVAL;
+  if (!aligned_elem(gate, kind != BSQ_GATE_FULL)) return BSQ_EINVAL;
+  return BSQ_OK;
+}
+
+bsq_status route_checks(int64_t tokens, int experts, int k) {
+  if (tokens < 0 || experts < 1 || k < 1 || k > experts) return BSQ_EINVAL;
+  if (experts > bsq::kMoeMaxExperts || k > bsq::kMoeMaxK) return BSQ_EUNSUPPORTED;
+  if (tokens > 0x7FFFFFFF / k) return BSQ_EINVAL;
+  return BSQ_OK;
+}
+
+bsq_status moe_rows_of(int64_t tokens, int experts, int k, int align, int64_t* rows) {
+  const bsq_status st = route_checks(tokens, experts, k);
+  if (st != BSQ_OK) return st;
+  if (align < 1 || align > 512) return BSQ_EINVAL;
+  const int64_t n = tokens * k;
+  int64_t r = n;
+  if (align > 1) r = (n + (n < experts ? n : experts) * (int64_t)(align - 1) + 511) / 512 * 512;
+  if (r > 0x7FFFFFFF) return BSQ_EINVAL;
+  *rows = r;
+  return BSQ_OK;
+}
+
+// Element counts and pointers of the token <-> expert row movers.
+bsq_status mover_checks(int64_t tokens, int64_t cols, int k, int64_t rows) {
+  if (tokens < 0 || cols < 0 || k < 1 || rows < 0 || rows > 0x7FFFFFFF) return BSQ_EINVAL;
+  if (tokens > 0x7FFFFFFF / k || too_many(tokens, cols) || too_many(rows, cols)) return BSQ_EINVAL;
+  return BSQ_OK;
+}
+
+bsq_status grouped_format(bsq_format fmt, bsq::Fmt* f) {
+  if (fmt == BSQ_FP8) return BSQ_EUNSUPPORTED;
+  if (fmt != BSQ_NVFP4 && fmt != BSQ_MXFP4 && fmt != BSQ_MXFP8) return BSQ_EINVAL;
+  *f = fmt == BSQ_NVFP4 ? bsq::kNVFP4 : fmt == BSQ_MXFP4 ? bsq::kMXFP4 : bsq::kMXFP8;
+  return BSQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -366,6 +421,233 @@ bsq_status bs_gemm_noalloc(bsq_format fmt, int64_t M, int64_t N, int64_t K,
                            void* c, int64_t ldc, void* stream) {
   return gemm_common(fmt, M, N, K, a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, c, ldc,
                      stream, true);
+}
+
+bsq_status block_norm(const void* x, bsq_dtype x_type, const void* o, int64_t rows, int64_t cols,
+                      const float* w_post, bsq_gate gate_kind, const void* gate, float alpha,
+                      const float* w_pre, float eps, void* r, void* h, float* rstd_post,
+                      float* rstd_pre, float* amax, void* stream) {
+  const bsq_status st = norm_checks(rows, cols, x_type, o, w_post, gate_kind, gate, w_pre);
+  if (st != BSQ_OK) return st;
+  const bool f32 = x_type == BSQ_F32;
+  if (!(eps > 0.0f)) return BSQ_EINVAL;
+  if (rows == 0 && amax)
+    return aligned4(amax) ? hip_status(bsq::launch_zero_amax(amax, nullptr, static_cast<hipStream_t>(stream)))
+                          : BSQ_EINVAL;
+  if (rows == 0) return BSQ_OK;
+  if ((o != nullptr) != (r != nullptr) || (w_pre != nullptr) != (h != nullptr)) return BSQ_EINVAL;
+  if ((rstd_post && !w_post) || (!w_pre && (rstd_pre || amax))) return BSQ_EINVAL;
+  if (!aligned_elem(x, f32) || !aligned_elem(r, f32) || !aligned2(h) || !aligned4(rstd_post) ||
+      !aligned4(rstd_pre) || !aligned4(amax))
+    return BSQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!x) return BSQ_EINVAL;
+  const int64_t n = rows * cols, xb = n * (f32 ? 4 : 2), gb = gate_kind == BSQ_GATE_FULL ? n * 2 : 0;
+  const void* outs[2] = {r, h};
+  const int64_t outb[2] = {r ? xb : 0, h ? n * 2 : 0};
+  for (int i = 0; i < 2; ++i) {
+    if (!outs[i]) continue;
+    if (overlap(outs[i], outb[i], x, xb) || (o && overlap(outs[i], outb[i], o, n * 2)) ||
+        (gb && overlap(outs[i], outb[i], gate, gb)))
+      return BSQ_EINVAL;
+  }
+  if (r && h && overlap(r, outb[0], h, outb[1])) return BSQ_EINVAL;
+  const bsq::NormFwd a{x,     o,   rows, cols, w_post,    (int)gate_kind, gate, alpha,
+                       w_pre, eps, r,    h,    rstd_post, rstd_pre,       amax, f32};
+  return hip_status(bsq::launch_block_norm(a, s));
+}
+
+bsq_status block_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  if (rows < 0 || cols < 1 || too_many(rows, cols) || !bytes) return BSQ_EINVAL;
+  if (cols > 16384) return BSQ_EUNSUPPORTED;
+  *bytes = bsq::block_norm_bwd_part_bytes(rows, cols);
+  return BSQ_OK;
+}
+
+bsq_status block_norm_backward(const void* r, bsq_dtype r_type, const void* o, const void* d_r,
+                               const void* d_h, int64_t rows, int64_t cols, const float* w_post,
+                               bsq_gate gate_kind, const void* gate, float alpha, const float* w_pre,
+                               const float* rstd_post, const float* rstd_pre, void* d_x, void* d_o,
+                               void* d_gate, float* d_w_pre, float* d_w_post, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  const bsq_status st = norm_checks(rows, cols, r_type, o, w_post, gate_kind, gate, w_pre);
+  if (st != BSQ_OK) return st;
+  const bool f32 = r_type == BSQ_F32;
+  if ((w_pre != nullptr) != (d_w_pre != nullptr) || (w_post != nullptr) != (d_w_post != nullptr) ||
+      ((rows > 0 || gate_kind == BSQ_GATE_CHANNEL) && (gate != nullptr) != (d_gate != nullptr)))
+    return BSQ_EINVAL;
+  if (!aligned_elem(r, f32) || !aligned_elem(d_r, f32) || !aligned_elem(d_x, f32) || !aligned2(d_h) ||
+      !aligned2(d_o) || !aligned4(rstd_post) || !aligned4(rstd_pre) || !aligned4(d_w_pre) ||
+      !aligned4(d_w_post) || !aligned_elem(d_gate, gate_kind != BSQ_GATE_FULL))
+    return BSQ_EINVAL;
+  if (rows > 0) {
+    if (!d_x || (o != nullptr) != (d_o != nullptr)) return BSQ_EINVAL;
+    if ((w_pre != nullptr) != (d_h != nullptr) || (w_pre && (!rstd_pre || !r)) || (w_post && !rstd_post))
+      return BSQ_EINVAL;
+    if (!w_pre && !d_r) return BSQ_EINVAL;                 // no incoming gradient
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < bsq::block_norm_bwd_part_bytes(rows, cols))
+      return BSQ_EINVAL;
+    const int64_t n = rows * cols, xb = n * (f32 ? 4 : 2);
+    const bool full = gate_kind == BSQ_GATE_FULL;
+    const void* outs[3] = {d_x, d_o, full ? d_gate : nullptr};
+    const int64_t outb[3] = {xb, n * 2, n * 2};
+    const void* ins[5] = {r, o, d_r, d_h, full ? gate : nullptr};
+    const int64_t inb[5] = {xb, n * 2, xb, n * 2, n * 2};
+    for (int i = 0; i < 3; ++i) {
+      if (!outs[i]) continue;
+      for (int j = 0; j < 5; ++j)
+        if (ins[j] && overlap(outs[i], outb[i], ins[j], inb[j])) return BSQ_EINVAL;
+      for (int j = 0; j < i; ++j)
+        if (outs[j] && overlap(outs[i], outb[i], outs[j], outb[j])) return BSQ_EINVAL;
+    }
+  }
+  const bsq::NormBwd a{r,     o,         d_r,      d_h, rows, cols,   w_post,  (int)gate_kind, gate,
+                       alpha, w_pre,     rstd_post, rstd_pre, d_x, d_o, d_gate, d_w_pre, d_w_post,
+                       static_cast<float*>(workspace), f32};
+  return hip_status(bsq::launch_block_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status moe_rows(int64_t tokens, int experts, int k, int align, int64_t* rows) {
+  if (!rows) return BSQ_EINVAL;
+  return moe_rows_of(tokens, experts, k, align, rows);
+}
+
+bsq_status moe_route_workspace(int64_t tokens, int experts, int k, int64_t* bytes) {
+  if (!bytes) return BSQ_EINVAL;
+  const bsq_status st = route_checks(tokens, experts, k);
+  if (st != BSQ_OK) return st;
+  *bytes = bsq::moe_route_hist_bytes(tokens, experts);
+  return BSQ_OK;
+}
+
+bsq_status moe_route(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                     const float* bias, bsq_scoring scoring, int normalize, float scale, int align,
+                     int64_t rows, int32_t* experts_out, float* weights, int32_t* offsets,
+                     int32_t* row_of, int32_t* src, void* workspace, int64_t workspace_bytes,
+                     void* stream) {
+  int64_t need = 0;
+  const bsq_status st = moe_rows_of(tokens, experts, k, align, &need);
+  if (st != BSQ_OK) return st;
+  if (!valid_dtype(type) || (scoring != BSQ_SOFTMAX && scoring != BSQ_SIGMOID)) return BSQ_EINVAL;
+  if (rows < need || rows > 0x7FFFFFFF) return BSQ_EINVAL;
+  if (!offsets || !aligned4(offsets) || (rows > 0 && !src) || !aligned4(src)) return BSQ_EINVAL;
+  if (tokens > 0 && (!logits || !experts_out || !weights || !row_of)) return BSQ_EINVAL;
+  if (!aligned_elem(logits, type == BSQ_F32) || !aligned4(bias) || !aligned4(experts_out) ||
+      !aligned4(weights) || !aligned4(row_of) || !aligned4(workspace))
+    return BSQ_EINVAL;
+  const int64_t hist = bsq::moe_route_hist_bytes(tokens, experts);
+  if (hist > 0 && (!workspace || workspace_bytes < hist)) return BSQ_EINVAL;
+  const bsq::RouteArgs a{logits, type == BSQ_F32, tokens, experts, k, bias, scoring == BSQ_SIGMOID, normalize != 0,
+                         scale, align, rows, experts_out, weights, offsets, row_of, src,
+                         static_cast<int32_t*>(workspace)};
+  return hip_status(bsq::launch_moe_route(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status moe_route_backward(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                              const int32_t* experts_in, const float* d_weights, bsq_scoring scoring,
+                              int normalize, float scale, void* d_logits, void* stream) {
+  const bsq_status st = route_checks(tokens, experts, k);
+  if (st != BSQ_OK) return st;
+  if (!valid_dtype(type) || (scoring != BSQ_SOFTMAX && scoring != BSQ_SIGMOID)) return BSQ_EINVAL;
+  if (tokens == 0) return BSQ_OK;
+  const bool f32 = type == BSQ_F32;
+  if (!logits || !experts_in || !d_weights || !d_logits || !aligned_elem(logits, f32) ||
+      !aligned_elem(d_logits, f32) || !aligned4(experts_in) || !aligned4(d_weights))
+    return BSQ_EINVAL;
+  const int64_t lb = tokens * experts * (f32 ? 4 : 2);
+  if (overlap(d_logits, lb, logits, lb)) return BSQ_EINVAL;
+  return hip_status(bsq::launch_moe_route_bwd(logits, f32, tokens, experts, k, experts_in, d_weights,
+                                              scoring == BSQ_SIGMOID, normalize != 0, scale, d_logits,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+bsq_status moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
+                      int64_t rows, void* out, void* stream) {
+  const bsq_status st = mover_checks(tokens, cols, k, rows);
+  if (st != BSQ_OK) return st;
+  if (rows * cols == 0) return BSQ_OK;
+  if ((tokens > 0 && !x) || !src || !out || !aligned2(x) || !aligned4(src) || !aligned2(out))
+    return BSQ_EINVAL;
+  if (overlap(out, rows * cols * 2, x, tokens * cols * 2)) return BSQ_EINVAL;
+  return hip_status(bsq::launch_moe_gather(x, tokens, cols, k, src, rows, out, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status moe_combine(const void* y, int64_t rows, int64_t cols, const int32_t* row_of,
+                       const float* weights, int64_t tokens, int k, void* out, void* stream) {
+  const bsq_status st = mover_checks(tokens, cols, k, rows);
+  if (st != BSQ_OK) return st;
+  if (tokens * cols == 0) return BSQ_OK;
+  if ((rows > 0 && !y) || !row_of || !out || !aligned2(y) || !aligned4(row_of) || !aligned4(weights) ||
+      !aligned2(out))
+    return BSQ_EINVAL;
+  if (overlap(out, tokens * cols * 2, y, rows * cols * 2)) return BSQ_EINVAL;
+  return hip_status(bsq::launch_moe_combine(y, rows, cols, row_of, weights, tokens, k, out,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+bsq_status moe_combine_backward(const void* d_out, const void* y, int64_t tokens, int64_t cols, int k,
+                                const int32_t* src, const int32_t* row_of, const float* weights,
+                                int64_t rows, void* d_y, float* d_weights, void* stream) {
+  const bsq_status st = mover_checks(tokens, cols, k, rows);
+  if (st != BSQ_OK) return st;
+  if (tokens == 0 && rows * cols == 0) return BSQ_OK;
+  if (tokens > 0 && (!row_of || !weights || !d_weights)) return BSQ_EINVAL;
+  if (tokens * cols > 0 && !d_out) return BSQ_EINVAL;
+  if (rows > 0 && !src) return BSQ_EINVAL;
+  if (rows * cols > 0 && (!y || !d_y)) return BSQ_EINVAL;
+  if (!aligned2(d_out) || !aligned2(y) || !aligned2(d_y) || !aligned4(src) || !aligned4(row_of) ||
+      !aligned4(weights) || !aligned4(d_weights))
+    return BSQ_EINVAL;
+  if (rows * cols > 0 &&
+      (overlap(d_y, rows * cols * 2, y, rows * cols * 2) || overlap(d_y, rows * cols * 2, d_out, tokens * cols * 2)))
+    return BSQ_EINVAL;
+  return hip_status(bsq::launch_moe_combine_bwd(d_out, y, tokens, cols, k, src, row_of, weights, rows, d_y,
+                                                d_weights, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status bs_gemm_grouped(bsq_format fmt, int experts, const int32_t* offsets, int64_t rows, int64_t N,
+                           int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
+                           const float* a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
+                           const float* b_amax, int b_amax_n, void* c, int64_t ldc, void* stream) {
+  bsq::Fmt f;
+  const bsq_status st = grouped_format(fmt, &f);
+  if (st != BSQ_OK) return st;
+  if (experts < 1 || experts > 4096 || rows < 0 || rows > 0x7FFFFFFF || N < 0 || K < 0) return BSQ_EINVAL;
+  if (N > 0x7FFFFFFF) return BSQ_EINVAL;
+  if (K % (fmt == BSQ_NVFP4 ? 16 : 32) != 0 || ldc < N) return BSQ_EINVAL;
+  if (too_many(rows, K) || too_many(N, K) || too_many(rows, ldc) || too_many(experts, N * K)) return BSQ_EINVAL;
+  if (rows == 0 || N == 0) return BSQ_OK;
+  if (!offsets || !aligned4(offsets) || !c || !aligned2(c)) return BSQ_EINVAL;
+  if (K > 0 && (!a_codes || !a_scales || !b_codes || !b_scales || !aligned16(a_codes) || !aligned16(b_codes)))
+    return BSQ_EINVAL;
+  if (fmt == BSQ_NVFP4 && (!a_amax || !b_amax || !aligned4(a_amax) || !aligned4(b_amax) ||
+                           (b_amax_n != 1 && b_amax_n != experts)))
+    return BSQ_EINVAL;
+  const bsq::GroupedArgs a{f, experts, offsets, rows, N, K, a_codes, a_scales, a_amax,
+                           b_codes, b_scales, b_amax, b_amax_n, c, ldc};
+  return hip_status(bsq::launch_gemm_grouped(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* offsets, int64_t M, int64_t N,
+                                 int64_t rows, const uint8_t* a_codes, const uint8_t* a_scales,
+                                 const float* a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
+                                 const float* b_amax, void* c, void* stream) {
+  bsq::Fmt f;
+  const bsq_status st = grouped_format(fmt, &f);
+  if (st != BSQ_OK) return st;
+  if (experts < 1 || experts > 4096 || rows < 0 || rows > 0x7FFFFFFF || M < 0 || N < 0) return BSQ_EINVAL;
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF) return BSQ_EINVAL;
+  if (rows % (fmt == BSQ_NVFP4 ? 16 : 32) != 0) return BSQ_EINVAL;
+  if (too_many(M, rows) || too_many(N, rows) || too_many(M, N) || too_many(experts, M * N)) return BSQ_EINVAL;
+  if (M == 0 || N == 0) return BSQ_OK;
+  if (!offsets || !aligned4(offsets) || !c || !aligned2(c)) return BSQ_EINVAL;
+  if (rows > 0 && (!a_codes || !a_scales || !b_codes || !b_scales || !aligned16(a_codes) || !aligned16(b_codes)))
+    return BSQ_EINVAL;
+  if (fmt == BSQ_NVFP4 && (!a_amax || !b_amax || !aligned4(a_amax) || !aligned4(b_amax))) return BSQ_EINVAL;
+  const bsq::GroupedArgs a{f, experts, offsets, M, N, rows, a_codes, a_scales, a_amax,
+                           b_codes, b_scales, b_amax, 1, c, N};
+  return hip_status(bsq::launch_gemm_grouped_wgrad(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -130,4 +130,109 @@ hipError_t launch_gemm(Fmt fmt, int64_t M, int64_t N, int64_t K, const uint8_t* 
                        const uint8_t* b_scales, const float* b_amax, void* c, int64_t ldc,
                        void* scratch, size_t scratch_bytes, hipStream_t s);
 
+// ---------------------------------------------------------------- block norms
+
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateRow = 2, kGateFull = 3 };
+
+// block_norm's arguments (include/bsq.h): x, r FP32 when f32, else BF16.
+struct NormFwd {
+  const void* x;
+  const void* o;                  // null: only h = norm(x)
+  int64_t rows, cols;
+  const float* w_post;            // null: o is not normalised
+  int gate_kind;
+  const void* gate;
+  float alpha;
+  const float* w_pre;             // null: no h
+  float eps;
+  void* r;
+  void* h;
+  float* rstd_post;
+  float* rstd_pre;
+  float* amax;
+  bool f32;
+};
+// 1 <= cols <= 16384, rows > 0; any alignment (16-byte pieces where it allows).
+hipError_t launch_block_norm(const NormFwd& a, hipStream_t s);
+
+struct NormBwd {
+  const void* r;
+  const void* o;
+  const void* d_r;                // null: zero
+  const void* d_h;
+  int64_t rows, cols;
+  const float* w_post;
+  int gate_kind;
+  const void* gate;
+  float alpha;
+  const float* w_pre;
+  const float* rstd_post;
+  const float* rstd_pre;
+  void* d_x;
+  void* d_o;
+  void* d_gate;
+  float* d_w_pre;
+  float* d_w_post;
+  float* part;                    // block_norm_bwd_part_bytes of device memory
+  bool f32;
+};
+int64_t block_norm_bwd_part_bytes(int64_t rows, int64_t cols);
+hipError_t launch_block_norm_bwd(const NormBwd& a, hipStream_t s);
+
+// ---------------------------------------------------------------- expert routing
+
+constexpr int kMoeMaxExperts = 512, kMoeMaxK = 16;
+
+struct RouteArgs {
+  const void* logits;             // [tokens, experts], FP32 when f32, else BF16
+  bool f32;
+  int64_t tokens;
+  int experts, k;
+  const float* bias;              // null: none
+  bool sigmoid, normalize;
+  float scale;
+  int align;
+  int64_t rows;
+  int32_t* ids;
+  float* weights;
+  int32_t* offsets;
+  int32_t* row_of;
+  int32_t* src;
+  int32_t* hist;                  // moe_route_hist_bytes of device memory
+};
+int64_t moe_route_hist_bytes(int64_t tokens, int experts);
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s);
+hipError_t launch_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts, int k,
+                                const int32_t* ids, const float* d_w, bool sigmoid, bool normalize,
+                                float scale, void* d_logits, hipStream_t s);
+hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
+                             int64_t rows, void* out, hipStream_t s);
+hipError_t launch_moe_combine(const void* y, int64_t rows, int64_t cols, const int32_t* row_of,
+                              const float* w, int64_t tokens, int k, void* out, hipStream_t s);
+hipError_t launch_moe_combine_bwd(const void* d_out, const void* y, int64_t tokens, int64_t cols, int k,
+                                  const int32_t* src, const int32_t* row_of, const float* w,
+                                  int64_t rows, void* d_y, float* d_w, hipStream_t s);
+
+// ---------------------------------------------------------------- expert-grouped GEMM
+
+struct GroupedArgs {
+  Fmt fmt;                        // kNVFP4, kMXFP4 or kMXFP8
+  int experts;
+  const int32_t* offsets;         // [experts + 1], device
+  int64_t M, N, K;                // rows: A [M, K], B [experts][N, K]; wgrad: A [M, K], B [N, K], K = rows
+  const uint8_t* ac;
+  const uint8_t* as;
+  const float* aa;
+  const uint8_t* bc;
+  const uint8_t* bs;
+  const float* ba;
+  int ba_n;                       // 1 or experts
+  void* c;                        // rows: [M, N]; wgrad: [experts][M, N]
+  int64_t ldc;
+};
+// C rows of group e = alpha A rows . B_e^T; rows of no group are zeroed.
+hipError_t launch_gemm_grouped(const GroupedArgs& a, hipStream_t s);
+// C_e = alpha A[:, group e] . B[:, group e]^T.
+hipError_t launch_gemm_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+
 }  // namespace bsq

@@ -1,0 +1,538 @@
+// Expert routing: the router (top-k selection, weights and the expert-ordered
+// row plan), its gradient, and the tokens' way to the experts' rows and back
+// (gather, combine, combine's gradient).  The contract is in include/bsq.h.
+//
+// The plan is deterministic: rows of an expert are in token order, then slot
+// order, from counts and ranks (no atomic order is observable: the only atomics
+// count integers in LDS).
+#include "bsq_internal.hpp"
+#include "bsq_wave.hpp"
+
+namespace bsq {
+
+namespace {
+
+__device__ __forceinline__ float logit_at(const void* p, bool f32, int64_t i) {
+  return f32 ? static_cast<const float*>(p)[i] : u2f((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+
+// log(sigmoid(l)) = min(l, 0) - log(1 + exp(-|l|)): finite for every finite l.
+__device__ __forceinline__ float log_sigmoid(float l) {
+  return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
+}
+__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+__device__ __forceinline__ float wave_max_f(float v) { return float_of_key(wave_max_dpp(float_key(v))); }
+
+constexpr float kNegInf = -__builtin_inff();
+
+// Softmax over the lanes with `on` (0 elsewhere).
+__device__ __forceinline__ float lanes_softmax(float l, bool on) {
+  const float m = wave_max_f(on ? l : kNegInf);
+  const float z = on ? expf(l - m) : 0.0f;
+  const float sum = wave_sum(z);
+  return on ? z / sum : 0.0f;
+}
+
+// Max and sum of exp(l - max) over a token's unmasked logits (NV per lane).
+template <int NV>
+__device__ __forceinline__ void full_softmax_stats(const float (&l)[NV], float& m, float& sum) {
+  float lm = kNegInf;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) lm = fmaxf(lm, l[j]);
+  m = wave_max_f(lm);
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) s += l[j] > kNegInf ? expf(l[j] - m) : 0.0f;
+  sum = wave_sum(s);
+}
+
+// A token's logits, expert lane * NV + j in element j; masked (past the last
+// expert, -inf, NaN) ones as -inf.
+template <int NV>
+__device__ __forceinline__ void load_logits(const void* logits, bool f32, int64_t t, int experts, int lane,
+                                            float (&l)[NV]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e = lane * NV + j;
+    const float v = e < experts ? logit_at(logits, f32, t * experts + e) : kNegInf;
+    l[j] = v > kNegInf ? v : kNegInf;              // NaN compares false
+  }
+}
+
+// Selection and weights of one token by one wave: lane j < k gets slot j's
+// expert (-1: none left) and weight.
+template <int NV>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, const float (&bias)[NV],
+                                            int& id, float& w) {
+  float l[NV];
+  load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
+  uint32_t key[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const float s = (l[j] + bias[j]) + 0.0f;       // -0 counts as +0
+    key[j] = s > kNegInf ? float_key(s) : 0u;
+  }
+  id = -1;
+  float sel = kNegInf;
+  for (int s = 0; s < a.k; ++s) {
+    uint32_t best = 0;
+    int bj = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (key[j] > best) best = key[j], bj = j;    // the lowest index of equal keys
+    const uint32_t m = wave_max_dpp(best);
+    if (m == 0) break;                             // nothing left
+    const int win = __builtin_ctzll(__ballot(best == m));
+    const int wj = __builtin_amdgcn_readlane(bj, win);
+    float lv = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (j == wj) lv = l[j];
+      if (lane == win && j == wj) key[j] = 0;
+    }
+    lv = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(lv), win));
+    if (lane == s) {
+      id = win * NV + wj;
+      sel = lv;
+    }
+  }
+  const bool on = id >= 0;
+  if (a.normalize) {
+    w = lanes_softmax(a.sigmoid && on ? log_sigmoid(sel) : sel, on);
+  } else if (a.sigmoid) {
+    w = on ? sigmoid(sel) : 0.0f;
+  } else {
+    float m, sum;
+    full_softmax_stats<NV>(l, m, sum);
+    w = on ? expf(sel - m) / sum : 0.0f;
+  }
+  w = on ? a.scale * w : 0.0f;
+}
+
+constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
+
+// Tokens per workgroup of the two router passes: at most 128 workgroups (each
+// of the second pass reads the counts of all), 64 tokens at least.
+__host__ __device__ inline int route_span(int64_t tokens) {
+  const int64_t s = (tokens + 127) / 128;
+  return (int)(s < 64 ? 64 : (s + 15) / 16 * 16);
+}
+
+// Selection, weights and per-expert counts of the workgroup's tokens.
+template <int NV>
+__device__ __forceinline__ void route_select(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* cnt) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  float bias[NV];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int e = lane * NV + j;
+    bias[j] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+  }
+  for (int64_t t = t0 + wave; t < t1; t += kRouteWaves) {
+    int id;
+    float w;
+    route_token<NV>(a, t, lane, bias, id, w);
+    if (lane < a.k) {
+      a.ids[t * a.k + lane] = id;
+      a.weights[t * a.k + lane] = w;
+      if (id >= 0) atomicAdd(&cnt[id], 1);
+    }
+  }
+}
+
+__device__ __forceinline__ void route_select_any(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* cnt) {
+  if (a.experts <= 64) route_select<1>(a, t0, t1, cnt);
+  else if (a.experts <= 128) route_select<2>(a, t0, t1, cnt);
+  else if (a.experts <= 256) route_select<4>(a, t0, t1, cnt);
+  else route_select<8>(a, t0, t1, cnt);
+}
+
+// Rows of the workgroup's assignments.  before[e]: assignments of expert e in
+// earlier workgroups; total[e]: in all.  The waves take consecutive spans of
+// the assignments; a wave counts its span per expert, and after a prefix over
+// the waves ranks its assignments 64 at a time (lanes of equal expert by
+// ballots over the bits of the expert number).
+struct RouteLds {
+  int32_t total[kMoeMaxExperts];
+  int32_t start[kMoeMaxExperts + 1];                     // padded row offsets
+  int32_t run[kRouteWaves][kMoeMaxExperts];              // next row of (wave, expert)
+};
+
+__device__ __forceinline__ uint64_t lanes_of_same(int v, bool on) {
+  uint64_t m = __ballot(on);
+#pragma unroll
+  for (int b = 0; b < 9; ++b) {                          // experts <= 512
+    const uint64_t s = __ballot((v >> b) & 1);
+    m &= ((v >> b) & 1) ? s : ~s;
+  }
+  return m;
+}
+
+// before[e] is in run[0][e] and total[] filled on entry (a barrier has passed).
+__device__ __forceinline__ void route_place(const RouteArgs& a, int64_t t0, int64_t t1, RouteLds& s, bool first) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.experts;
+  // padded offsets: exclusive prefix over the experts by the first wave
+  if (wave == 0) {
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      const int e = e0 + lane;
+      const int n = e < E ? (s.total[e] + a.align - 1) / a.align * a.align : 0;
+      int inc = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(inc, d, 64);
+        if (lane >= d) inc += up;
+      }
+      if (e < E) s.start[e] = carry + inc - n;
+      carry += __shfl(inc, 63, 64);
+    }
+    if (lane == 0) s.start[E] = carry;
+  }
+  __syncthreads();
+  const int64_t n0 = t0 * a.k, n1 = t1 * a.k;
+  const int64_t span = (((n1 - n0) + kRouteWaves - 1) / kRouteWaves + 63) / 64 * 64;
+  const int64_t w0 = n0 + wave * span, w1 = w0 + span < n1 ? w0 + span : n1;
+  for (int e = tid; e < E; e += kRouteThreads) s.run[0][e] += s.start[e];
+  for (int i = tid; i < (kRouteWaves - 1) * E; i += kRouteThreads) s.run[1 + i / E][i % E] = 0;
+  __syncthreads();
+  // counts of wave w go to row w + 1 and are summed down the waves
+  if (wave + 1 < kRouteWaves)
+    for (int64_t i = w0 + lane; i < w1; i += 64) {
+      const int id = a.ids[i];
+      if (id >= 0) atomicAdd(&s.run[wave + 1][id], 1);
+    }
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads)
+    for (int w = 1; w < kRouteWaves; ++w) s.run[w][e] += s.run[w - 1][e];
+  __syncthreads();
+  for (int64_t i0 = w0; i0 < w1; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const int id = i < w1 ? a.ids[i] : -1;
+    const uint64_t same = lanes_of_same(id, id >= 0);
+    int row = -1;
+    if (id >= 0) {
+      const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+      row = s.run[wave][id] + rank;
+    }
+    // the reads above before the writes, the writes before the next reads
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0 && (same >> lane) == 1) s.run[wave][id] = row + 1;   // the last lane of the expert
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (i < w1) a.row_of[i] = row;
+    if (row >= 0 && row < a.rows) a.src[row] = (int32_t)i;
+  }
+  if (first)
+    for (int e = tid; e <= E; e += kRouteThreads) a.offsets[e] = s.start[e];
+}
+
+// Rows of no assignment: the padding of each group and the rows past the last.
+__device__ __forceinline__ void route_fill(const RouteArgs& a, const RouteLds& s, int blk, int nblk) {
+  for (int e = blk; e < a.experts; e += nblk)
+    for (int64_t r = (int64_t)s.start[e] + s.total[e] + threadIdx.x; r < s.start[e + 1]; r += kRouteThreads)
+      if (r < a.rows) a.src[r] = -1;
+  for (int64_t r = s.start[a.experts] + (int64_t)blk * kRouteThreads + threadIdx.x; r < a.rows;
+       r += (int64_t)nblk * kRouteThreads)
+    a.src[r] = -1;
+}
+
+// Everything in one workgroup (few tokens: launches cost more than the work).
+__global__ __launch_bounds__(kRouteThreads) void k_moe_route_small(RouteArgs a) {
+  __shared__ RouteLds s;
+  const int tid = threadIdx.x;
+  for (int e = tid; e < a.experts; e += kRouteThreads) s.total[e] = s.run[0][e] = 0;
+  __syncthreads();
+  route_select_any(a, 0, a.tokens, s.total);
+  __threadfence_block();                                 // ids written above are read below by other waves
+  __syncthreads();
+  route_place(a, 0, a.tokens, s, true);
+  route_fill(a, s, 0, 1);
+}
+
+__global__ __launch_bounds__(kRouteThreads) void k_moe_select(RouteArgs a) {
+  __shared__ int32_t cnt[kMoeMaxExperts];
+  const int span = route_span(a.tokens);
+  const int64_t t0 = (int64_t)blockIdx.x * span, t1 = t0 + span < a.tokens ? t0 + span : a.tokens;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) cnt[e] = 0;
+  __syncthreads();
+  route_select_any(a, t0, t1, cnt);
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
+}
+
+__global__ __launch_bounds__(kRouteThreads) void k_moe_place(RouteArgs a) {
+  __shared__ RouteLds s;
+  const int tid = threadIdx.x, E = a.experts, nblk = gridDim.x, blk = blockIdx.x;
+  const int span = route_span(a.tokens);
+  const int64_t t0 = (int64_t)blk * span, t1 = t0 + span < a.tokens ? t0 + span : a.tokens;
+  for (int e = tid; e < E; e += kRouteThreads) s.total[e] = s.run[0][e] = 0;
+  __syncthreads();
+  // counts of all workgroups: slices of them by the threads of each expert
+  const int slices = E <= kRouteThreads ? kRouteThreads / E : 1;
+  const int e = tid % E, sl = tid / E;
+  if (sl < slices) {
+    int all = 0, before = 0;
+#pragma unroll 4
+    for (int b = sl; b < nblk; b += slices) {
+      const int v = a.hist[(int64_t)b * E + e];
+      all += v;
+      before += b < blk ? v : 0;
+    }
+    atomicAdd(&s.total[e], all);
+    atomicAdd(&s.run[0][e], before);
+  }
+  __syncthreads();
+  route_place(a, t0, t1, s, blk == 0);
+  route_fill(a, s, blk, nblk);
+}
+
+// Gradient of the weights with respect to the logits, one wave per token.
+template <int NV>
+__global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts,
+                                                       int k, const int32_t* __restrict__ ids,
+                                                       const float* __restrict__ d_w, bool sig, bool normalize,
+                                                       float scale, void* d_logits) {
+  const int lane = threadIdx.x & 63;
+  const int64_t nw = (int64_t)gridDim.x * 4;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tokens; t += nw) {
+    int id = lane < k ? ids[t * k + lane] : -1;
+    if ((unsigned)id >= (unsigned)experts) id = -1;
+    const bool on = id >= 0;
+    const float dp = on ? scale * d_w[t * k + lane] : 0.0f;
+    const float sel = on ? logit_at(logits, f32, t * experts + id) : kNegInf;
+    float l[NV], d[NV];
+    float ds = 0.0f;                                     // this lane's slot: gradient of its logit
+    float mean = 0.0f, m = 0.0f, sum = 1.0f;
+    const bool full = !sig && !normalize;
+    if (full) {
+      load_logits<NV>(logits, f32, t, experts, lane, l);
+      full_softmax_stats<NV>(l, m, sum);
+      const float p = on ? expf(sel - m) / sum : 0.0f;
+      mean = wave_sum(dp * p);
+      ds = dp;                                           // joined with the rest below
+    } else if (normalize) {
+      const float p = lanes_softmax(sig && on ? log_sigmoid(sel) : sel, on);
+      mean = wave_sum(dp * p);
+      ds = on ? p * (dp - mean) : 0.0f;
+      if (sig && on) ds *= sigmoid(-sel);                // d log(sigmoid) = sigmoid(-l)
+    } else if (on) {
+      ds = dp * (sigmoid(sel) * sigmoid(-sel));
+    }
+    const bool any = __ballot(on) != 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) d[j] = 0.0f;
+    for (int s = 0; s < k; ++s) {
+      const int e = __builtin_amdgcn_readlane(id, s);
+      const float v = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(ds), s));
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (e == lane * NV + j) d[j] = v;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (full) d[j] = any && l[j] > kNegInf ? (expf(l[j] - m) / sum) * (d[j] - mean) : 0.0f;
+      const int e = lane * NV + j;
+      if (e < experts) {
+        if (f32) static_cast<float*>(d_logits)[t * experts + e] = d[j];
+        else static_cast<uint16_t*>(d_logits)[t * experts + e] = bf16_rne(d[j]);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows to the experts and back
+
+// out[p] = x[src[p] / k], zeros where src[p] is no assignment.  One wave per
+// row and 512-column slab, 16 bytes per lane.
+template <bool VEC>
+__global__ __launch_bounds__(256) void k_moe_gather(const uint16_t* __restrict__ x, int64_t tokens, int64_t cols,
+                                                    int k, const int32_t* __restrict__ src, int64_t rows,
+                                                    uint16_t* __restrict__ out) {
+  const int lane = threadIdx.x & 63;
+  const int64_t nw = (int64_t)gridDim.x * 4;
+  for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += nw) {
+    const int a = __builtin_amdgcn_readfirstlane(src[p]);
+    const int64_t t = a >= 0 ? a / k : -1;
+    const bool on = t >= 0 && t < tokens;
+    const uint16_t* xr = x + (on ? t : 0) * cols;
+    uint16_t* o = out + p * cols;
+    if constexpr (VEC) {
+#pragma unroll 4
+      for (int64_t c = lane * 8; c < cols; c += 512) {
+        const uint4 v = on ? *reinterpret_cast<const uint4*>(xr + c) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(o + c) = v;
+      }
+    } else {
+#pragma unroll 4
+      for (int64_t c = lane; c < cols; c += 64) o[c] = on ? xr[c] : (uint16_t)0;
+    }
+  }
+}
+
+// out[t] = sum over the slots j, in order, of w[t, j] y[row_of[t, j]] (w null: 1).
+template <bool VEC>
+__global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict__ y, int64_t rows, int64_t cols,
+                                                     const int32_t* __restrict__ row_of,
+                                                     const float* __restrict__ w, int64_t tokens, int k,
+                                                     uint16_t* __restrict__ out) {
+  constexpr int W = VEC ? 512 : 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t slabs = (cols + W - 1) / W, units = tokens * slabs;
+  const int64_t nw = (int64_t)gridDim.x * 4;
+  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += nw) {
+    const int64_t t = u / slabs, c = (u - t * slabs) * W + lane * (W / 64);
+    float acc[8] = {};
+    if (c < cols) {
+      for (int j = 0; j < k; ++j) {
+        const int p = row_of[t * k + j];
+        if (p < 0 || p >= rows) continue;
+        const float wj = w ? w[t * k + j] : 1.0f;
+        if constexpr (VEC) {
+          float v[8];
+          bf16x8_to_f32(*reinterpret_cast<const uint4*>(y + (int64_t)p * cols + c), v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] += wj * v[e];
+        } else {
+          acc[0] += wj * u2f((uint32_t)y[(int64_t)p * cols + c] << 16);
+        }
+      }
+      if constexpr (VEC) *reinterpret_cast<uint4*>(out + t * cols + c) = f32_to_bf16x8(acc);
+      else out[t * cols + c] = bf16_rne(acc[0]);
+    }
+  }
+}
+
+// d_y[p] = w d_out[t], d_w[t, j] = <d_out[t], y[p]> for the assignment (t, j) of
+// row p; rows of none get zeros, slots of none d_w = 0.  One wave per row.
+template <bool VEC>
+__global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restrict__ d_out,
+                                                         const uint16_t* __restrict__ y, int64_t tokens,
+                                                         int64_t cols, int k, const int32_t* __restrict__ src,
+                                                         const int32_t* __restrict__ row_of,
+                                                         const float* __restrict__ w, int64_t rows,
+                                                         uint16_t* __restrict__ d_y, float* __restrict__ d_w) {
+  const int lane = threadIdx.x & 63;
+  const int64_t nw = (int64_t)gridDim.x * 4, slots = tokens * k;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < slots; i += nw * 64)
+    if (row_of[i] < 0) d_w[i] = 0.0f;
+  for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += nw) {
+    const int a = __builtin_amdgcn_readfirstlane(src[p]);
+    const bool on = a >= 0 && a < slots;
+    const int64_t t = on ? a / k : 0;
+    const float wa = on ? w[a] : 0.0f;
+    const uint16_t *g = d_out + t * cols, *yr = y + p * cols;
+    uint16_t* o = d_y + p * cols;
+    float dot = 0.0f;
+    if constexpr (VEC) {
+#pragma unroll 2
+      for (int64_t c = lane * 8; c < cols; c += 512) {
+        uint4 z = make_uint4(0, 0, 0, 0);
+        if (on) {
+          float gv[8], yv[8];
+          bf16x8_to_f32(*reinterpret_cast<const uint4*>(g + c), gv);
+          bf16x8_to_f32(*reinterpret_cast<const uint4*>(yr + c), yv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            dot += gv[e] * yv[e];
+            gv[e] *= wa;
+          }
+          z = f32_to_bf16x8(gv);
+        }
+        *reinterpret_cast<uint4*>(o + c) = z;
+      }
+    } else {
+      for (int64_t c = lane; c < cols; c += 64) {
+        const float gv = on ? u2f((uint32_t)g[c] << 16) : 0.0f;
+        if (on) dot += gv * u2f((uint32_t)yr[c] << 16);
+        o[c] = bf16_rne(gv * wa);
+      }
+    }
+    dot = wave_sum(dot);
+    if (on && lane == 0) d_w[a] = dot;
+  }
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Workgroups for `waves` waves of work, four per workgroup, at most eight
+// workgroups per compute unit.
+unsigned wave_grid(int64_t waves) {
+  const int64_t n = (waves + 3) / 4, cap = (int64_t)(device_cus() > 0 ? device_cus() : 256) * 8;
+  return (unsigned)(n < cap ? n : cap);
+}
+
+}  // namespace
+
+int64_t moe_route_hist_bytes(int64_t tokens, int experts) {
+  const int span = route_span(tokens);
+  return (tokens + span - 1) / span * experts * (int64_t)sizeof(int32_t);
+}
+
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
+  const int span = route_span(a.tokens);
+  const unsigned blocks = (unsigned)((a.tokens + span - 1) / span);
+  if (blocks <= 1) {
+    hipLaunchKernelGGL(k_moe_route_small, dim3(1), dim3(kRouteThreads), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_moe_select, dim3(blocks), dim3(kRouteThreads), 0, s, a);
+  hipLaunchKernelGGL(k_moe_place, dim3(blocks), dim3(kRouteThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts, int k,
+                                const int32_t* ids, const float* d_w, bool sigmoid, bool normalize,
+                                float scale, void* d_logits, hipStream_t s) {
+  const dim3 grid(wave_grid(tokens)), block(256);
+#define BSQ_BWD(NV)                                                                                  \
+  hipLaunchKernelGGL(k_moe_route_bwd<NV>, grid, block, 0, s, logits, f32, tokens, experts, k, ids, d_w, \
+                     sigmoid, normalize, scale, d_logits)
+  if (experts <= 64) BSQ_BWD(1);
+  else if (experts <= 128) BSQ_BWD(2);
+  else if (experts <= 256) BSQ_BWD(4);
+  else BSQ_BWD(8);
+#undef BSQ_BWD
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
+                             int64_t rows, void* out, hipStream_t s) {
+  const dim3 grid(wave_grid(rows)), block(256);
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  uint16_t* op = static_cast<uint16_t*>(out);
+  if (cols % 8 == 0 && al16(x) && al16(out))
+    hipLaunchKernelGGL(k_moe_gather<true>, grid, block, 0, s, xp, tokens, cols, k, src, rows, op);
+  else
+    hipLaunchKernelGGL(k_moe_gather<false>, grid, block, 0, s, xp, tokens, cols, k, src, rows, op);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void* y, int64_t rows, int64_t cols, const int32_t* row_of,
+                              const float* w, int64_t tokens, int k, void* out, hipStream_t s) {
+  const uint16_t* yp = static_cast<const uint16_t*>(y);
+  uint16_t* op = static_cast<uint16_t*>(out);
+  if (cols % 8 == 0 && al16(y) && al16(out))
+    hipLaunchKernelGGL(k_moe_combine<true>, dim3(wave_grid(tokens * ((cols + 511) / 512))), dim3(256), 0, s, yp,
+                       rows, cols, row_of, w, tokens, k, op);
+  else
+    hipLaunchKernelGGL(k_moe_combine<false>, dim3(wave_grid(tokens * ((cols + 63) / 64))), dim3(256), 0, s, yp,
+                       rows, cols, row_of, w, tokens, k, op);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_bwd(const void* d_out, const void* y, int64_t tokens, int64_t cols, int k,
+                                  const int32_t* src, const int32_t* row_of, const float* w,
+                                  int64_t rows, void* d_y, float* d_w, hipStream_t s) {
+  const dim3 grid(wave_grid(rows > 0 ? rows : 1)), block(256);
+  const uint16_t *gp = static_cast<const uint16_t*>(d_out), *yp = static_cast<const uint16_t*>(y);
+  uint16_t* op = static_cast<uint16_t*>(d_y);
+  if (cols % 8 == 0 && al16(d_out) && al16(y) && al16(d_y))
+    hipLaunchKernelGGL(k_moe_combine_bwd<true>, grid, block, 0, s, gp, yp, tokens, cols, k, src, row_of, w, rows, op, d_w);
+  else
+    hipLaunchKernelGGL(k_moe_combine_bwd<false>, grid, block, 0, s, gp, yp, tokens, cols, k, src, row_of, w, rows, op, d_w);
+  return hipGetLastError();
+}
+
+}  // namespace bsq

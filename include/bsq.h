@@ -332,6 +332,181 @@ bsq_status bs_gemm_nvfp4_bx(int64_t M, int64_t N, int64_t K, const uint8_t* a_co
                             const uint8_t* a_scales, const float* a_amax, const void* b_x,
                             const float* b_amax, void* c, int64_t ldc, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the MLP block: norms, gate and residual, and a mixture-of-experts MLP.
+ * The pages' "Performance results" models are pre-norm transformers, and the HN
+ * page's pasted paragraph names a sparse hybrid; the pages give no formulas for
+ * these parts, so the usual definitions are used, written out below.  All
+ * arithmetic is FP32 with one rounding at each store; no result depends on the
+ * order of atomics.
+ * ------------------------------------------------------------------------- */
+
+/* Type of a residual stream or of router logits. */
+typedef enum { BSQ_BF16 = 0, BSQ_F32 = 1 } bsq_dtype;
+/* What a gate is broadcast over: FP32 [cols], FP32 [rows], or BF16 [rows, cols]. */
+typedef enum { BSQ_GATE_NONE = 0, BSQ_GATE_CHANNEL = 1, BSQ_GATE_ROW = 2, BSQ_GATE_FULL = 3 } bsq_gate;
+/* Score of a router logit. */
+typedef enum { BSQ_SOFTMAX = 0, BSQ_SIGMOID = 1 } bsq_scoring;
+
+/*
+ * The step from one block to the next: norm of the block's output, its gate and
+ * the scaled residual, and the norm that opens the next block, in one pass.
+ *   n = o * rstd_post * w_post   (w_post NULL: n = o)
+ *   r = alpha * x + gate * n
+ *   h = BF16(r * rstd_pre * w_pre),  r before its rounding
+ *   rstd = 1 / sqrt(mean over the row of v^2 + eps)
+ *   x    : in, [rows, cols] of x_type.   o : in, BF16 [rows, cols], or NULL:
+ *          then h = norm(x) only (w_post, gate and r must be absent too).
+ *   gate : in, see bsq_gate (NULL with BSQ_GATE_NONE).
+ *   w_post, w_pre : in, FP32 [cols].  w_pre NULL: no h, rstd_pre and amax.
+ *   r    : out, [rows, cols] of x_type.  h : out, BF16 [rows, cols].
+ *   rstd_post, rstd_pre : out, FP32 [rows] (what the backward takes), or NULL.
+ *   amax : out, device FP32 max|h| for the NVFP4 quantizers, or NULL.
+ * Outputs must not overlap inputs.  1 <= cols <= 16384 (BSQ_EUNSUPPORTED above),
+ * eps > 0.  Pointers need their element's alignment only; whole 16-byte pieces
+ * are used where cols % 8 == 0 and all of them are 16-byte aligned.
+ */
+bsq_status block_norm(const void* x, bsq_dtype x_type, const void* o, int64_t rows, int64_t cols,
+                      const float* w_post, bsq_gate gate_kind, const void* gate, float alpha,
+                      const float* w_pre, float eps, void* r, void* h, float* rstd_post,
+                      float* rstd_pre, float* amax, void* stream);
+
+/* Bytes of device workspace block_norm_backward needs for these sizes. */
+bsq_status block_norm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * Gradient of block_norm.  With rn = r * rstd_pre, on = o * rstd_post (w_post
+ * NULL: on = o, its factor 1), a = d_h * w_pre:
+ *   G      = d_r + rstd_pre * (a - rn * mean(a rn))
+ *   d_x    = alpha * G (without o: G)            [rows, cols] of r_type
+ *   d_gate = G * on * w_post, summed over what the gate is broadcast over
+ *            (FP32 [cols] or [rows]; BF16 [rows, cols] for BSQ_GATE_FULL)
+ *   b      = G * gate * w_post;  d_o = rstd_post * (b - on * mean(b on)), BF16
+ *   d_w_pre = sum over rows of d_h rn;  d_w_post = sum over rows of G gate on (FP32)
+ *   r    : in, block_norm's r (without o: its x).  d_r : in, or NULL (zero).
+ *   d_h  : in, BF16; required with w_pre, NULL without.
+ * Column sums are accumulated per workgroup and joined in a fixed order.
+ * rows == 0 writes zeros to d_w_pre, d_w_post and a channel gate's d_gate.
+ *   workspace : device memory, 16-byte aligned, at least the bytes of
+ *               block_norm_backward_workspace.
+ */
+bsq_status block_norm_backward(const void* r, bsq_dtype r_type, const void* o, const void* d_r,
+                               const void* d_h, int64_t rows, int64_t cols, const float* w_post,
+                               bsq_gate gate_kind, const void* gate, float alpha, const float* w_pre,
+                               const float* rstd_post, const float* rstd_pre, void* d_x, void* d_o,
+                               void* d_gate, float* d_w_pre, float* d_w_post, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/*
+ * Rows of the expert-ordered buffers of moe_route: enough for every routing of
+ * tokens * k assignments to groups padded to `align` rows.  align == 1: tokens *
+ * k; else a multiple of 512, so that a quantized reduction over the rows keeps
+ * 16-byte aligned scale rows.
+ */
+bsq_status moe_rows(int64_t tokens, int experts, int k, int align, int64_t* rows);
+
+/* Bytes of device workspace moe_route needs. */
+bsq_status moe_route_workspace(int64_t tokens, int experts, int k, int64_t* bytes);
+
+/*
+ * The router.  Per token: the k experts with the largest logit + bias (FP32
+ * sum), in descending order, ties to the lowest expert; a logit or sum that is
+ * -inf or NaN is masked and never taken.  Weights, times scale:
+ *   softmax, normalize : softmax over the selected logits
+ *   softmax            : softmax over all unmasked logits
+ *   sigmoid, normalize : sigmoid(l) over the sum of the selected sigmoids
+ *   sigmoid            : sigmoid(l)
+ * (the bias steers the selection only).  A slot without a candidate left gets
+ * expert -1, weight 0 and row -1.  Rows: the assignments sorted by expert, then
+ * token, then slot, each expert's group padded to a multiple of align rows.
+ *   logits  : in, [tokens, experts] of type.  bias : in, FP32 [experts] or NULL.
+ *   rows    : length of src, at least moe_rows (BSQ_EINVAL otherwise).
+ *   experts_out : out, int32 [tokens, k].    weights : out, FP32 [tokens, k].
+ *   offsets : out, int32 [experts + 1], first row of each padded group and the end.
+ *   row_of  : out, int32 [tokens, k], row of the assignment.
+ *   src     : out, int32 [rows], token * k + slot of the row, -1 in the padding
+ *             and past the last group.
+ *   workspace : device memory, 4-byte aligned (moe_route_workspace bytes).
+ * 1 <= k <= min(experts, 16), experts <= 512 (BSQ_EUNSUPPORTED above), 1 <= align
+ * <= 512, rows < 2^31.
+ */
+bsq_status moe_route(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                     const float* bias, bsq_scoring scoring, int normalize, float scale, int align,
+                     int64_t rows, int32_t* experts_out, float* weights, int32_t* offsets,
+                     int32_t* row_of, int32_t* src, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+
+/*
+ * Gradient of moe_route's weights with respect to its logits; the selection is
+ * constant.  Logits of no slot get 0, except for softmax without normalize
+ * (masked ones, and tokens without any expert, 0 there too).
+ *   experts_in : in, moe_route's experts.  d_weights : in, FP32 [tokens, k].
+ *   d_logits   : out, [tokens, experts] of type.
+ */
+bsq_status moe_route_backward(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                              const int32_t* experts_in, const float* d_weights, bsq_scoring scoring,
+                              int normalize, float scale, void* d_logits, void* stream);
+
+/*
+ * Token rows to expert order: out[p] = x[src[p] / k], zeros where src[p] is not
+ * in [0, tokens * k).  Its gradient is moe_combine without weights.
+ *   x : in, BF16 [tokens, cols].  src : in, int32 [rows].  out : out, BF16 [rows, cols].
+ */
+bsq_status moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
+                      int64_t rows, void* out, void* stream);
+
+/*
+ * Expert rows back to tokens: out[t] = sum over the slots j, in order, of
+ * weights[t, j] * y[row_of[t, j]], slots whose row is not in [0, rows) left out.
+ *   y : in, BF16 [rows, cols].  row_of : in, int32 [tokens, k].
+ *   weights : in, FP32 [tokens, k], or NULL (1).  out : out, BF16 [tokens, cols].
+ */
+bsq_status moe_combine(const void* y, int64_t rows, int64_t cols, const int32_t* row_of,
+                       const float* weights, int64_t tokens, int k, void* out, void* stream);
+
+/*
+ * Gradient of moe_combine: d_y[p] = weights[a] * d_out[a / k] with a = src[p]
+ * (zeros where a is not in [0, tokens * k)), d_weights[a] = <d_out[a / k], y[p]>,
+ * 0 for slots whose row_of is negative.  src and row_of come from one moe_route.
+ */
+bsq_status moe_combine_backward(const void* d_out, const void* y, int64_t tokens, int64_t cols, int k,
+                                const int32_t* src, const int32_t* row_of, const float* weights,
+                                int64_t rows, void* d_y, float* d_weights, void* stream);
+
+/*
+ * Products grouped by expert, the rows ragged (FPROP and DGRAD of an expert
+ * MLP, prompts and single tokens): for the rows p of group e, offsets[e] <= p <
+ * offsets[e + 1],
+ *   C[p, n] = alpha_e * sum_k deq(A)[p, k] * deq(B_e)[n, k]
+ * and zeros in the rows past offsets[experts].  FP32 accumulation, one BF16
+ * rounding.  Operands as for bs_gemm: A [rows, K], B [experts, N, K], contiguous.
+ *   fmt     : BSQ_NVFP4 (K % 16 == 0), BSQ_MXFP4 or BSQ_MXFP8 (K % 32 == 0);
+ *             BSQ_FP8 is BSQ_EUNSUPPORTED.
+ *   offsets : in, device int32 [experts + 1], ascending (values outside [0,
+ *             rows] are read as the nearest bound).  Groups may be empty.
+ *   a_amax  : NVFP4: device FP32.  b_amax : NVFP4: device FP32 [b_amax_n],
+ *             b_amax_n 1 or experts.  alpha as for bs_gemm; ignored for MX.
+ * 1 <= experts <= 4096, rows < 2^31.  Codes must be 16-byte aligned.
+ */
+bsq_status bs_gemm_grouped(bsq_format fmt, int experts, const int32_t* offsets, int64_t rows, int64_t N,
+                           int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
+                           const float* a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
+                           const float* b_amax, int b_amax_n, void* c, int64_t ldc, void* stream);
+
+/*
+ * Products grouped by expert, the reduction ragged (WGRAD of an expert MLP):
+ *   C[e, m, n] = alpha * sum over the rows p of group e of deq(A)[m, p] * deq(B)[n, p]
+ * with A [M, rows], B [N, rows] quantized along the rows (the column outputs of
+ * quantize_transpose on expert-ordered tensors); an empty group's C is zero.
+ *   offsets : as above, multiples of the scale block (16 NVFP4, 32 MX; other
+ *             values are read as the multiple below).  rows % block == 0.
+ *   a_amax, b_amax : NVFP4: device FP32.   c : out, BF16 [experts, M, N].
+ */
+bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* offsets, int64_t M, int64_t N,
+                                 int64_t rows, const uint8_t* a_codes, const uint8_t* a_scales,
+                                 const float* a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
+                                 const float* b_amax, void* c, void* stream);
+
 /* Static, human-readable name of a status code; host-side, thread-safe. */
 const char* bsq_status_string(bsq_status status);
 
