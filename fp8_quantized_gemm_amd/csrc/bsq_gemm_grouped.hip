@@ -18,6 +18,7 @@
 // Any K (in whole scale blocks) and any group boundary (wgrad: in whole scale
 // blocks): pieces past the range are zero with a unit scale.
 #include "bsq_gemm_common.hpp"
+#include "bsq_gemm_grouped.hpp"
 #include "bsq_internal.hpp"
 
 namespace bsq {
@@ -26,61 +27,6 @@ namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// A tile's group: rows [row0, row1) of it (C rows, or the K range in wgrad).
-struct GroupTile {
-  int e;                  // -1: the rows of no group
-  int64_t row0, row1;
-};
-
-// Group bounds as stored, kept inside [0, rows] and ordered, so that no offset
-// reaches outside the operands.
-__device__ __forceinline__ void group_bounds(const int32_t* off, int e, int64_t rows, int64_t& b, int64_t& n) {
-  b = off[e];
-  n = off[e + 1];
-  b = b < 0 ? 0 : b > rows ? rows : b;
-  n = n < b ? b : n > rows ? rows : n;
-}
-
-// The tile_m-th row tile of MT rows, groups in order, each starting a new
-// tile; after them the tiles of the rows past the last group (e = -1).
-// Returns false past the last tile.  Every wave computes it for itself.
-template <int MT>
-__device__ __forceinline__ bool find_tile(const int32_t* off, int experts, int64_t rows, int tile_m,
-                                          GroupTile& g) {
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int e0 = 0; e0 < experts; e0 += 64) {
-    const int e = e0 + lane;
-    int64_t b = 0, n = 0;
-    if (e < experts) group_bounds(off, e, rows, b, n);
-    const int tiles = (int)((n - b + MT - 1) / MT);
-    int inc = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(inc, d, 64);
-      if (lane >= d) inc += up;
-    }
-    const uint64_t hit = __ballot(before + inc > tile_m);
-    if (hit) {
-      const int w = __builtin_ctzll(hit);
-      const int first = before + __shfl(inc - tiles, w, 64);
-      g.e = e0 + w;
-      const int64_t gb = __shfl((int)b, w, 64);
-      g.row0 = gb + (int64_t)(tile_m - first) * MT;
-      g.row1 = __shfl((int)n, w, 64);
-      // always so for ascending offsets (others could overflow the counts)
-      return g.row0 >= gb && g.row0 < g.row1;
-    }
-    before += __shfl(inc, 63, 64);
-  }
-  int64_t last = off[experts];
-  last = last < 0 ? 0 : last > rows ? rows : last;
-  g.e = -1;
-  g.row0 = last + (int64_t)(tile_m - before) * MT;
-  g.row1 = rows;
-  return g.row0 >= last && g.row0 < rows;
-}
 
 // One operand's rows as seen by a lane.
 struct GsRow {
@@ -153,31 +99,31 @@ __device__ __forceinline__ void gs_expand(const GsFrag<kNVFP4>& f, halfx8 (&x)[4
 }
 
 template <int FMT, int MI, int NI, int W, bool WGRAD>
-__global__ __launch_bounds__(W * 64) void k_gemm_grouped(GroupedArgs a, int tiles_n, int vec_store) {
+__global__ __launch_bounds__(W * 64) void k_gemm_grouped(GroupedArgs a, int tiles_m, int tiles_n, int vec_store) {
   constexpr int MT = MI * 16, NT = NI * 16, RS = NT + 4;
   extern __shared__ __attribute__((aligned(16))) float part[];   // [W][MT][RS]
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r16 = lane & 15, g = lane >> 4;
-  const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
+  const GroupRef ref{a.offsets, a.experts, a.ba_n};
+  int tn;
   constexpr int PB = FMT == kMXFP8 ? 1 : 2, SB = FMT == kNVFP4 ? 16 : 32;   // elements per code / scale byte
   const int64_t code_ld = a.K / PB, scale_ld = a.K / SB;
   int64_t m0, mend, k0 = 0, klen = a.K;
-  const int64_t n0 = (int64_t)tn * NT;
   int e;
   const uint8_t *bc = a.bc, *bs = a.bs;
   uint16_t* c = static_cast<uint16_t*>(a.c);
   if constexpr (WGRAD) {
-    e = blockIdx.y;
+    int tm, lo, hi;
+    e = wgrad_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
     m0 = (int64_t)tm * MT;
     mend = a.M;
-    int64_t b, n;
-    group_bounds(a.offsets, e, a.K, b, n);
-    k0 = b / SB * SB;                                    // whole scale blocks
-    klen = n / SB * SB - k0;
-    klen = klen < 0 ? 0 : klen;
+    GroupTile t;
+    group_range<SB, SB>(ref, e, a.K, lo, hi, t);
+    k0 = t.row0;
+    klen = hi;
     c += (int64_t)e * a.M * a.ldc;
   } else {
     GroupTile t;
-    if (!find_tile<MT>(a.offsets, a.experts, a.M, tm, t)) return;
+    if (!group_tile_rows<MT>(ref, a.M, blockIdx.x, tiles_n, t, tn)) return;
     e = t.e;
     m0 = t.row0;
     mend = t.row1;
@@ -187,6 +133,7 @@ __global__ __launch_bounds__(W * 64) void k_gemm_grouped(GroupedArgs a, int tile
       bs += (int64_t)e * a.N * scale_ld;
     }
   }
+  const int64_t n0 = (int64_t)tn * NT;
   GsRow ra[MI], rb[NI];
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
@@ -281,18 +228,21 @@ hipError_t run_gs(const GroupedArgs& a, hipStream_t s) {
   const int64_t tn = (a.N + NT - 1) / NT;
   // rows: each group may end inside a tile, and so may the rows past the last
   const int64_t tm = WGRAD ? (a.M + MT - 1) / MT : a.M / MT + a.experts + 1;
-  if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t blocks = tm * tn * (WGRAD ? a.experts : 1);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
   const void* fn = reinterpret_cast<const void*>(&k_gemm_grouped<FMT, MI, NI, W, WGRAD>);
   if (LDS > 64 * 1024 && set_lds_limit(fn, LDS) != hipSuccess) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_gemm_grouped<FMT, MI, NI, W, WGRAD>), dim3((unsigned)(tm * tn), WGRAD ? a.experts : 1),
-                     dim3(W * 64), LDS, s, a, (int)tn, vec ? 1 : 0);
+  hipLaunchKernelGGL((k_gemm_grouped<FMT, MI, NI, W, WGRAD>), dim3((unsigned)blocks), dim3(W * 64), LDS,
+                     s, a, (int)tm, (int)tn, vec ? 1 : 0);
   return hipGetLastError();
 }
 
 template <int FMT>
 hipError_t pick_rows(const GroupedArgs& a, hipStream_t s) {
   const int64_t per = a.M / a.experts;                   // rows per group, on average
+  if (FMT == kNVFP4 && per > 160 && gemm_nvfp4_rx_grouped_fits(a, false))
+    return launch_gemm_nvfp4_rx_grouped(a, false, s);
   if (per <= 16) return run_gs<FMT, 1, 4, 4, false>(a, s);
   return run_gs<FMT, 4, 4, 4, false>(a, s);
 }
@@ -306,6 +256,8 @@ hipError_t launch_gemm_grouped(const GroupedArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_gemm_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
+  if (a.fmt == kNVFP4 && a.K / a.experts > 160 && gemm_nvfp4_rx_grouped_fits(a, true))
+    return launch_gemm_nvfp4_rx_grouped(a, true, s);
   if (a.fmt == kNVFP4) return run_gs<kNVFP4, 4, 4, 4, true>(a, s);
   if (a.fmt == kMXFP4) return run_gs<kMXFP4, 4, 4, 4, true>(a, s);
   return run_gs<kMXFP8, 4, 4, 4, true>(a, s);

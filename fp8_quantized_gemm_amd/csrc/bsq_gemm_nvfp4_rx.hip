@@ -57,6 +57,7 @@
 // lanes (sixteen consecutive rows, one chunk) per cycle by 64 four-byte banks;
 // rows of one parity start on the same bank, so their eight slots must differ.
 #include "bsq_gemm_common.hpp"
+#include "bsq_gemm_grouped.hpp"
 #include "bsq_internal.hpp"
 
 #include <mutex>
@@ -354,6 +355,27 @@ __device__ __forceinline__ void rx_kstep(floatx4 (&acc)[8][8], RxRegs& r, const 
   rx_steps<UP, LOADS, KS, 0>(acc, r, unxt, ln, ld);
 }
 
+// K range of a reduction that starts or ends inside a pair (RANGE: K elements
+// lo <= k < hi count, multiples of 16; the units start at a pair boundary at or
+// below lo).  Once pair p has landed, and before its scales are read, the A
+// scales of the blocks outside are zeroed in LDS, one row per thread: an
+// expansion by a zero scale is an exact zero, and the B values it meets are
+// finite.  Only the first and the last pair can need it.
+__device__ __forceinline__ void rx_clip(uint8_t* smem, int p, int NU, int lo, int hi) {
+  const int k0 = p * 256;
+  if (2 * p >= NU || (k0 >= lo && k0 + 256 <= hi)) return;
+  uint4* row = reinterpret_cast<uint4*>(smem + (p & 1) * kRxUnitB + kRxCodeB) + threadIdx.x;
+  const uint4 v = *row;
+  uint32_t sc[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int b = 0; b < 16; ++b) {
+    const int k = k0 + 16 * b;
+    if (k < lo || k >= hi) sc[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
+  }
+  *row = make_uint4(sc[0], sc[1], sc[2], sc[3]);
+  lds_barrier();
+}
+
 // Unit U (parity UP): make unit U + 1 visible to every wave (this wave's own
 // loads of it waited for, then a barrier, which also means every wave has
 // finished reading unit U - 1), then the four steps, which (LOADS: unless
@@ -367,13 +389,14 @@ __device__ __forceinline__ void rx_kstep(floatx4 (&acc)[8][8], RxRegs& r, const 
 // during the units before them), whose buffer its loads then refill.  An
 // even unit reads unit U + 1 from its own pair, made visible by the previous
 // odd unit's barrier (the prologue's for unit 1), and issues no loads.
-template <int UP, bool LOADS>
+template <int UP, bool LOADS, bool RANGE>
 __device__ __forceinline__ void rx_unit(floatx4 (&acc)[8][8], RxRegs& r, uint8_t* smem,
                                         uint32_t smem_lds, const RxSrc& s, int U, int NU, int w,
-                                        int lane, const RxLane& ln) {
+                                        int lane, const RxLane& ln, int lo, int hi) {
   if constexpr (UP == 1) {
     wait_vmcnt<0>();
     lds_barrier();
+    if constexpr (RANGE) rx_clip(smem, (U + 1) >> 1, NU, lo, hi);
   }
   // an odd unit issues pair (U + 3) / 2 (units U + 3, U + 4) into the buffer
   // of units U - 1, U, which every wave has finished reading (the codes and
@@ -405,28 +428,57 @@ __device__ __forceinline__ void rx_prologue_tiles(RxRegs& r) {
   }
 }
 
-template <bool SPLIT>
+// GROUP: kGroupNone, one product; kGroupRows and kGroupWgrad, the
+// expert-grouped products of bsq_gemm_grouped.hpp on the same schedule.
+template <bool SPLIT, int GROUP>
 __global__ __launch_bounds__(kRxThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
                      const uint8_t* a_scales, const float* __restrict__ a_amax,
                      const uint8_t* b_codes, const uint8_t* b_scales,
                      const float* __restrict__ b_amax, uint16_t* __restrict__ c, int64_t ldc,
                      int tiles_m, int tiles_n, int vec_store, int tiles_full, int tail,
-                     floatx4* __restrict__ part) {
+                     floatx4* __restrict__ part, GroupRef g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   // SPLIT: block h * tail + j computes tile tiles_full + j over the K half h
   // and writes FP32 partials; otherwise block b computes tile b.
   const int half = SPLIT ? (int)blockIdx.x / tail : -1;
   const int pid = SPLIT ? tiles_full + ((int)blockIdx.x - half * tail) : (int)blockIdx.x;
   int tm, tn;
-  tile_of_block(pid, tiles_m, tiles_n, tm, tn);
+  int lo = 0, hi = 0;                  // kGroupWgrad: the K elements that count, from the first unit
+  GroupTile gt{};
+  if constexpr (GROUP == kGroupRows) {
+    // A, C and M from the tile's group on; B of its expert
+    if (!group_tile_rows<256>(g, M, pid, tiles_n, gt, tn)) return;
+    tm = 0;
+    a_codes += gt.row0 * (K / 2);
+    a_scales += gt.row0 * (K / 16);
+    c += gt.row0 * ldc;
+    M = gt.row1 - gt.row0;
+    if (gt.e < 0) {
+      K = 0;                           // rows of no group: zeros
+    } else {
+      b_codes += (int64_t)gt.e * N * (K / 2);
+      b_scales += (int64_t)gt.e * N * (K / 16);
+      b_amax += g.ba_n > 1 ? gt.e : 0;
+    }
+  } else if constexpr (GROUP == kGroupWgrad) {
+    const int e = wgrad_tile(pid, tiles_m, tiles_n, tm, tn);
+    c += (int64_t)e * M * ldc;
+    group_range<16, 256>(g, e, K, lo, hi, gt);
+    a_codes += gt.row0 / 2;
+    a_scales += gt.row0 / 16;
+    b_codes += gt.row0 / 2;
+    b_scales += gt.row0 / 16;
+  } else {
+    tile_of_block(pid, tiles_m, tiles_n, tm, tn);
+  }
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = w >> 1, wn = w & 1;
   const uint32_t smem_lds = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)smem;
   RxSrc s;
   // a K half starts NU units in (64 code bytes and 8 scale bytes per unit and row)
-  const int NU = SPLIT ? (int)(K / 256) : (int)(K / 128);
+  const int NU = GROUP == kGroupWgrad ? (hi + 255) / 256 * 2 : SPLIT ? (int)(K / 256) : (int)(K / 128);
   const uint32_t ku = SPLIT ? (uint32_t)(half * NU) : 0u;
   s.a_codes = a_codes + ku * 64;
   s.a_scales = a_scales + ku * 8;
@@ -459,6 +511,7 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
 
   // prologue: pairs 0 and 1 (units 0-3) in flight; unit 0's codes and
   // scales in registers; the A tiles and B tiles 0-6 of step 0 expanded
+  if (GROUP == kGroupNone || NU > 0) {
   RxRegs r;
   rx_stage(s, 0, smem_lds, w, lane);
   if (NU > 2) rx_stage(s, 1, smem_lds + kRxUnitB, w, lane);
@@ -466,6 +519,7 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
   if (NU > 2) wait_vmcnt<kRxLoadsPerPair>();
   else wait_vmcnt<0>();
   lds_barrier();
+  if constexpr (GROUP == kGroupWgrad) rx_clip(smem, 0, NU, lo, hi);
 #pragma unroll
   for (int T = 0; T < 16; ++T) {
     const uint4 q = *reinterpret_cast<const uint4*>(smem + (T < 8 ? ln.ca[0] : ln.cb[0]) + (T & 7) * 2048);
@@ -482,12 +536,14 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
   // loads; NU is even
   int U = 0;
   for (; U + 4 < NU; U += 2) {
-    rx_unit<0, false>(acc, r, smem, smem_lds, s, U, NU, w, lane, ln);
-    rx_unit<1, true>(acc, r, smem, smem_lds, s, U + 1, NU, w, lane, ln);
+    rx_unit<0, false, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U, NU, w, lane, ln, lo, hi);
+    rx_unit<1, true, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U + 1, NU, w, lane, ln, lo, hi);
   }
   for (; U < NU; U += 2) {
-    rx_unit<0, false>(acc, r, smem, smem_lds, s, U, NU, w, lane, ln);
-    rx_unit<1, false>(acc, r, smem, smem_lds, s, U + 1, NU, w, lane, ln);
+    rx_unit<0, false, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U, NU, w, lane, ln, lo, hi);
+    rx_unit<1, false, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U + 1, NU, w, lane, ln, lo, hi);
+  }
+
   }
 
   // every wave is done with the unit buffers (the epilogue reuses the LDS),
@@ -643,24 +699,51 @@ hipError_t launch_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* 
   const bool vec_store = (ldc % 8 == 0) && (reinterpret_cast<uintptr_t>(c) % 16 == 0);
   if (tail < 0 || tail > tiles || (tail > 0 && (part == nullptr || K % 512 != 0)))
     return hipErrorInvalidValue;
-  if (set_lds_limit(reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false>), kRxLds) != hipSuccess ||
-      set_lds_limit(reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<true>), kRxLds) != hipSuccess)
+  if (set_lds_limit(reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false, kGroupNone>), kRxLds) != hipSuccess ||
+      set_lds_limit(reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<true, kGroupNone>), kRxLds) != hipSuccess)
     return hipErrorInvalidConfiguration;
   uint16_t* cp = static_cast<uint16_t*>(c);
   floatx4* pp = static_cast<floatx4*>(part);
   // the full waves, then the split last wave (two K halves per tile) and the
   // join of its partials
   if (tiles_full > 0)
-    hipLaunchKernelGGL(k_gemm_nvfp4_rx<false>, dim3((unsigned)tiles_full), dim3(kRxThreads), kRxLds, s,
+    hipLaunchKernelGGL((k_gemm_nvfp4_rx<false, kGroupNone>), dim3((unsigned)tiles_full), dim3(kRxThreads), kRxLds, s,
                        M, N, K, ac, as, aa, bc, bs, ba, cp, ldc, tiles_m, tiles_n, vec_store ? 1 : 0,
-                       tiles_full, 1, nullptr);
+                       tiles_full, 1, nullptr, GroupRef{});
   if (tail > 0) {
-    hipLaunchKernelGGL(k_gemm_nvfp4_rx<true>, dim3((unsigned)(2 * tail)), dim3(kRxThreads), kRxLds, s,
+    hipLaunchKernelGGL((k_gemm_nvfp4_rx<true, kGroupNone>), dim3((unsigned)(2 * tail)), dim3(kRxThreads), kRxLds, s,
                        M, N, K, ac, as, aa, bc, bs, ba, cp, ldc, tiles_m, tiles_n, vec_store ? 1 : 0,
-                       tiles_full, tail, pp);
+                       tiles_full, tail, pp, GroupRef{});
     hipLaunchKernelGGL(k_gemm_nvfp4_rx_join, dim3((unsigned)(4 * tail)), dim3(kRxThreads), 0, s, M, N, pp,
                        aa, ba, cp, ldc, tiles_m, tiles_n, tiles_full, tail, vec_store ? 1 : 0);
   }
+  return hipGetLastError();
+}
+
+bool gemm_nvfp4_rx_grouped_fits(const GroupedArgs& a, bool wgrad) {
+  // wgrad loads whole pairs of units, from a pair boundary at or below a group's first row
+  return a.K > 0 && a.K % 256 == 0 && a.N < ((int64_t)1 << 31) - 256 &&
+         gemm_nvfp4_rx_fits(wgrad ? a.M : 256, a.N, a.K, a.ac, a.as, a.bc, a.bs);
+}
+
+hipError_t launch_gemm_nvfp4_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s) {
+  const int64_t tn = (a.N + 255) / 256;
+  const int64_t tm = wgrad ? (a.M + 255) / 256 : a.M / 256 + a.experts + 1;
+  if (tm * tn * (wgrad ? a.experts : 1) > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const void* fn = wgrad ? reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false, kGroupWgrad>)
+                         : reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false, kGroupRows>);
+  if (set_lds_limit(fn, kRxLds) != hipSuccess) return hipErrorInvalidConfiguration;
+  const bool vec_store = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+  const GroupRef g{a.offsets, a.experts, a.ba_n};
+  uint16_t* cp = static_cast<uint16_t*>(a.c);
+  if (wgrad)
+    hipLaunchKernelGGL((k_gemm_nvfp4_rx<false, kGroupWgrad>), dim3((unsigned)(tm * tn * a.experts)),
+                       dim3(kRxThreads), kRxLds, s, a.M, a.N, a.K, a.ac, a.as, a.aa, a.bc, a.bs, a.ba, cp, a.ldc,
+                       (int)tm, (int)tn, vec_store ? 1 : 0, 0, 1, nullptr, g);
+  else
+    hipLaunchKernelGGL((k_gemm_nvfp4_rx<false, kGroupRows>), dim3((unsigned)(tm * tn)), dim3(kRxThreads), kRxLds,
+                       s, a.M, a.N, a.K, a.ac, a.as, a.aa, a.bc, a.bs, a.ba, cp, a.ldc, (int)tm, (int)tn,
+                       vec_store ? 1 : 0, 0, 1, nullptr, g);
   return hipGetLastError();
 }
 

@@ -234,5 +234,10 @@ struct GroupedArgs {
 hipError_t launch_gemm_grouped(const GroupedArgs& a, hipStream_t s);
 // C_e = alpha A[:, group e] . B[:, group e]^T.
 hipError_t launch_gemm_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+// The same products on the 256 x 256 NVFP4 kernel: whether it takes these
+// operands (K resp. rows % 256 == 0, codes and scales 16-byte aligned, 32-bit
+// offsets), and its launch.
+bool gemm_nvfp4_rx_grouped_fits(const GroupedArgs& a, bool wgrad);
+hipError_t launch_gemm_nvfp4_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s);
 
 }  // namespace bsq

@@ -68,6 +68,8 @@ ROWS = [  # sizes, rows past the last group, N, K
     ([33, 200], 31, 65, 1408),
     ([300], 0, 300, 544),
     ([257, 0, 511, 256, 3], 100, 520, 1024),
+    ([180] * 67 + [0, 1, 700], 300, 40, 256),
+    ([1, 1023, 0, 2], 0, 33, 768),
 ]
 
 
@@ -142,6 +144,8 @@ WGRAD = [  # sizes (in scale blocks), blocks past the last group, M, N
     ([8, 16, 40, 0], 16, 65, 257),
     ([17, 15, 33, 31, 64, 0, 1, 95], 0, 256, 300),
     ([100, 1, 27], 128, 520, 264),
+    ([5, 6, 1, 100, 0, 2, 142], 0, 300, 40),
+    ([1, 510, 0, 1], 0, 257, 64),
 ]
 
 
