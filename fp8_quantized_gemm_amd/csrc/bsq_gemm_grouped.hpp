@@ -33,12 +33,15 @@ __device__ __forceinline__ void group_bounds(const int32_t* off, int e, int64_t 
   n = n < b ? b : n > rows ? rows : n;
 }
 
-__device__ __forceinline__ int lanes_prefix(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(v, d, 64);
-    if (lane >= d) v += up;
-  }
+// Inclusive prefix sum over the 64 lanes: within rows of 16 by shifts, then the
+// rows' totals carried on (DPP: no LDS round trips on the way to the first load).
+__device__ __forceinline__ int lanes_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row 0 -> 1, 2 -> 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row 1 -> 2, 3
   return v;
 }
 
@@ -58,7 +61,7 @@ __device__ __forceinline__ bool group_tile_rows(const GroupRef& g, int64_t rows,
     b = n = 0;
     if (e < g.experts) group_bounds(g.offsets, e, rows, b, n);
     mine = (int)((n - b + MT - 1) / MT);
-    inc = lanes_prefix(mine, lane);
+    inc = lanes_prefix(mine);
   };
   for (e0 = 0; e0 < g.experts; e0 += 64) {
     block(e0);
@@ -118,6 +121,30 @@ __device__ __forceinline__ void group_range(const GroupRef& g, int e, int64_t ro
   t.row1 = n;
   lo = (int)(b - t.row0);
   hi = n > b ? (int)(n - t.row0) : 0;
+}
+
+// Most row tiles of MT rows there can be: every group with rows (the rows of no
+// group count as one) has at most one partly filled tile.
+inline int64_t max_row_tiles(int64_t rows, int experts, int MT) {
+  const int64_t g = rows < experts + 1 ? rows : experts + 1;
+  return (rows - g) / MT + g;
+}
+
+// Zeros in the 256 x 256 tile at (m0, n0) of c [M, N] (256 threads): the rows of
+// no group, and the product of an empty group.
+__device__ __forceinline__ void zero_tile(uint16_t* c, int64_t ldc, int64_t M, int64_t N, int64_t m0, int64_t n0,
+                                          int vec_store) {
+  for (int i = threadIdx.x; i < 256 * 32; i += 256) {
+    const int64_t m = m0 + (i >> 5), n = n0 + (i & 31) * 8;
+    if (m >= M) return;
+    uint16_t* dst = c + m * ldc + n;
+    if (vec_store && n + 7 < N) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int e = 0; e < 8; ++e)
+        if (n + e < N) dst[e] = 0;
+    }
+  }
 }
 
 }  // namespace

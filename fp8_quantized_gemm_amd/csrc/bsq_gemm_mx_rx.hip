@@ -43,6 +43,7 @@
 // one basic block (the compiler does not see the MFMAs' operand timing and
 // must not move work across a branch next to them).
 #include "bsq_gemm_common.hpp"
+#include "bsq_gemm_grouped.hpp"
 #include "bsq_internal.hpp"
 
 namespace bsq {
@@ -214,16 +215,37 @@ __device__ __forceinline__ void mr_steps(floatx16 (&acc)[4][4], const MrFrag<FMT
   }
 }
 
+// K range of a reduction that starts or ends inside a scale period (RANGE: K
+// elements lo <= k < hi count, multiples of 32; the units start at a period
+// boundary at or below lo): once unit u has landed, and before its fragments are
+// read, the A codes of the blocks outside are zeroed in LDS, one row per thread.
+// Their products with finite B values and scales are exact zeros.  Only units of
+// the first and the last period can need it.
+template <int FMT>
+__device__ __forceinline__ void mr_clip(uint8_t* smem, int u, int NU, int lo, int hi) {
+  constexpr int KU = fp8_elems(FMT) ? 128 : 256, CB = fp8_elems(FMT) ? 2 : 1;   // K per unit, chunks per block
+  const int k0 = u * KU;
+  if (u >= NU || (k0 >= lo && k0 + KU <= hi)) return;
+  const int row = threadIdx.x;
+  uint8_t* r = smem + (u & 1) * kMrUnitB + row * kMrRowB;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const int k = k0 + c / CB * 32;
+    if (k < lo || k >= hi) *reinterpret_cast<u32x4*>(r + ((c ^ mr_swz(row)) << 4)) = u32x4{0u, 0u, 0u, 0u};
+  }
+  lds_barrier();
+}
+
 // K step at position KP (0-7) of a scale period starting at unit U0: unit
 // U0 + KP / S, step j = KP % S.  The last step of a unit first waits for the
 // next unit (all of this wave's loads in flight belong to it), then a
 // barrier (the next unit visible; every wave done with this unit's buffer,
 // whose last reads were issued in the step before), then issues the loads of
 // the unit two ahead into this unit's buffer (LD: unless past the end).
-template <int FMT, int KP, bool LD>
+template <int FMT, int KP, bool LD, bool RANGE>
 __device__ __forceinline__ void mr_kstep(floatx16 (&acc)[4][4], const MrFrag<FMT>& F, MrFrag<FMT>& G,
-                                         const uint8_t* smem, uint32_t smem_lds, const MrSrc& s, int U0,
-                                         int NU, const MrLane& L) {
+                                         uint8_t* smem, uint32_t smem_lds, const MrSrc& s, int U0,
+                                         int NU, const MrLane& L, int lo, int hi) {
   constexpr int S = mr_ksteps<FMT>(), P = mr_period<FMT>();
   constexpr int I = KP / S, j = KP % S;
   constexpr bool last = j == S - 1;
@@ -231,6 +253,7 @@ __device__ __forceinline__ void mr_kstep(floatx16 (&acc)[4][4], const MrFrag<FMT
   if constexpr (last) {
     wait_vmcnt<0>();
     lds_barrier();
+    if constexpr (RANGE) mr_clip<FMT>(smem, U + 1, NU, lo, hi);
     asm volatile("s_nop 4" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -251,16 +274,16 @@ __device__ __forceinline__ void mr_kstep(floatx16 (&acc)[4][4], const MrFrag<FMT
   mr_steps<FMT, NLD, 0>(acc, F, G, nbuf, nsbuf, nsbyte, nj, s, lu, lp, lraw, lsc, L);
 }
 
-template <int FMT, bool LAST, int KP = 0>
+template <int FMT, bool LAST, bool RANGE, int KP = 0>
 __device__ __forceinline__ void mr_period_body(floatx16 (&acc)[4][4], MrFrag<FMT>& F0, MrFrag<FMT>& F1,
-                                               const uint8_t* smem, uint32_t smem_lds, const MrSrc& s,
-                                               int U0, int NU, const MrLane& L) {
+                                               uint8_t* smem, uint32_t smem_lds, const MrSrc& s,
+                                               int U0, int NU, const MrLane& L, int lo, int hi) {
   constexpr int S = mr_ksteps<FMT>(), P = mr_period<FMT>();
   if constexpr (KP < S * P) {
     constexpr bool ld = !LAST || (KP / S) + 2 < P;
-    if constexpr ((KP & 1) == 0) mr_kstep<FMT, KP, ld>(acc, F0, F1, smem, smem_lds, s, U0, NU, L);
-    else mr_kstep<FMT, KP, ld>(acc, F1, F0, smem, smem_lds, s, U0, NU, L);
-    mr_period_body<FMT, LAST, KP + 1>(acc, F0, F1, smem, smem_lds, s, U0, NU, L);
+    if constexpr ((KP & 1) == 0) mr_kstep<FMT, KP, ld, RANGE>(acc, F0, F1, smem, smem_lds, s, U0, NU, L, lo, hi);
+    else mr_kstep<FMT, KP, ld, RANGE>(acc, F1, F0, smem, smem_lds, s, U0, NU, L, lo, hi);
+    mr_period_body<FMT, LAST, RANGE, KP + 1>(acc, F0, F1, smem, smem_lds, s, U0, NU, L, lo, hi);
   }
 }
 
@@ -286,16 +309,44 @@ __device__ __forceinline__ void mr_read_all(MrFrag<FMT>& F, const uint8_t* buf, 
   }
 }
 
-template <int FMT>
-__global__ __launch_bounds__(kMrThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
-void k_gemm_mx_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
-                  const float* __restrict__ a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
-                  const float* __restrict__ b_amax, uint16_t* __restrict__ c, int64_t ldc, int tiles_m,
-                  int tiles_n, int vec_store) {
+// One output tile.  GROUP: kGroupNone, one product; kGroupRows and kGroupWgrad,
+// the expert-grouped products of bsq_gemm_grouped.hpp on the same schedule.
+template <int FMT, int GROUP>
+__device__ __forceinline__ void mr_tile(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
+                                        const uint8_t* a_scales, const float* __restrict__ a_amax,
+                                        const uint8_t* b_codes, const uint8_t* b_scales,
+                                        const float* __restrict__ b_amax, uint16_t* __restrict__ c, int64_t ldc,
+                                        int tiles_m, int tiles_n, int vec_store, GroupRef g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   constexpr int P = mr_period<FMT>();
+  constexpr bool RANGE = GROUP == kGroupWgrad;
+  constexpr int PB = fp8_elems(FMT) ? 1 : 2;             // K elements per code byte
   int tm, tn;
-  tile_of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  int lo = 0, hi = 0;                  // kGroupWgrad: the K elements that count, from the first unit
+  GroupTile gt{};
+  if constexpr (GROUP == kGroupRows) {
+    // A, C and M from the tile's group on; B of its expert
+    if (!group_tile_rows<256>(g, M, blockIdx.x, tiles_n, gt, tn)) return;
+    tm = 0;
+    a_codes += gt.row0 * (K / PB);
+    a_scales += gt.row0 * (K / 32);
+    c += gt.row0 * ldc;
+    M = gt.row1 - gt.row0;
+    if (gt.e < 0) return zero_tile(c, ldc, M, N, 0, (int64_t)tn * 256, vec_store);
+    b_codes += (int64_t)gt.e * N * (K / PB);
+    b_scales += (int64_t)gt.e * N * (K / 32);
+  } else if constexpr (GROUP == kGroupWgrad) {
+    const int e = wgrad_tile(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    c += (int64_t)e * M * ldc;
+    group_range<32, 512>(g, e, K, lo, hi, gt);
+    if (hi == 0) return zero_tile(c, ldc, M, N, (int64_t)tm * 256, (int64_t)tn * 256, vec_store);
+    a_codes += gt.row0 / PB;
+    a_scales += gt.row0 / 32;
+    b_codes += gt.row0 / PB;
+    b_scales += gt.row0 / 32;
+  } else {
+    tile_of_block(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  }
   const int t = threadIdx.x;
   MrLane L;
   L.lane = t & 63;
@@ -316,7 +367,8 @@ void k_gemm_mx_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const
   s.last_n = (uint32_t)(N - 1);
   s.code_ld = (uint32_t)(fp8_elems(FMT) ? K : K / 2);
   s.scale_ld = (uint32_t)(K / 32);
-  const int NU = (int)(s.code_ld / kMrRowB);             // a multiple of P
+  // units, a multiple of P
+  const int NU = RANGE ? (hi + 511) / 512 * P : (int)(s.code_ld / kMrRowB);
 
   // accumulators zeroed here, fenced: an accumulator written by a VALU
   // operation needs wait states before an MFMA reads it, and the compiler
@@ -337,13 +389,14 @@ void k_gemm_mx_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const
   mr_issue<FMT>(s, 1, smem_lds, L);
   wait_vmcnt<16>();                                      // unit 0 landed (unit 1: 16 code loads)
   lds_barrier();
+  if constexpr (RANGE) mr_clip<FMT>(smem, 0, NU, lo, hi);
   MrFrag<FMT> F0, F1;
   mr_read_all<FMT>(F0, smem, smem + kMrScOff, L);
   __builtin_amdgcn_sched_barrier(0);
 
   int U = 0;
-  for (; U + P < NU; U += P) mr_period_body<FMT, false>(acc, F0, F1, smem, smem_lds, s, U, NU, L);
-  mr_period_body<FMT, true>(acc, F0, F1, smem, smem_lds, s, U, NU, L);
+  for (; U + P < NU; U += P) mr_period_body<FMT, false, RANGE>(acc, F0, F1, smem, smem_lds, s, U, NU, L, lo, hi);
+  mr_period_body<FMT, true, RANGE>(acc, F0, F1, smem, smem_lds, s, U, NU, L, lo, hi);
 
   // every wave is done with the unit buffers (the epilogue reuses the LDS;
   // no load is in flight: the last two units issue none), and the last
@@ -396,6 +449,41 @@ void k_gemm_mx_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const
   }
 }
 
+template <int FMT>
+__global__ __launch_bounds__(kMrThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void k_gemm_mx_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
+                  const float* __restrict__ a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
+                  const float* __restrict__ b_amax, uint16_t* __restrict__ c, int64_t ldc, int tiles_m,
+                  int tiles_n, int vec_store) {
+  mr_tile<FMT, kGroupNone>(M, N, K, a_codes, a_scales, a_amax, b_codes, b_scales, b_amax, c, ldc, tiles_m, tiles_n,
+                           vec_store, GroupRef{});
+}
+
+template <int FMT, int GROUP>
+__global__ __launch_bounds__(kMrThreads) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void k_gemm_mx_grouped_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes, const uint8_t* a_scales,
+                          const uint8_t* b_codes, const uint8_t* b_scales, uint16_t* __restrict__ c, int64_t ldc,
+                          int tiles_m, int tiles_n, int vec_store, GroupRef g) {
+  mr_tile<FMT, GROUP>(M, N, K, a_codes, a_scales, nullptr, b_codes, b_scales, nullptr, c, ldc, tiles_m, tiles_n,
+                      vec_store, g);
+}
+
+template <int FMT, int GROUP>
+hipError_t run_mx_grouped(const GroupedArgs& a, hipStream_t s) {
+  constexpr bool wgrad = GROUP == kGroupWgrad;
+  const int64_t tn = (a.N + 255) / 256;
+  const int64_t tm = wgrad ? (a.M + 255) / 256 : max_row_tiles(a.M, a.experts, 256);
+  const int64_t blocks = tm * tn * (wgrad ? a.experts : 1);
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (set_lds_limit(reinterpret_cast<const void*>(&k_gemm_mx_grouped_rx<FMT, GROUP>), kMrLds) != hipSuccess)
+    return hipErrorInvalidConfiguration;
+  const bool vec_store = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+  hipLaunchKernelGGL((k_gemm_mx_grouped_rx<FMT, GROUP>), dim3((unsigned)blocks), dim3(kMrThreads), kMrLds, s, a.M,
+                     a.N, a.K, a.ac, a.as, a.bc, a.bs, static_cast<uint16_t*>(a.c), a.ldc, (int)tm, (int)tn,
+                     vec_store ? 1 : 0, GroupRef{a.offsets, a.experts, 1});
+  return hipGetLastError();
+}
+
 }  // namespace
 
 // whole scale periods (16 scale bytes per row: K % 512 == 0), at least one
@@ -434,5 +522,19 @@ BSQ_MX_RX(kMXFP4)
 BSQ_MX_RX(kMXFP8)
 BSQ_MX_RX(kFP8)
 #undef BSQ_MX_RX
+
+bool gemm_mx_rx_grouped_fits(const GroupedArgs& a, bool wgrad) {
+  // wgrad loads whole scale periods, from a period boundary at or below a group's first row
+  const int64_t rows = wgrad ? a.M : 256;
+  if (a.N >= ((int64_t)1 << 31) - 256) return false;
+  return a.fmt == kMXFP8 ? gemm_mx_rx_fits<kMXFP8>(rows, a.N, a.K, a.ac, a.as, a.bc, a.bs)
+                         : gemm_mx_rx_fits<kMXFP4>(rows, a.N, a.K, a.ac, a.as, a.bc, a.bs);
+}
+
+hipError_t launch_gemm_mx_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s) {
+  if (a.fmt == kMXFP8)
+    return wgrad ? run_mx_grouped<kMXFP8, kGroupWgrad>(a, s) : run_mx_grouped<kMXFP8, kGroupRows>(a, s);
+  return wgrad ? run_mx_grouped<kMXFP4, kGroupWgrad>(a, s) : run_mx_grouped<kMXFP4, kGroupRows>(a, s);
+}
 
 }  // namespace bsq

@@ -454,17 +454,15 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
     a_scales += gt.row0 * (K / 16);
     c += gt.row0 * ldc;
     M = gt.row1 - gt.row0;
-    if (gt.e < 0) {
-      K = 0;                           // rows of no group: zeros
-    } else {
-      b_codes += (int64_t)gt.e * N * (K / 2);
-      b_scales += (int64_t)gt.e * N * (K / 16);
-      b_amax += g.ba_n > 1 ? gt.e : 0;
-    }
+    if (gt.e < 0) return zero_tile(c, ldc, M, N, 0, (int64_t)tn * 256, vec_store);
+    b_codes += (int64_t)gt.e * N * (K / 2);
+    b_scales += (int64_t)gt.e * N * (K / 16);
+    b_amax += g.ba_n > 1 ? gt.e : 0;
   } else if constexpr (GROUP == kGroupWgrad) {
     const int e = wgrad_tile(pid, tiles_m, tiles_n, tm, tn);
     c += (int64_t)e * M * ldc;
     group_range<16, 256>(g, e, K, lo, hi, gt);
+    if (hi == 0) return zero_tile(c, ldc, M, N, (int64_t)tm * 256, (int64_t)tn * 256, vec_store);
     a_codes += gt.row0 / 2;
     a_scales += gt.row0 / 16;
     b_codes += gt.row0 / 2;
@@ -511,7 +509,6 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
 
   // prologue: pairs 0 and 1 (units 0-3) in flight; unit 0's codes and
   // scales in registers; the A tiles and B tiles 0-6 of step 0 expanded
-  if (GROUP == kGroupNone || NU > 0) {
   RxRegs r;
   rx_stage(s, 0, smem_lds, w, lane);
   if (NU > 2) rx_stage(s, 1, smem_lds + kRxUnitB, w, lane);
@@ -542,8 +539,6 @@ void k_gemm_nvfp4_rx(int64_t M, int64_t N, int64_t K, const uint8_t* a_codes,
   for (; U < NU; U += 2) {
     rx_unit<0, false, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U, NU, w, lane, ln, lo, hi);
     rx_unit<1, false, GROUP == kGroupWgrad>(acc, r, smem, smem_lds, s, U + 1, NU, w, lane, ln, lo, hi);
-  }
-
   }
 
   // every wave is done with the unit buffers (the epilogue reuses the LDS),
@@ -728,7 +723,7 @@ bool gemm_nvfp4_rx_grouped_fits(const GroupedArgs& a, bool wgrad) {
 
 hipError_t launch_gemm_nvfp4_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s) {
   const int64_t tn = (a.N + 255) / 256;
-  const int64_t tm = wgrad ? (a.M + 255) / 256 : a.M / 256 + a.experts + 1;
+  const int64_t tm = wgrad ? (a.M + 255) / 256 : max_row_tiles(a.M, a.experts, 256);
   if (tm * tn * (wgrad ? a.experts : 1) > 0x7FFFFFFF) return hipErrorInvalidValue;
   const void* fn = wgrad ? reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false, kGroupWgrad>)
                          : reinterpret_cast<const void*>(&k_gemm_nvfp4_rx<false, kGroupRows>);

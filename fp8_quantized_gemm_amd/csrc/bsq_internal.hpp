@@ -239,5 +239,8 @@ hipError_t launch_gemm_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
 // offsets), and its launch.
 bool gemm_nvfp4_rx_grouped_fits(const GroupedArgs& a, bool wgrad);
 hipError_t launch_gemm_nvfp4_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s);
+// ... and on the four-wave MX kernel (K resp. rows % 512 == 0, aligned as above).
+bool gemm_mx_rx_grouped_fits(const GroupedArgs& a, bool wgrad);
+hipError_t launch_gemm_mx_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s);
 
 }  // namespace bsq

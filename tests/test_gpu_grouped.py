@@ -70,6 +70,10 @@ ROWS = [  # sizes, rows past the last group, N, K
     ([257, 0, 511, 256, 3], 100, 520, 1024),
     ([180] * 67 + [0, 1, 700], 300, 40, 256),
     ([1, 1023, 0, 2], 0, 33, 768),
+    ([40, 70, 33, 0, 90], 10, 150, 320),
+    ([64, 65, 63, 128, 1], 0, 129, 640),
+    ([130, 127, 90], 70, 260, 384),
+    ([40, 41, 39], 0, 128, 192),
 ]
 
 
@@ -146,6 +150,8 @@ WGRAD = [  # sizes (in scale blocks), blocks past the last group, M, N
     ([100, 1, 27], 128, 520, 264),
     ([5, 6, 1, 100, 0, 2, 142], 0, 300, 40),
     ([1, 510, 0, 1], 0, 257, 64),
+    ([7, 1, 3, 9, 0, 2, 2], 0, 140, 129),
+    ([3, 4, 1, 4], 4, 70, 260),
 ]
 
 
