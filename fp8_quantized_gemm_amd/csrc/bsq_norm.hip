@@ -6,7 +6,9 @@
 //
 // Both directions are one pass over the rows (HBM-bound): a group of TPR
 // threads holds one row in registers, CH pieces of 8 columns per thread, so x, o
-// (forward) and d_r, d_h, r, o (backward) are read once.
+// (forward) and d_r, d_h, r, o (backward) are read once.  Workgroups walk the
+// rows, so the weights of a thread's columns stay in registers, and load the next
+// row while the current one is reduced.
 #include "bsq_internal.hpp"
 #include "bsq_wave.hpp"
 
@@ -14,75 +16,104 @@ namespace bsq {
 
 namespace {
 
-// Column of element j of piece c of thread t: pieces of 8 consecutive columns
-// (VEC 8: 16-byte accesses, cols % 8 == 0 and aligned), or single columns
-// strided over the group (VEC 1: any cols).
-template <int VEC, int TPR>
-__device__ __forceinline__ int col_of(int c, int j, int t) {
-  return VEC == 8 ? (c * TPR + t) * 8 + j : (c * 8 + j) * TPR + t;
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes at an address of 2, 4 or 16-byte alignment.
+template <int A>
+struct Piece;
+template <>
+struct Piece<2> { typedef u32x4 type __attribute__((aligned(2))); };
+template <>
+struct Piece<4> { typedef u32x4 type __attribute__((aligned(4))); };
+template <>
+struct Piece<16> { typedef u32x4 type; };
+
+// 8 columns of a row as stored: 16 bytes of BF16, 32 of FP32.
+template <typename T>
+struct Raw {
+  u32x4 v[sizeof(T) / 2];
+};
+
+// Piece at column col of a row of cols columns, zeros past its end.  AL: rows
+// are 16-byte aligned and cols % 8 == 0; else any element alignment (one
+// unaligned 16-byte access per piece, single elements in the row's last piece:
+// 3.5 times faster on odd widths than lanes striding over single elements).
+template <bool AL, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* row, int col, int cols) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
+  if (AL ? col < cols : col + 8 <= cols) {
+    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const U*>(row + col)[i];
+  } else if (!AL && col < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) {
+        if constexpr (sizeof(T) == 2) r.v[0][j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
+        else r.v[j >> 2][j & 3] = f2u(row[col + j]);
+      }
+  }
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float raw_at(const Raw<T>& r, int j) {
+  if constexpr (sizeof(T) == 2) return (j & 1) ? bf16_hi(r.v[0][j >> 1]) : bf16_lo(r.v[0][j >> 1]);
+  else return u2f(r.v[j >> 2][j & 3]);
+}
+// Makes the compiler forget what it unpacked from r: a piece is unpacked again
+// where it is used next, instead of being held as 8 FP32 registers meanwhile.
+template <typename T>
+__device__ __forceinline__ void forget(Raw<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) asm volatile("" : "+v"(r.v[i]));
+}
+template <bool AL, typename T>
+__device__ __forceinline__ void store8(T* row, int col, int cols, const float (&y)[8]) {
+  Raw<T> r;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[0][j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j >> 2][j & 3] = f2u(y[j]);
+  }
+  if (AL ? col < cols : col + 8 <= cols) {
+    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<U*>(row + col)[i] = r.v[i];
+  } else if (!AL && col < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) {
+        if constexpr (sizeof(T) == 2) row[col + j] = (uint16_t)(r.v[0][j >> 1] >> (16 * (j & 1)));
+        else row[col + j] = y[j];
+      }
+  }
+}
+// Weights of a piece, `fill` where there are none.
+template <bool AL>
+__device__ __forceinline__ void load_w(const float* w, int col, int cols, float fill, float (&y)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = fill;
+    return;
+  }
+  const Raw<float> r = load_raw<AL>(w, col, cols);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = raw_at(r, j);
 }
 
-template <int VEC, int TPR>
-__device__ __forceinline__ void load8(const uint16_t* p, int c, int t, int cols, float* y) {
-  if constexpr (VEC == 8) {
-    const int col = col_of<8, TPR>(c, 0, t);
-    const uint4 v = col < cols ? *reinterpret_cast<const uint4*>(p + col) : make_uint4(0, 0, 0, 0);
-    bf16x8_to_f32(v, y);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<1, TPR>(c, j, t);
-      y[j] = col < cols ? u2f((uint32_t)p[col] << 16) : 0.0f;
-    }
-  }
-}
-template <int VEC, int TPR>
-__device__ __forceinline__ void load8(const float* p, int c, int t, int cols, float* y) {
-  if constexpr (VEC == 8) {
-    const int col = col_of<8, TPR>(c, 0, t);
-    float4 a = make_float4(0, 0, 0, 0), b = a;
-    if (col < cols) {
-      a = *reinterpret_cast<const float4*>(p + col);
-      b = *reinterpret_cast<const float4*>(p + col + 4);
-    }
-    y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w;
-    y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<1, TPR>(c, j, t);
-      y[j] = col < cols ? p[col] : 0.0f;
-    }
-  }
-}
-template <int VEC, int TPR>
-__device__ __forceinline__ void store8(uint16_t* p, int c, int t, int cols, const float* y) {
-  if constexpr (VEC == 8) {
-    const int col = col_of<8, TPR>(c, 0, t);
-    if (col < cols) *reinterpret_cast<uint4*>(p + col) = f32_to_bf16x8(y);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<1, TPR>(c, j, t);
-      if (col < cols) p[col] = bf16_rne(y[j]);
-    }
-  }
-}
-template <int VEC, int TPR>
-__device__ __forceinline__ void store8(float* p, int c, int t, int cols, const float* y) {
-  if constexpr (VEC == 8) {
-    const int col = col_of<8, TPR>(c, 0, t);
-    if (col < cols) {
-      *reinterpret_cast<float4*>(p + col) = make_float4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<float4*>(p + col + 4) = make_float4(y[4], y[5], y[6], y[7]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = col_of<1, TPR>(c, j, t);
-      if (col < cols) p[col] = y[j];
-    }
-  }
+// Sum over the 16 lanes of a DPP row or, with L 32, two of them, in every lane.
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += u2f(dpp_or0<0xB1, 0xF>(f2u(v)));
+  v += u2f(dpp_or0<0x4E, 0xF>(f2u(v)));
+  v += u2f(dpp_or0<0x141, 0xF>(f2u(v)));
+  v += u2f(dpp_or0<0x140, 0xF>(f2u(v)));
+  if constexpr (L == 32) v += __shfl_xor(v, 16, 64);
+  return v;
 }
 
 // Sums of NV values over the TPR threads of a row group, in every thread of it.
@@ -91,7 +122,10 @@ __device__ __forceinline__ void store8(float* p, int c, int t, int cols, const f
 template <int TPR, int NV>
 __device__ __forceinline__ void group_sum(float (&v)[NV], float* red) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
+  for (int i = 0; i < NV; ++i) {
+    if constexpr (TPR < 64) v[i] = lanes_sum<TPR>(v[i]);
+    else v[i] = wave_sum(v[i]);
+  }
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     const int wave = threadIdx.x >> 6, g0 = wave / W * W;
@@ -112,103 +146,111 @@ __device__ __forceinline__ void group_sum(float (&v)[NV], float* red) {
 
 // ---------------------------------------------------------------- forward
 
-// 256 threads at least per workgroup: BT / TPR rows at a time, grid-stride.
-template <typename T, int VEC, int TPR, int CH>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm(NormFwd a) {
+// At least 256 threads per workgroup: BT / TPR rows at a time, grid-stride.
+template <typename T, bool AL, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_block_norm(NormFwd a) {
   constexpr int BT = TPR < 256 ? 256 : TPR, RPB = BT / TPR;
   __shared__ float red[2][16];
   __shared__ uint32_t mred[16];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
+  const bool has_o = a.o != nullptr, both = a.w_pre && a.w_post;
+  const T* x = static_cast<const T*>(a.x);
+  const uint16_t* o = static_cast<const uint16_t*>(a.o);
+  const uint16_t* gf = a.gate_kind == kGateFull ? static_cast<const uint16_t*>(a.gate) : nullptr;
+  const auto col = [&](int c) { return (c * TPR + t) * 8; };
+  // the columns' weights: w_post times a channel gate, and w_pre
+  float wq[CH][8], wp[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_w<AL>(a.w_post, col(c), cols, 1.0f, wq[c]);
+    load_w<AL>(a.w_pre, col(c), cols, 0.0f, wp[c]);
+    if (a.gate_kind == kGateChannel) {
+      float g[8];
+      load_w<AL>(static_cast<const float*>(a.gate), col(c), cols, 1.0f, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wq[c][j] *= g[j];
+    }
+  }
+  Raw<T> xr[CH];
+  Raw<uint16_t> orow[CH], gr[CH];
+  const auto load = [&](int64_t b) {
+    const int64_t row = b * RPB + sub, base = (row < a.rows ? row : a.rows - 1) * a.cols;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      xr[c] = load_raw<AL>(x + base, col(c), cols);
+      if (has_o) orow[c] = load_raw<AL>(o + base, col(c), cols);
+      if (gf) gr[c] = load_raw<AL>(gf + base, col(c), cols);
+    }
+  };
   uint32_t hmax = 0;
   const int64_t trips = (a.rows + RPB - 1) / RPB;
-  for (int64_t b = blockIdx.x; b < trips; b += gridDim.x) {
+  int64_t b = blockIdx.x;
+  if (b < trips) load(b);
+  while (b < trips) {
     const int64_t row = b * RPB + sub;
     const bool live = row < a.rows;
     const int64_t base = (live ? row : a.rows - 1) * a.cols;
     float r[CH][8];
-    const T* x = static_cast<const T*>(a.x) + base;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) load8<VEC, TPR>(x, c, t, cols, r[c]);
-    if (a.o) {
-      float o[CH][8];
-      const uint16_t* op = static_cast<const uint16_t*>(a.o) + base;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) load8<VEC, TPR>(op, c, t, cols, o[c]);
-      if (a.w_post) {
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[0] += o[c][j] * o[c][j];
-        group_sum<TPR, 1>(s, red[0]);
-        const float rs = 1.0f / __builtin_sqrtf(s[0] * inv + a.eps);
-        if (live && t == 0 && a.rstd_post) a.rstd_post[row] = rs;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float w[8];
-          load8<VEC, TPR>(a.w_post, c, t, cols, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[c][j] = o[c][j] * rs * w[j];
-        }
-      }
-      if (a.gate_kind == kGateRow) {
-        const float g = static_cast<const float*>(a.gate)[live ? row : a.rows - 1];
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[c][j] *= g;
-      } else if (a.gate_kind != kGateNone) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float g[8];
-          if (a.gate_kind == kGateChannel)
-            load8<VEC, TPR>(static_cast<const float*>(a.gate), c, t, cols, g);
-          else
-            load8<VEC, TPR>(static_cast<const uint16_t*>(a.gate) + base, c, t, cols, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[c][j] *= g[j];
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[c][j] = a.alpha * r[c][j] + o[c][j];
-      if (live) {
-        T* rp = static_cast<T*>(a.r) + base;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) store8<VEC, TPR>(rp, c, t, cols, r[c]);
-      }
-    }
-    if (a.w_pre) {
+    float rq = 1.0f;
+    if (a.w_post) {
       float s[1] = {0.0f};
 #pragma unroll
       for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += r[c][j] * r[c][j];
+        for (int j = 0; j < 8; ++j) {
+          const float v = raw_at(orow[c], j);
+          s[0] = __builtin_fmaf(v, v, s[0]);
+        }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) forget(orow[c]);
+      group_sum<TPR, 1>(s, red[0]);
+      rq = 1.0f / __builtin_sqrtf(s[0] * inv + a.eps);
+      if (live && t == 0 && a.rstd_post) a.rstd_post[row] = rq;
+    }
+    if (a.gate_kind == kGateRow) rq *= static_cast<const float*>(a.gate)[live ? row : a.rows - 1];
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float v = raw_at(xr[c], j);
+        if (has_o) {
+          float n = raw_at(orow[c], j) * rq * wq[c][j];
+          if (gf) n *= raw_at(gr[c], j);
+          v = __builtin_fmaf(a.alpha, v, n);
+        }
+        r[c][j] = v;
+        s[0] = __builtin_fmaf(v, v, s[0]);
+      }
+    const int64_t next = b + gridDim.x;
+    if (next < trips) load(next);                     // in flight during the second reduction and the stores
+    if (has_o && live) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) store8<AL>(static_cast<T*>(a.r) + base, col(c), cols, r[c]);
+    }
+    if (a.w_pre) {
       group_sum<TPR, 1>(s, red[1]);
       const float rs = 1.0f / __builtin_sqrtf(s[0] * inv + a.eps);
       if (live && t == 0 && a.rstd_pre) a.rstd_pre[row] = rs;
-      uint16_t* hp = static_cast<uint16_t*>(a.h) + base;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float w[8];
-        load8<VEC, TPR>(a.w_pre, c, t, cols, w);
+        float y[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = r[c][j] * rs * w[j];
-        if (live) {
-          store8<VEC, TPR>(hp, c, t, cols, w);
+        for (int j = 0; j < 8; ++j) {
+          y[j] = r[c][j] * rs * wp[c][j];
           // amax of the stored values: rounding to BF16 is monotone, so the
           // rounding of the maximum is the maximum of the rounded
-#pragma unroll
-          for (int j = 0; j < 8; ++j) hmax = max(hmax, f2u(w[j]) & 0x7FFFFFFFu);
+          if (live) hmax = max(hmax, f2u(y[j]) & 0x7FFFFFFFu);
         }
+        if (live) store8<AL>(static_cast<uint16_t*>(a.h) + base, col(c), cols, y);
       }
     }
-    // red[0] and red[1] are each written once per trip, with the other's
-    // barrier in between only when both norms run
-    if (TPR > 64 && !(a.w_pre && a.o && a.w_post)) __syncthreads();
+    // red[0] and red[1] are each written once per trip, with the other's barrier
+    // in between only when both norms run
+    if (TPR > 64 && !both) __syncthreads();
+    b = next;
   }
   if (a.amax) {
     hmax = wave_max_dpp(hmax);
@@ -217,7 +259,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm(NormFwd a)
     if (threadIdx.x == 0) {
       for (int i = 1; i < BT / 64; ++i) hmax = max(hmax, mred[i]);
       const float m = u2f((uint32_t)bf16_rne(u2f(hmax)) << 16);
-      if (gridDim.x == 1) *a.amax = m;             // no other writer: no clearing launch before
+      if (gridDim.x == 1) *a.amax = m;                // no other writer: no clearing launch before
       else atomicMax(reinterpret_cast<unsigned int*>(a.amax), f2u(m));
     }
   }
@@ -225,26 +267,64 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_block_norm(NormFwd a)
 
 // ---------------------------------------------------------------- backward
 
-// One pass over the rows, each workgroup BT / TPR rows at a time; the column
-// sums (d_w_pre, d_w_post, a channel gate's) stay in registers over all rows of
-// the workgroup and go to the workspace once, [workgroup][3][cols]; k_col_sum
-// adds them in workgroup order (no atomics: repeated calls give the same bits).
+// One pass over the rows, each workgroup BT / TPR rows at a time.  With G, rn, on
+// as in include/bsq.h, two column sums carry all column gradients:
+//   d_w_pre = sum d_h rn;  T = sum G on (times a row or full gate):
+//   d_w_post = g T and d_gate = w_post T for a channel gate.
+// They stay in registers over all rows of the workgroup and go to the workspace
+// once, [workgroup][2][cols]; k_col_sum adds them in workgroup order (no atomics:
+// repeated calls give the same bits).
 // The two row means need one reduction only: with q = g w_post on,
 //   G = d_r + rs (a - rn m1),  m1 = mean(a rn)
 //   mean(G q) = mean(d_r q) + rs (mean(a q) - m1 mean(rn q)).
-template <typename T, int VEC, int TPR, int CH>
-__global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void k_block_norm_bwd(NormBwd a) {
+template <typename T, bool AL, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(NormBwd a) {
   constexpr int BT = TPR < 512 ? 512 : TPR, RPB = BT / TPR;
   __shared__ float red[2][4 * 16];
-  extern __shared__ float fold[];                   // [BT][8] for the fold over the row groups
+  // CH 1: [8][BT], the fold over the row groups.  CH 2: the column sums themselves
+  // ([2][CH][2][BT] of float4, a thread's own), whose registers would spill.
+  extern __shared__ __attribute__((aligned(16))) float fold[];
+  float4* sums = reinterpret_cast<float4*>(fold);
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
-  float sp[CH][8], sq[CH][8], sg[CH][8];
+  const bool has_o = a.o != nullptr, pre = a.w_pre != nullptr, post = a.w_post != nullptr;
+  const T *d_r = static_cast<const T*>(a.d_r), *r = static_cast<const T*>(a.r);
+  const uint16_t *d_h = static_cast<const uint16_t*>(a.d_h), *o = static_cast<const uint16_t*>(a.o);
+  const uint16_t* gf = a.gate_kind == kGateFull ? static_cast<const uint16_t*>(a.gate) : nullptr;
+  const auto col = [&](int c) { return (c * TPR + t) * 8; };
+  // the columns' weights: in registers with one piece per thread, read again
+  // (from the L2) where they are used with two, whose registers would spill
+  float wq1[8], wp1[8], sp[8], st[8];
+  const auto load_sums = [&](int k, int c, float (&v)[8]) {
+    const float4 x = sums[((k * CH + c) * 2) * BT + threadIdx.x], y = sums[((k * CH + c) * 2 + 1) * BT + threadIdx.x];
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  };
+  const auto store_sums = [&](int k, int c, const float (&v)[8]) {
+    sums[((k * CH + c) * 2) * BT + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+    sums[((k * CH + c) * 2 + 1) * BT + threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
+  };
+  const auto weights = [&](int c, float (&wq)[8], float (&wp)[8]) {
+    load_w<AL>(a.w_post, col(c), cols, 1.0f, wq);
+    load_w<AL>(a.w_pre, col(c), cols, 0.0f, wp);
+    if (a.gate_kind == kGateChannel) {
+      float g[8];
+      load_w<AL>(static_cast<const float*>(a.gate), col(c), cols, 1.0f, g);
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+      for (int j = 0; j < 8; ++j) wq[j] *= g[j];
+    }
+  };
+  if constexpr (CH == 1) weights(0, wq1, wp1);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sp[c][j] = sq[c][j] = sg[c][j] = 0.0f;
+  for (int j = 0; j < 8; ++j) sp[j] = st[j] = 0.0f;
+  if constexpr (CH > 1) {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      store_sums(0, c, sp);
+      store_sums(1, c, st);
+    }
+  }
   int par = 0;
   const int64_t trips = (a.rows + RPB - 1) / RPB;
   for (int64_t b = blockIdx.x; b < trips; b += gridDim.x, par ^= 1) {
@@ -252,96 +332,92 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void k_block_norm_bwd(NormBw
     const bool live = row < a.rows;
     const int64_t rw = live ? row : a.rows - 1;
     const int64_t base = rw * a.cols;
-    const float rs = a.w_pre ? a.rstd_pre[rw] : 0.0f;
-    const float rp = a.w_post ? a.rstd_post[rw] : 1.0f;
-    const float grow = a.gate_kind == kGateRow ? static_cast<const float*>(a.gate)[rw] : 1.0f;
-    float G[CH][8], av[CH][8], rn[CH][8], on[CH][8];
+    Raw<T> dr[CH], rr[CH];
+    Raw<uint16_t> dh[CH], orow[CH], gr[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      if (a.d_r) {
-        load8<VEC, TPR>(static_cast<const T*>(a.d_r) + base, c, t, cols, G[c]);
+      if (d_r) {
+        dr[c] = load_raw<AL>(d_r + base, col(c), cols);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) G[c][j] = 0.0f;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) dr[c].v[i] = u32x4{0u, 0u, 0u, 0u};
       }
-      if (a.w_pre) {
-        float w[8];
-        load8<VEC, TPR>(static_cast<const uint16_t*>(a.d_h) + base, c, t, cols, av[c]);
-        load8<VEC, TPR>(static_cast<const T*>(a.r) + base, c, t, cols, rn[c]);
-        load8<VEC, TPR>(a.w_pre, c, t, cols, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          rn[c][j] *= rs;
-          if (live) sp[c][j] += av[c][j] * rn[c][j];
-          av[c][j] *= w[j];
-        }
+      if (pre) {
+        dh[c] = load_raw<AL>(d_h + base, col(c), cols);
+        rr[c] = load_raw<AL>(r + base, col(c), cols);
       } else {
+        dh[c].v[0] = u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) av[c][j] = rn[c][j] = 0.0f;
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) rr[c].v[i] = u32x4{0u, 0u, 0u, 0u};
       }
-      if (a.o) {
-        load8<VEC, TPR>(static_cast<const uint16_t*>(a.o) + base, c, t, cols, on[c]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) on[c][j] *= rp;
-      }
+      if (has_o) orow[c] = load_raw<AL>(o + base, col(c), cols);
+      else orow[c].v[0] = u32x4{0u, 0u, 0u, 0u};
+      if (gf) gr[c] = load_raw<AL>(gf + base, col(c), cols);
     }
+    const float rs = pre ? a.rstd_pre[rw] : 0.0f;
+    const float rp = post ? a.rstd_post[rw] : 1.0f;
+    const float grow = a.gate_kind == kGateRow ? static_cast<const float*>(a.gate)[rw] : 1.0f;
+    const float one = live ? 1.0f : 0.0f;           // rows past the last add nothing to the column sums
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float wq[8], g[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wq[j] = 1.0f, g[j] = 1.0f;
-      if (a.o) {
-        if (a.w_post) load8<VEC, TPR>(a.w_post, c, t, cols, wq);
-        if (a.gate_kind == kGateChannel) load8<VEC, TPR>(static_cast<const float*>(a.gate), c, t, cols, g);
-        else if (a.gate_kind == kGateFull) load8<VEC, TPR>(static_cast<const uint16_t*>(a.gate) + base, c, t, cols, g);
+      if constexpr (CH > 1) {
+        __builtin_amdgcn_sched_barrier(0);              // one piece at a time: fewer registers
+        weights(c, wq1, wp1);
+        load_sums(0, c, sp);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        s[0] += av[c][j] * rn[c][j];
-        if (a.o) {
-          const float q = g[j] * wq[j] * on[c][j];
-          s[1] += G[c][j] * q;
-          s[2] += av[c][j] * q;
-          s[3] += rn[c][j] * q;
-        }
+        const float h = raw_at(dh[c], j), rn = raw_at(rr[c], j) * rs, av = h * wp1[j];
+        float q = raw_at(orow[c], j) * rp * wq1[j];
+        if (gf) q *= raw_at(gr[c], j);
+        sp[j] = __builtin_fmaf(h * one, rn, sp[j]);
+        s[0] = __builtin_fmaf(av, rn, s[0]);
+        s[1] = __builtin_fmaf(raw_at(dr[c], j), q, s[1]);
+        s[2] = __builtin_fmaf(av, q, s[2]);
+        s[3] = __builtin_fmaf(rn, q, s[3]);
       }
+      if constexpr (CH > 1) store_sums(0, c, sp);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      forget(dr[c]);
+      forget(rr[c]);
+      forget(dh[c]);
+      forget(orow[c]);
+      if (gf) forget(gr[c]);
     }
     group_sum<TPR, 4>(s, red[par]);
     const float m1 = s[0] * inv;
-    const float tot = s[1] + rs * (s[2] - m1 * s[3]);   // sum of G g w_post on (row gate left out)
+    const float tot = s[1] + rs * (s[2] - m1 * s[3]);   // sum of G q, a row gate left out
     const float m2 = tot * grow * inv;
     if (a.gate_kind == kGateRow && live && t == 0) static_cast<float*>(a.d_gate)[row] = tot;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      float y[8];
+      if constexpr (CH > 1) {
+        __builtin_amdgcn_sched_barrier(0);
+        weights(c, wq1, wp1);
+        load_sums(1, c, st);
+      }
+      float y[8], z[8], dg[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        G[c][j] += rs * (av[c][j] - rn[c][j] * m1);
-        y[j] = a.o ? a.alpha * G[c][j] : G[c][j];
+        const float av = raw_at(dh[c], j) * wp1[j], rn = raw_at(rr[c], j) * rs;
+        const float G = __builtin_fmaf(rs, __builtin_fmaf(-m1, rn, av), raw_at(dr[c], j));
+        y[j] = has_o ? a.alpha * G : G;
+        const float on = raw_at(orow[c], j) * rp;
+        const float g = gf ? raw_at(gr[c], j) : grow;
+        const float Gg = G * g;
+        st[j] = __builtin_fmaf(Gg * one, on, st[j]);
+        dg[j] = G * wq1[j] * on;                        // full gate
+        z[j] = Gg * wq1[j];
+        if (post) z[j] = rp * __builtin_fmaf(-m2, on, z[j]);
       }
-      if (live) store8<VEC, TPR>(static_cast<T*>(a.d_x) + base, c, t, cols, y);
-      if (a.o) {
-        float wq[8], g[8], z[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wq[j] = 1.0f, g[j] = grow;
-        if (a.w_post) load8<VEC, TPR>(a.w_post, c, t, cols, wq);
-        if (a.gate_kind == kGateChannel) load8<VEC, TPR>(static_cast<const float*>(a.gate), c, t, cols, g);
-        else if (a.gate_kind == kGateFull) load8<VEC, TPR>(static_cast<const uint16_t*>(a.gate) + base, c, t, cols, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float Gg = G[c][j] * g[j];
-          y[j] = G[c][j] * wq[j] * on[c][j];             // d gate
-          if (live) {
-            sg[c][j] += y[j];
-            sq[c][j] += Gg * on[c][j];
-          }
-          z[j] = a.w_post ? rp * (Gg * wq[j] - on[c][j] * m2) : Gg;
-        }
-        if (live) {
-          store8<VEC, TPR>(static_cast<uint16_t*>(a.d_o) + base, c, t, cols, z);
-          if (a.gate_kind == kGateFull) store8<VEC, TPR>(static_cast<uint16_t*>(a.d_gate) + base, c, t, cols, y);
-        }
+      if constexpr (CH > 1) store_sums(1, c, st);
+      if (live) {
+        store8<AL>(static_cast<T*>(a.d_x) + base, col(c), cols, y);
+        if (has_o) store8<AL>(static_cast<uint16_t*>(a.d_o) + base, col(c), cols, z);
+        if (gf) store8<AL>(static_cast<uint16_t*>(a.d_gate) + base, col(c), cols, dg);
       }
     }
   }
@@ -349,10 +425,10 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void k_block_norm_bwd(NormBw
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      const bool want = k == 0 ? a.w_pre != nullptr : k == 1 ? a.w_post != nullptr : a.gate_kind == kGateChannel;
-      if (!want) continue;
-      float* v = k == 0 ? sp[c] : k == 1 ? sq[c] : sg[c];
+    for (int k = 0; k < 2; ++k) {
+      if (k == 0 ? !pre : !has_o) continue;
+      float (&v)[8] = k == 0 ? sp : st;
+      if constexpr (CH > 1) load_sums(k, c, v);
       if constexpr (RPB > 1) {
         __syncthreads();
 #pragma unroll
@@ -361,25 +437,25 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR) void k_block_norm_bwd(NormBw
         if (sub == 0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float s = 0.0f;
-            for (int q = 0; q < RPB; ++q) s += fold[j * BT + q * TPR + t];
-            v[j] = s;
+            float f = 0.0f;
+            for (int q = 0; q < RPB; ++q) f += fold[j * BT + q * TPR + t];
+            v[j] = f;
           }
         }
       }
-      if (sub == 0)
-        store8<VEC, TPR>(a.part + ((int64_t)blockIdx.x * 3 + k) * a.cols, c, t, cols, v);
+      if (sub == 0) store8<AL>(a.part + ((int64_t)blockIdx.x * 2 + k) * a.cols, col(c), cols, v);
     }
   }
 }
 
-// out[k][c] = sum over the nblk partials, in order: 16 slices of the partials by
-// 16 row groups of a workgroup, folded in slice order.  blockIdx.y = k.
+// Sums of the nblk partials in order: 16 slices of them by the 16 waves of a
+// workgroup, folded in slice order.  blockIdx.y 0: d_w_pre; 1: T, from which
+// d_w_post (times a channel gate) and a channel gate's gradient (times w_post).
 __global__ __launch_bounds__(1024) void k_col_sum(const float* __restrict__ part, int nblk, int64_t cols,
-                                                  float* o0, float* o1, float* o2) {
+                                                  float* d_w_pre, float* d_w_post, float* d_gate,
+                                                  const float* w_post, const float* gate) {
   __shared__ float s[16][64];
-  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
-  if (!out) return;
+  if (blockIdx.y == 0 ? !d_w_pre : !d_w_post && !d_gate) return;
   const int lane = threadIdx.x & 63, sl = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   const int per = (nblk + 15) / 16, b0 = sl * per, b1 = min(nblk, b0 + per);
@@ -387,13 +463,17 @@ __global__ __launch_bounds__(1024) void k_col_sum(const float* __restrict__ part
   if (c < cols) {
     const float* p = part + (int64_t)blockIdx.y * cols + c;
 #pragma unroll 8
-    for (int b = b0; b < b1; ++b) v += p[(int64_t)b * 3 * cols];
+    for (int b = b0; b < b1; ++b) v += p[(int64_t)b * 2 * cols];
   }
   s[sl][lane] = v;
   __syncthreads();
-  if (sl == 0 && c < cols) {
-    for (int i = 1; i < 16; ++i) v += s[i][lane];
-    out[c] = v;
+  if (sl != 0 || c >= cols) return;
+  for (int i = 1; i < 16; ++i) v += s[i][lane];
+  if (blockIdx.y == 0) {
+    d_w_pre[c] = v;
+  } else {
+    if (d_w_post) d_w_post[c] = gate ? gate[c] * v : v;
+    if (d_gate) d_gate[c] = w_post ? w_post[c] * v : v;
   }
 }
 
@@ -402,61 +482,74 @@ struct NormCfg {
   int tpr, ch;
 };
 NormCfg norm_cfg(int64_t cols) {
+  if (cols <= 128) return {16, 1};
+  if (cols <= 256) return {32, 1};
   if (cols <= 512) return {64, 1};
+  if (cols <= 1024) return {128, 1};
   if (cols <= 2048) return {256, 1};
-  if (cols <= 4096) return {256, 2};
-  if (cols <= 8192) return {512, 2};
+  if (cols <= 4096) return {512, 1};
+  if (cols <= 8192) return {1024, 1};
   return {1024, 2};
 }
 
-template <typename T, int VEC, int TPR, int CH>
+template <typename T, bool AL, int TPR, int CH>
 hipError_t run_fwd(const NormFwd& a, hipStream_t s) {
   constexpr int BT = TPR < 256 ? 256 : TPR, RPB = BT / TPR;
   const int64_t trips = (a.rows + RPB - 1) / RPB;
-  const int64_t cap = (int64_t)device_cus() * (2048 / BT);
+  const int64_t cap = (int64_t)device_cus() * (BT < 1024 ? 1536 / BT : 2);
   const unsigned grid = (unsigned)(trips < cap || cap <= 0 ? trips : cap);
   if (a.amax && grid > 1) {
     const hipError_t e = launch_zero_amax(a.amax, nullptr, s);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((k_block_norm<T, VEC, TPR, CH>), dim3(grid), dim3(BT), 0, s, a);
+  hipLaunchKernelGGL((k_block_norm<T, AL, TPR, CH>), dim3(grid), dim3(BT), 0, s, a);
   return hipGetLastError();
 }
 
-template <typename T, int VEC>
+template <typename T, bool AL>
 hipError_t pick_fwd(const NormFwd& a, hipStream_t s) {
   const NormCfg c = norm_cfg(a.cols);
-  if (c.tpr == 64) return run_fwd<T, VEC, 64, 1>(a, s);
-  if (c.tpr == 256) return c.ch == 1 ? run_fwd<T, VEC, 256, 1>(a, s) : run_fwd<T, VEC, 256, 2>(a, s);
-  if (c.tpr == 512) return run_fwd<T, VEC, 512, 2>(a, s);
-  return run_fwd<T, VEC, 1024, 2>(a, s);
+  if (c.tpr == 16) return run_fwd<T, AL, 16, 1>(a, s);
+  if (c.tpr == 32) return run_fwd<T, AL, 32, 1>(a, s);
+  if (c.tpr == 64) return run_fwd<T, AL, 64, 1>(a, s);
+  if (c.tpr == 128) return run_fwd<T, AL, 128, 1>(a, s);
+  if (c.tpr == 256) return run_fwd<T, AL, 256, 1>(a, s);
+  if (c.tpr == 512) return run_fwd<T, AL, 512, 1>(a, s);
+  return c.ch == 1 ? run_fwd<T, AL, 1024, 1>(a, s) : run_fwd<T, AL, 1024, 2>(a, s);
 }
 
-template <typename T, int VEC, int TPR, int CH>
+template <typename T, bool AL, int TPR, int CH>
 hipError_t run_bwd(const NormBwd& a, unsigned grid, hipStream_t s) {
   constexpr int BT = TPR < 512 ? 512 : TPR;
-  hipLaunchKernelGGL((k_block_norm_bwd<T, VEC, TPR, CH>), dim3(grid), dim3(BT),
-                     BT > TPR ? BT * 8 * sizeof(float) : 0, s, a);
+  constexpr int LDS = CH > 1 ? 2 * CH * 8 * BT * 4 : BT > TPR ? BT * 8 * 4 : 0;
+  const void* fn = reinterpret_cast<const void*>(&k_block_norm_bwd<T, AL, TPR, CH>);
+  if (LDS > 64 * 1024 && set_lds_limit(fn, LDS) != hipSuccess) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_block_norm_bwd<T, AL, TPR, CH>), dim3(grid), dim3(BT), LDS, s, a);
   return hipGetLastError();
 }
 
-template <typename T, int VEC>
+template <typename T, bool AL>
 hipError_t pick_bwd(const NormBwd& a, unsigned grid, hipStream_t s) {
   const NormCfg c = norm_cfg(a.cols);
-  if (c.tpr == 64) return run_bwd<T, VEC, 64, 1>(a, grid, s);
-  if (c.tpr == 256) return c.ch == 1 ? run_bwd<T, VEC, 256, 1>(a, grid, s) : run_bwd<T, VEC, 256, 2>(a, grid, s);
-  if (c.tpr == 512) return run_bwd<T, VEC, 512, 2>(a, grid, s);
-  return run_bwd<T, VEC, 1024, 2>(a, grid, s);
+  if (c.tpr == 16) return run_bwd<T, AL, 16, 1>(a, grid, s);
+  if (c.tpr == 32) return run_bwd<T, AL, 32, 1>(a, grid, s);
+  if (c.tpr == 64) return run_bwd<T, AL, 64, 1>(a, grid, s);
+  if (c.tpr == 128) return run_bwd<T, AL, 128, 1>(a, grid, s);
+  if (c.tpr == 256) return run_bwd<T, AL, 256, 1>(a, grid, s);
+  if (c.tpr == 512) return run_bwd<T, AL, 512, 1>(a, grid, s);
+  return c.ch == 1 ? run_bwd<T, AL, 1024, 1>(a, grid, s) : run_bwd<T, AL, 1024, 2>(a, grid, s);
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Workgroups of the backward pass: at most 512 (two per compute unit of the
-// 256), so that the partial column sums stay small next to the tensors.
+// 256; one where the column sums fill its LDS), so that the partial column sums
+// stay small next to the tensors.
 unsigned bwd_grid(int64_t rows, int64_t cols) {
-  const int tpr = norm_cfg(cols).tpr, rpb = (tpr < 512 ? 512 : tpr) / tpr;
-  const int64_t trips = (rows + rpb - 1) / rpb;
-  return (unsigned)(trips < 512 ? trips : 512);
+  const NormCfg c = norm_cfg(cols);
+  const int rpb = (c.tpr < 512 ? 512 : c.tpr) / c.tpr;
+  const int64_t trips = (rows + rpb - 1) / rpb, most = c.ch > 1 ? 256 : 512;
+  return (unsigned)(trips < most ? trips : most);
 }
 
 }  // namespace
@@ -464,12 +557,12 @@ unsigned bwd_grid(int64_t rows, int64_t cols) {
 hipError_t launch_block_norm(const NormFwd& a, hipStream_t s) {
   const bool vec = a.cols % 8 == 0 && al16(a.x) && al16(a.o) && al16(a.w_post) && al16(a.w_pre) && al16(a.r) &&
                    al16(a.h) && (a.gate_kind == kGateNone || a.gate_kind == kGateRow || al16(a.gate));
-  if (a.f32) return vec ? pick_fwd<float, 8>(a, s) : pick_fwd<float, 1>(a, s);
-  return vec ? pick_fwd<uint16_t, 8>(a, s) : pick_fwd<uint16_t, 1>(a, s);
+  if (a.f32) return vec ? pick_fwd<float, true>(a, s) : pick_fwd<float, false>(a, s);
+  return vec ? pick_fwd<uint16_t, true>(a, s) : pick_fwd<uint16_t, false>(a, s);
 }
 
 int64_t block_norm_bwd_part_bytes(int64_t rows, int64_t cols) {
-  return (int64_t)bwd_grid(rows, cols) * 3 * cols * (int64_t)sizeof(float);
+  return (int64_t)bwd_grid(rows, cols) * 2 * cols * (int64_t)sizeof(float);
 }
 
 hipError_t launch_block_norm_bwd(const NormBwd& a, hipStream_t s) {
@@ -480,16 +573,15 @@ hipError_t launch_block_norm_bwd(const NormBwd& a, hipStream_t s) {
   const unsigned grid = bwd_grid(a.rows, a.cols);
   hipError_t e = hipSuccess;
   if (a.rows > 0) {                                 // the column sums of no rows are zero
-    if (a.f32) e = vec ? pick_bwd<float, 8>(a, grid, s) : pick_bwd<float, 1>(a, grid, s);
-    else e = vec ? pick_bwd<uint16_t, 8>(a, grid, s) : pick_bwd<uint16_t, 1>(a, grid, s);
+    if (a.f32) e = vec ? pick_bwd<float, true>(a, grid, s) : pick_bwd<float, false>(a, grid, s);
+    else e = vec ? pick_bwd<uint16_t, true>(a, grid, s) : pick_bwd<uint16_t, false>(a, grid, s);
   }
   if (e != hipSuccess) return e;
-  float* o0 = a.w_pre ? a.d_w_pre : nullptr;
-  float* o1 = a.w_post ? a.d_w_post : nullptr;
-  float* o2 = chan ? static_cast<float*>(a.d_gate) : nullptr;
-  if (o0 || o1 || o2)
-    hipLaunchKernelGGL(k_col_sum, dim3((unsigned)((a.cols + 63) / 64), 3), dim3(1024), 0, s, a.part, (int)grid,
-                       a.cols, o0, o1, o2);
+  float* d_gate = chan ? static_cast<float*>(a.d_gate) : nullptr;
+  if (a.d_w_pre || a.d_w_post || d_gate)
+    hipLaunchKernelGGL(k_col_sum, dim3((unsigned)((a.cols + 63) / 64), 2), dim3(1024), 0, s, a.part,
+                       a.rows > 0 ? (int)grid : 0, a.cols, a.d_w_pre, a.d_w_post, d_gate, a.w_post,
+                       chan ? static_cast<const float*>(a.gate) : nullptr);
   return hipGetLastError();
 }
 

@@ -69,6 +69,13 @@ CASES = [  # rows, cols, residual, gate, post, pre, o
     (515, 1408, "bf16", None, False, True, False),
     (70, 64, "f32", None, False, True, False),
     (2, 63, "bf16", None, False, False, True),
+    (1000, 127, "bf16", "channel", True, True, True),
+    (301, 128, "f32", "row", True, True, True),
+    (77, 200, "bf16", "full", True, True, True),
+    (50, 256, "f32", None, True, True, True),
+    (40, 1024, "bf16", "channel", True, True, True),
+    (21, 8192, "f32", "full", True, True, True),
+    (19, 12000, "bf16", "row", True, True, True),
 ]
 
 
