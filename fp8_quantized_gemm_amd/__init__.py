@@ -9,6 +9,7 @@ entry point raises; there is no fallback.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -95,11 +96,18 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle without building a Stream object (0.1 against 2.1 us
+# of the 10-20 us that a small call takes on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check_device(*tensors, out=None):
@@ -517,10 +525,8 @@ def block_norm_backward(r, o=None, d_r=None, d_h=None, w_pre=None, w_post=None, 
     rstd_pre = _check_like(rstd_pre, "rstd_pre", (R,), torch.float32, dev)
     rstd_post = _check_like(rstd_post, "rstd_post", (R,), torch.float32, dev)
     kind, gate = _check_gate(gate, R, C, dev)
-    need = ctypes.c_int64(0)
-    _check("block_norm_backward_workspace",
-           lib().block_norm_backward_workspace(R, C, ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    need = _size("block_norm_backward_workspace", R, C)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
     d_x = torch.empty_like(r)
     d_o = torch.empty_like(o) if o is not None else None
     d_g = torch.empty_like(gate) if gate is not None else None
@@ -529,7 +535,7 @@ def block_norm_backward(r, o=None, d_r=None, d_h=None, w_pre=None, w_post=None, 
     st = lib().block_norm_backward(_ptr(r), int(r.dtype == torch.float32), _ptr(o), _ptr(d_r), _ptr(d_h),
                                    R, C, _ptr(w_post), kind, _ptr(gate), float(alpha), _ptr(w_pre),
                                    _ptr(rstd_post), _ptr(rstd_pre), _ptr(d_x), _ptr(d_o), _ptr(d_g),
-                                   _ptr(d_wp), _ptr(d_wq), _ptr(ws), need.value, _stream(dev))
+                                   _ptr(d_wp), _ptr(d_wq), _ptr(ws), need, _stream(dev))
     _check("block_norm_backward", st)
     return dict(d_x=d_x, d_o=d_o, d_gate=d_g, d_w_pre=d_wp, d_w_post=d_wq)
 
@@ -542,11 +548,17 @@ def _scoring(name):
     return SCORING[name]
 
 
+@functools.lru_cache(maxsize=1024)
+def _size(fn, *args):
+    """The int64 a size query of the library returns for these sizes."""
+    n = ctypes.c_int64(0)
+    _check(fn, getattr(lib(), fn)(*args, ctypes.byref(n)))
+    return n.value
+
+
 def moe_rows(tokens, experts, k, align=1):
     """Rows of the expert-ordered buffers of moe_route for these sizes."""
-    n = ctypes.c_int64(0)
-    _check("moe_rows", lib().moe_rows(int(tokens), int(experts), int(k), int(align), ctypes.byref(n)))
-    return n.value
+    return _size("moe_rows", int(tokens), int(experts), int(k), int(align))
 
 
 def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1):
@@ -559,16 +571,15 @@ def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0
     logits = _check_stream(logits, "logits")
     (T, E), dev, k = logits.shape, logits.device, int(k)
     bias = _check_like(bias, "bias", (E,), torch.float32, dev)
-    sc, need = _scoring(scoring), ctypes.c_int64(0)
-    rows = moe_rows(T, E, k, align)
-    _check("moe_route_workspace", lib().moe_route_workspace(T, E, k, ctypes.byref(need)))
+    sc, rows = _scoring(scoring), moe_rows(T, E, k, align)
+    need = _size("moe_route_workspace", T, E, k)
     i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
     ids, row_of, off, src = i32(T, k), i32(T, k), i32(E + 1), i32(rows)
     w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    ws = i32(need.value // 4)
+    ws = i32(need // 4) if need else None
     st = lib().moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
                          1 if normalize else 0, float(scale), int(align), rows, _ptr(ids), _ptr(w), _ptr(off),
-                         _ptr(row_of), _ptr(src), _ptr(ws), need.value, _stream(dev))
+                         _ptr(row_of), _ptr(src), _ptr(ws), need, _stream(dev))
     _check("moe_route", st)
     return dict(experts=ids, weights=w, offsets=off, row_of=row_of, src=src)
 

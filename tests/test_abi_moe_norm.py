@@ -54,7 +54,7 @@ def _norm_bwd(**kw):
 
 def test_block_norm_backward_refusals():
     need = ctypes.c_int64(0)
-    assert bsq.lib().block_norm_backward_workspace(8, 64, ctypes.byref(need)) == OK and need.value >= 3 * 64 * 4
+    assert bsq.lib().block_norm_backward_workspace(8, 64, ctypes.byref(need)) == OK and need.value > 0
     assert bsq.lib().block_norm_backward_workspace(8, 64, None) == EINVAL
     assert _norm_bwd(wsb=need.value - 1) == EINVAL and _norm_bwd(ws=None) == EINVAL and _norm_bwd(ws=G + 4) == EINVAL
     assert _norm_bwd(dx=None) == EINVAL and _norm_bwd(do=None) == EINVAL
@@ -91,10 +91,10 @@ def test_moe_route_refusals():
     assert _route(rows=31) == EINVAL and _route(al=16) == EINVAL       # src shorter than the bound
     assert _route(k=0) == EINVAL and _route(k=9) == EINVAL and _route(E=600) == EUNSUP
     assert _route(sc=2) == EINVAL and _route(t=3) == EINVAL
-    for p in ("lg", "ids", "w", "off", "ro", "src", "ws"):
+    for p in ("lg", "ids", "w", "off", "ro", "src"):
         assert _route(**{p: None}) == EINVAL, p
     assert _route(ids=B + 2) == EINVAL and _route(lg=A + 1) == EINVAL and _route(bias=A + 2) == EINVAL
-    assert _route(wsb=4) == EINVAL
+    assert _route(T=128, rows=256, ws=None) == EINVAL and _route(T=128, rows=256, wsb=4) == EINVAL
     L = bsq.lib()
     assert L.moe_route_backward(A, 0, 16, 8, 2, B, C, 0, 1, 1.0, A, None) == EINVAL    # overlap
     assert L.moe_route_backward(A, 0, 16, 8, 2, None, C, 0, 1, 1.0, D, None) == EINVAL
