@@ -22,103 +22,102 @@ __device__ __forceinline__ float log_sigmoid(float l) {
 }
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-__device__ __forceinline__ float wave_max_f(float v) { return float_of_key(wave_max_dpp(float_key(v))); }
+// One token per DPP row of 16 lanes, four tokens per wave: a lane holds NV experts
+// (expert 16 j + lane in element j) and, afterwards, slot `lane` of the token
+// (k <= 16).  Against one token per wave the exponentials of the k slots and the
+// steps of each argmax serve four tokens, and the reductions are four steps
+// instead of seven (16,381 tokens over 128 experts: 9 us against 18 us).
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, dpp_or0<0xB1, 0xF>(v));
+  v = max(v, dpp_or0<0x4E, 0xF>(v));
+  v = max(v, dpp_or0<0x141, 0xF>(v));
+  return max(v, dpp_or0<0x140, 0xF>(v));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t v) { return ~row_max(~v); }
+__device__ __forceinline__ float row_max_f(float v) { return float_of_key(row_max(float_key(v))); }
+__device__ __forceinline__ float row_sum(float v) {
+  v += u2f(dpp_or0<0xB1, 0xF>(f2u(v)));
+  v += u2f(dpp_or0<0x4E, 0xF>(f2u(v)));
+  v += u2f(dpp_or0<0x141, 0xF>(f2u(v)));
+  return v + u2f(dpp_or0<0x140, 0xF>(f2u(v)));
+}
 
 constexpr float kNegInf = -__builtin_inff();
 
-// Softmax over the lanes with `on` (0 elsewhere).
-__device__ __forceinline__ float lanes_softmax(float l, bool on) {
-  const float m = wave_max_f(on ? l : kNegInf);
+// Softmax over the row's lanes with `on` (0 elsewhere).
+__device__ __forceinline__ float row_softmax(float l, bool on) {
+  const float m = row_max_f(on ? l : kNegInf);
   const float z = on ? expf(l - m) : 0.0f;
-  const float sum = wave_sum(z);
+  const float sum = row_sum(z);
   return on ? z / sum : 0.0f;
 }
 
-// Max and sum of exp(l - max) over a token's unmasked logits (NV per lane).
+// Max and sum of exp(l - max) over a token's unmasked logits.
 template <int NV>
 __device__ __forceinline__ void full_softmax_stats(const float (&l)[NV], float& m, float& sum) {
   float lm = kNegInf;
 #pragma unroll
   for (int j = 0; j < NV; ++j) lm = fmaxf(lm, l[j]);
-  m = wave_max_f(lm);
+  m = row_max_f(lm);
   float s = 0.0f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) s += l[j] > kNegInf ? expf(l[j] - m) : 0.0f;
-  sum = wave_sum(s);
+  sum = row_sum(s);
 }
 
-// A token's logits, expert lane * NV + j in element j; masked (past the last
+// A token's logits, expert 16 j + lane in element j; masked (past the last
 // expert, -inf, NaN) ones as -inf.
 template <int NV>
 __device__ __forceinline__ void load_logits(const void* logits, bool f32, int64_t t, int experts, int lane,
                                             float (&l)[NV]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = lane * NV + j;
+    const int e = 16 * j + lane;
     const float v = e < experts ? logit_at(logits, f32, t * experts + e) : kNegInf;
     l[j] = v > kNegInf ? v : kNegInf;              // NaN compares false
   }
 }
 
-// Selection and weights of U tokens from t0 on by one wave: lane j < k gets slot
-// j's expert (-1: none left) and weight of each.  Each slot is an argmax over
-// the wave, a chain of some 15 dependent steps; the U chains are independent and
-// hide each other's latency (4 tokens at a time: 16,381 tokens over 128 experts in
-// 12 us against 31 us one at a time).
-template <int NV, int U>
-__device__ __forceinline__ void route_tokens(const RouteArgs& a, int64_t t0, int64_t t1, int lane,
-                                             const float (&bias)[NV], int (&id)[U], float (&w)[U]) {
-  float l[U][NV], sel[U];
-  uint32_t key[U][NV];
+// Selection and weight of token t: lane j < k of the row gets slot j's expert
+// (-1: none left) and weight.
+template <int NV>
+__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, const float (&bias)[NV],
+                                            int& id, float& w) {
+  float l[NV];                                     // read again for the softmax over all: fewer registers
+  load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
+  uint32_t key[NV];
 #pragma unroll
-  for (int u = 0; u < U; ++u) load_logits<NV>(a.logits, a.f32, t0 + u < t1 ? t0 + u : t1 - 1, a.experts, lane, l[u]);
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    id[u] = -1;
-    sel[u] = kNegInf;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const float s = (l[u][j] + bias[j]) + 0.0f;  // -0 counts as +0
-      key[u][j] = s > kNegInf ? float_key(s) : 0u;
-    }
+  for (int j = 0; j < NV; ++j) {
+    const float s = (l[j] + bias[j]) + 0.0f;       // -0 counts as +0
+    key[j] = s > kNegInf ? float_key(s) : 0u;
   }
+  uint32_t mine = ~0u;
   for (int s = 0; s < a.k; ++s) {
+    uint32_t best = 0, e = ~0u;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t best = 0;
-      int bj = 0;
-      float bl = kNegInf;
+    for (int j = 0; j < NV; ++j)
+      if (key[j] > best) best = key[j], e = 16 * j + lane;   // the lowest of equal keys
+    const uint32_t m = row_max(best);
+    const uint32_t win = row_min(best == m && m != 0 ? e : ~0u);   // ... over the lanes; ~0: nothing left
+    if (lane == s) mine = win;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (key[u][j] > best) best = key[u][j], bj = j, bl = l[u][j];   // the lowest index of equal keys
-      const uint32_t m = wave_max_dpp(best);
-      const int win = __builtin_ctzll(__ballot(best == m));
-      const int e = __builtin_amdgcn_readlane(lane * NV + bj, win);
-      const float lv = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(bl), win));
-      if (lane == s && m != 0) {                   // m == 0: nothing left
-        id[u] = e;
-        sel[u] = lv;
-      }
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (lane == win && j == bj) key[u][j] = 0;
-    }
+    for (int j = 0; j < NV; ++j)
+      if (win == (uint32_t)(16 * j + lane)) key[j] = 0;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const bool on = id[u] >= 0;
-    float p;
-    if (a.normalize) {
-      p = lanes_softmax(a.sigmoid && on ? log_sigmoid(sel[u]) : sel[u], on);
-    } else if (a.sigmoid) {
-      p = on ? sigmoid(sel[u]) : 0.0f;
-    } else {
-      float m, sum;
-      full_softmax_stats<NV>(l[u], m, sum);
-      p = on ? expf(sel[u] - m) / sum : 0.0f;
-    }
-    w[u] = on ? a.scale * p : 0.0f;
+  id = (int)mine;                                  // ~0 is -1
+  const bool on = id >= 0;
+  const float sel = on ? logit_at(a.logits, a.f32, t * a.experts + id) : kNegInf;
+  if (a.normalize) {
+    w = row_softmax(a.sigmoid && on ? log_sigmoid(sel) : sel, on);
+  } else if (a.sigmoid) {
+    w = on ? sigmoid(sel) : 0.0f;
+  } else {
+    float m, sum;
+    load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
+    full_softmax_stats<NV>(l, m, sum);
+    w = on ? expf(sel - m) / sum : 0.0f;
   }
+  w = on ? a.scale * w : 0.0f;
 }
 
 constexpr int kRouteThreads = 1024, kRouteWaves = kRouteThreads / 64;
@@ -133,33 +132,24 @@ __host__ __device__ inline int route_span(int64_t tokens) {
 // Selection, weights and per-expert counts of the workgroup's tokens.
 template <int NV>
 __device__ __forceinline__ void route_select(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* cnt) {
-  constexpr int U = NV <= 4 ? 4 : 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 15, row = threadIdx.x >> 4;
   float bias[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int e = lane * NV + j;
+    const int e = 16 * j + lane;
     bias[j] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
   }
-  for (int64_t t = t0 + wave * U; t < t1; t += kRouteWaves * U) {
-    int id[U];
-    float w[U];
-    route_tokens<NV, U>(a, t, t1, lane, bias, id, w);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (lane < a.k && t + u < t1) {
-        a.ids[(t + u) * a.k + lane] = id[u];
-        a.weights[(t + u) * a.k + lane] = w[u];
-        if (id[u] >= 0) atomicAdd(&cnt[id[u]], 1);
-      }
+  for (int64_t tb = t0; tb < t1; tb += kRouteThreads / 16) {
+    const int64_t t = tb + row;
+    int id;
+    float w;
+    route_token<NV>(a, t < t1 ? t : t1 - 1, lane, bias, id, w);
+    if (lane < a.k && t < t1) {
+      a.ids[t * a.k + lane] = id;
+      a.weights[t * a.k + lane] = w;
+      if (id >= 0) atomicAdd(&cnt[id], 1);
+    }
   }
-}
-
-__device__ __forceinline__ void route_select_any(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* cnt) {
-  if (a.experts <= 64) route_select<1>(a, t0, t1, cnt);
-  else if (a.experts <= 128) route_select<2>(a, t0, t1, cnt);
-  else if (a.experts <= 256) route_select<4>(a, t0, t1, cnt);
-  else route_select<8>(a, t0, t1, cnt);
 }
 
 // Rows of the workgroup's assignments.  before[e]: assignments of expert e in
@@ -253,25 +243,27 @@ __device__ __forceinline__ void route_fill(const RouteArgs& a, const RouteLds& s
 }
 
 // Everything in one workgroup (few tokens: launches cost more than the work).
+template <int NV>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route_small(RouteArgs a) {
   __shared__ RouteLds s;
   const int tid = threadIdx.x;
   for (int e = tid; e < a.experts; e += kRouteThreads) s.total[e] = s.run[0][e] = 0;
   __syncthreads();
-  route_select_any(a, 0, a.tokens, s.total);
+  route_select<NV>(a, 0, a.tokens, s.total);
   __threadfence_block();                                 // ids written above are read below by other waves
   __syncthreads();
   route_place(a, 0, a.tokens, s, true);
   route_fill(a, s, 0, 1);
 }
 
+template <int NV>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_select(RouteArgs a) {
   __shared__ int32_t cnt[kMoeMaxExperts];
   const int span = route_span(a.tokens);
   const int64_t t0 = (int64_t)blockIdx.x * span, t1 = t0 + span < a.tokens ? t0 + span : a.tokens;
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) cnt[e] = 0;
   __syncthreads();
-  route_select_any(a, t0, t1, cnt);
+  route_select<NV>(a, t0, t1, cnt);
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
 }
@@ -288,7 +280,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_place(RouteArgs a) {
   const int e = tid % E, sl = tid / E;
   if (sl < slices) {
     int all = 0, before = 0;
-#pragma unroll 4
+#pragma unroll 16
     for (int b = sl; b < nblk; b += slices) {
       const int v = a.hist[(int64_t)b * E + e];
       all += v;
@@ -302,57 +294,63 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_place(RouteArgs a) {
   route_fill(a, s, blk, nblk);
 }
 
-// Gradient of the weights with respect to the logits, one wave per token.
+// Gradient of the weights with respect to the logits, one token per 16 lanes.
 template <int NV>
 __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts,
                                                        int k, const int32_t* __restrict__ ids,
                                                        const float* __restrict__ d_w, bool sig, bool normalize,
                                                        float scale, void* d_logits) {
-  const int lane = threadIdx.x & 63;
-  const int64_t nw = (int64_t)gridDim.x * 4;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tokens; t += nw) {
+  // the slots' gradients are scattered into the token's row here, each 16 lanes
+  // (of one wave) their own
+  __shared__ float scat[16][NV * 16];
+  const int lane = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const bool full = !sig && !normalize;
+  for (int64_t tb = (int64_t)blockIdx.x * 16; tb < tokens; tb += (int64_t)gridDim.x * 16) {
+    const bool live = tb + row < tokens;
+    const int64_t t = live ? tb + row : tokens - 1;
     int id = lane < k ? ids[t * k + lane] : -1;
     if ((unsigned)id >= (unsigned)experts) id = -1;
     const bool on = id >= 0;
     const float dp = on ? scale * d_w[t * k + lane] : 0.0f;
     const float sel = on ? logit_at(logits, f32, t * experts + id) : kNegInf;
-    float l[NV], d[NV];
+    float l[NV];
     float ds = 0.0f;                                     // this lane's slot: gradient of its logit
     float mean = 0.0f, m = 0.0f, sum = 1.0f;
-    const bool full = !sig && !normalize;
     if (full) {
       load_logits<NV>(logits, f32, t, experts, lane, l);
       full_softmax_stats<NV>(l, m, sum);
       const float p = on ? expf(sel - m) / sum : 0.0f;
-      mean = wave_sum(dp * p);
+      mean = row_sum(dp * p);
       ds = dp;                                           // joined with the rest below
     } else if (normalize) {
-      const float p = lanes_softmax(sig && on ? log_sigmoid(sel) : sel, on);
-      mean = wave_sum(dp * p);
+      const float p = row_softmax(sig && on ? log_sigmoid(sel) : sel, on);
+      mean = row_sum(dp * p);
       ds = on ? p * (dp - mean) : 0.0f;
       if (sig && on) ds *= sigmoid(-sel);                // d log(sigmoid) = sigmoid(-l)
     } else if (on) {
       ds = dp * (sigmoid(sel) * sigmoid(-sel));
     }
-    const bool any = __ballot(on) != 0;
+    const bool any = row_max(on ? 1u : 0u) != 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) d[j] = 0.0f;
-    for (int s = 0; s < k; ++s) {
-      const int e = __builtin_amdgcn_readlane(id, s);
-      const float v = u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(ds), s));
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (e == lane * NV + j) d[j] = v;
-    }
+    for (int j = 0; j < NV; ++j) scat[row][16 * j + lane] = 0.0f;
+    // one wave's LDS operations stay in order; the fences keep the compiler's
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (on) scat[row][id] = ds;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (full) d[j] = any && l[j] > kNegInf ? (expf(l[j] - m) / sum) * (d[j] - mean) : 0.0f;
-      const int e = lane * NV + j;
-      if (e < experts) {
-        if (f32) static_cast<float*>(d_logits)[t * experts + e] = d[j];
-        else static_cast<uint16_t*>(d_logits)[t * experts + e] = bf16_rne(d[j]);
+      const int e = 16 * j + lane;
+      float d = scat[row][e];
+      if (full) d = any && l[j] > kNegInf ? (expf(l[j] - m) / sum) * (d - mean) : 0.0f;
+      if (live && e < experts) {
+        if (f32) static_cast<float*>(d_logits)[t * experts + e] = d;
+        else static_cast<uint16_t*>(d_logits)[t * experts + e] = bf16_rne(d);
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -488,11 +486,19 @@ int64_t moe_route_hist_bytes(int64_t tokens, int experts) {
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
   const int span = route_span(a.tokens);
   const unsigned blocks = (unsigned)((a.tokens + span - 1) / span);
-  if (blocks <= 1) {
-    hipLaunchKernelGGL(k_moe_route_small, dim3(1), dim3(kRouteThreads), 0, s, a);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(k_moe_select, dim3(blocks), dim3(kRouteThreads), 0, s, a);
+#define BSQ_ROUTE(NV)                                                                              \
+  if (blocks <= 1) {                                                                                \
+    hipLaunchKernelGGL(k_moe_route_small<NV>, dim3(1), dim3(kRouteThreads), 0, s, a);                \
+    return hipGetLastError();                                                                       \
+  }                                                                                                 \
+  hipLaunchKernelGGL(k_moe_select<NV>, dim3(blocks), dim3(kRouteThreads), 0, s, a)
+  if (a.experts <= 16) { BSQ_ROUTE(1); }
+  else if (a.experts <= 32) { BSQ_ROUTE(2); }
+  else if (a.experts <= 64) { BSQ_ROUTE(4); }
+  else if (a.experts <= 128) { BSQ_ROUTE(8); }
+  else if (a.experts <= 256) { BSQ_ROUTE(16); }
+  else { BSQ_ROUTE(32); }
+#undef BSQ_ROUTE
   hipLaunchKernelGGL(k_moe_place, dim3(blocks), dim3(kRouteThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -500,14 +506,16 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
 hipError_t launch_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts, int k,
                                 const int32_t* ids, const float* d_w, bool sigmoid, bool normalize,
                                 float scale, void* d_logits, hipStream_t s) {
-  const dim3 grid(wave_grid(tokens)), block(256);
+  const dim3 grid(wave_grid((tokens + 3) / 4)), block(256);
 #define BSQ_BWD(NV)                                                                                  \
   hipLaunchKernelGGL(k_moe_route_bwd<NV>, grid, block, 0, s, logits, f32, tokens, experts, k, ids, d_w, \
                      sigmoid, normalize, scale, d_logits)
-  if (experts <= 64) BSQ_BWD(1);
-  else if (experts <= 128) BSQ_BWD(2);
-  else if (experts <= 256) BSQ_BWD(4);
-  else BSQ_BWD(8);
+  if (experts <= 16) BSQ_BWD(1);
+  else if (experts <= 32) BSQ_BWD(2);
+  else if (experts <= 64) BSQ_BWD(4);
+  else if (experts <= 128) BSQ_BWD(8);
+  else if (experts <= 256) BSQ_BWD(16);
+  else BSQ_BWD(32);
 #undef BSQ_BWD
   return hipGetLastError();
 }
