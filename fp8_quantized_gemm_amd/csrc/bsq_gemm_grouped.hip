@@ -353,10 +353,10 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_gemm_grouped(GroupedArgs 
 
 // ---------------------------------------------------------------- LDS-staged kernel
 //
-// A workgroup of four waves (WM x WN) per output tile of WM MI x WN NI MFMA tiles.  Steps of 128 code bytes per row reach LDS by global ->
-// LDS direct loads (eight lanes per row read one whole line), in two buffers: a
-// step's loads run while the step before is multiplied, one barrier per step.
-// 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so that 16
+// A workgroup of four waves (WM x WN) per output tile of WM MI x WN NI MFMA tiles.
+// Steps of 128 code bytes per row reach LDS by global -> LDS direct loads (eight
+// lanes per row read one whole line), in NB buffers: with two, a step's loads run
+// while the step before is multiplied, one barrier per step.  16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so that 16
 // consecutive rows of one chunk fall on distinct banks.  Scales are staged as
 // dwords.  Steps start at a multiple of the step in a row; a step that holds K
 // elements outside [lo, hi) (the range's ends) is clipped: its A codes there are
@@ -364,9 +364,9 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_gemm_grouped(GroupedArgs 
 constexpr int kGlThreads = 256;
 template <int FMT, int MT, int NT>
 constexpr int gl_buf() { return (MT + NT) * (128 + gs_scales<FMT>()); }
-template <int FMT, int MT, int NT>
+template <int FMT, int MT, int NT, int NB>
 constexpr int gl_lds() {
-  constexpr int ring = 2 * gl_buf<FMT, MT, NT>(), epi = gs_store_lds<MT, NT, 1>();
+  constexpr int ring = NB * gl_buf<FMT, MT, NT>(), epi = gs_store_lds<MT, NT, 1>();
   return ring > epi ? ring : epi;
 }
 __host__ __device__ constexpr int gl_swz(int r) { return (r >> 1) & 7; }
@@ -395,8 +395,8 @@ __device__ __forceinline__ void gl_stage(const uint8_t* codes, const uint8_t* sc
   }
 }
 
-template <int FMT, int MI, int NI, int WM, int WN, bool WGRAD>
-__global__ __launch_bounds__(kGlThreads, 2) void k_gemm_grouped_lds(GroupedArgs a, int tiles_m, int tiles_n,
+template <int FMT, int MI, int NI, int WM, int WN, bool WGRAD, int NB>
+__global__ __launch_bounds__(kGlThreads, NB == 1 ? 3 : 2) void k_gemm_grouped_lds(GroupedArgs a, int tiles_m, int tiles_n,
                                                                     int vec_store) {
   constexpr int MT = 16 * WM * MI, NT = 16 * WN * NI, STEP = gs_step<FMT>(), S = gs_scales<FMT>();
   constexpr int BUF = gl_buf<FMT, MT, NT>(), BC = MT * 128, SA = (MT + NT) * 128, SBO = SA + MT * S;
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(kGlThreads, 2) void k_gemm_grouped_lds(GroupedArgs 
   const int last_n = (int)(a.N - n0 < NT ? a.N - n0 - 1 : NT - 1);
   const int steps = (hi + STEP - 1) / STEP;
   const auto stage = [&](int s) {
-    const uint32_t b = smem_lds + (uint32_t)((s & 1) * BUF);
+    const uint32_t b = smem_lds + (uint32_t)((s & (NB - 1)) * BUF);
     gl_stage<FMT, MT>(ac, as, code_ld, scale_ld, kc + s * 128u, ks + (uint32_t)(s * S), last_m, b, b + SA, w, lane);
     gl_stage<FMT, NT>(bc, bs, code_ld, scale_ld, kc + s * 128u, ks + (uint32_t)(s * S), last_n, b + BC, b + SBO, w, lane);
   };
@@ -452,14 +452,18 @@ __global__ __launch_bounds__(kGlThreads, 2) void k_gemm_grouped_lds(GroupedArgs 
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NI; ++j) acc[i][j] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-  if (steps > 0) stage(0);
+  if (NB == 2 && steps > 0) stage(0);
   for (int s = 0; s < steps; ++s) {
-    // step s has landed for every wave, and every wave has read step s - 1,
-    // whose buffer step s + 1 goes into
+    if constexpr (NB == 1) {
+      if (s > 0) lds_barrier();                            // every wave has read step s - 1
+      stage(s);
+    }
+    // step s has landed for every wave, and (two buffers) every wave has read
+    // step s - 1, whose buffer step s + 1 goes into
     wait_vmcnt<0>();
     lds_barrier();
-    if (s + 1 < steps) stage(s + 1);
-    uint8_t* b = smem + (s & 1) * BUF;
+    if (NB == 2 && s + 1 < steps) stage(s + 1);
+    uint8_t* b = smem + (s & (NB - 1)) * BUF;
     if (s * STEP < lo || s * STEP + STEP > hi) {
       for (int q = threadIdx.x; q < MT * 8; q += kGlThreads) {
         const int r = q >> 3, ch = q & 7;
@@ -499,17 +503,17 @@ bool gl_fits(const GroupedArgs& a) {
   return a.K > 0 && a.K % (FMT == kNVFP4 ? 64 : 128) == 0 && a.K < ((int64_t)1 << 24) && sc % 4 == 0;
 }
 
-template <int FMT, int MI, int NI, int WM, int WN, bool WGRAD>
+template <int FMT, int MI, int NI, int WM, int WN, bool WGRAD, int NB = 2>
 hipError_t run_gl(const GroupedArgs& a, hipStream_t s) {
-  constexpr int MT = 16 * WM * MI, NT = 16 * WN * NI, LDS = gl_lds<FMT, MT, NT>();
+  constexpr int MT = 16 * WM * MI, NT = 16 * WN * NI, LDS = gl_lds<FMT, MT, NT, NB>();
   const int64_t tn = (a.N + NT - 1) / NT;
   const int64_t tm = WGRAD ? (a.M + MT - 1) / MT : max_row_tiles(a.M, a.experts, MT);
   const int64_t blocks = tm * tn * (WGRAD ? a.experts : 1);
   if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
   const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
-  if (set_lds_limit(reinterpret_cast<const void*>(&k_gemm_grouped_lds<FMT, MI, NI, WM, WN, WGRAD>), LDS) != hipSuccess)
+  if (set_lds_limit(reinterpret_cast<const void*>(&k_gemm_grouped_lds<FMT, MI, NI, WM, WN, WGRAD, NB>), LDS) != hipSuccess)
     return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_gemm_grouped_lds<FMT, MI, NI, WM, WN, WGRAD>), dim3((unsigned)blocks), dim3(kGlThreads), LDS, s, a,
+  hipLaunchKernelGGL((k_gemm_grouped_lds<FMT, MI, NI, WM, WN, WGRAD, NB>), dim3((unsigned)blocks), dim3(kGlThreads), LDS, s, a,
                      (int)tm, (int)tn, vec ? 1 : 0);
   return hipGetLastError();
 }
@@ -560,7 +564,12 @@ hipError_t run_variant(const GroupedArgs& a, int v, hipStream_t s) {
   if (v == k256x256) return run_rx<FMT>(a, WGRAD, s);
   if (v == kLds64x64) return run_gl<FMT, 2, 2, 2, 2, WGRAD>(a, s);
   if (v == kLds64x128) return run_gl<FMT, 2, 4, 2, 2, WGRAD>(a, s);
-  if (v == kLds128x128) return run_gl<FMT, 4, 4, 2, 2, WGRAD>(a, s);
+  // short reductions (MX): one buffer, so three workgroups instead of two share a
+  // compute unit and cover each other's loads and stores (32 experts of 125 rows,
+  // 2048 x 1408, MXFP4: 46 us against 57 us); NVFP4's expansion keeps the vector
+  // units busy either way and its registers allow only two (106 against 90 us), and
+  // a long K is better off with the next step in flight
+  if (v == kLds128x128) return run_gl<FMT, 4, 4, 2, 2, WGRAD, WGRAD && FMT != kNVFP4 ? 1 : 2>(a, s);
   if (!narrow(a)) return run_gs<FMT, 1, 4, 1, 1, 4, WGRAD, uint64_t>(a, s);
   if constexpr (!WGRAD) {
     if (v == kLds16x128) return run_gl<FMT, 1, 2, 1, 4, WGRAD>(a, s);
@@ -596,10 +605,10 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 // The kernel with the least estimated time for `tiles` tiles of `steps` steps:
 // the longest of the chip's throughput over all tiles, one workgroup's own way
 // through K, and reading B once per row tile at 5 TB/s (rows), plus 0.3 of the
-// other two, which overlap it only in part.  The sizes of the
-// groups are on the device; their average and 0.6 tiles of padding each are
-// taken; a 256 x 256 reduction starts and ends at whole 512-element periods (MX).  Against the
-// best kernel of each shape, over 183 shapes of 1 to 1,024 rows per expert, 4 to
+// other two, which overlap it only in part.  The sizes of the groups are on the
+// device; their average and 0.6 tiles of padding each are taken; a 256 x 256
+// reduction starts and ends at whole 512-element periods (MX).  Against the best
+// kernel of each shape, over 183 shapes of 1 to 1,024 rows per expert, 4 to
 // 64 experts, N 256 to 28,672, all formats and both products: within 10% of it
 // in 147, within 30% in all but one (a 6 us call); the 128 x 128 tile alone would
 // take 2 to 5 times as long for single tokens, the 16 x 128 tile 2 to 4 times for
@@ -622,9 +631,11 @@ int pick(const GroupedArgs& a, bool wgrad) {
     const double tn = (double)((a.N + t.nt - 1) / t.nt);
     const double in_group = rows / groups / t.mt + 0.6;
     const double tm = wgrad ? groups * (double)((a.M + t.mt - 1) / t.mt) : groups * (in_group > 1 ? in_group : 1.0);
-    const double full = tm * tn / cus * (steps * t.step[f] + t.tile);
+    double full = tm * tn / cus * (steps * t.step[f] + t.tile);
     const double alone = steps / t.wk * t.alone[f] + t.tile;
     const double read = wgrad ? 0.0 : tm * (double)a.N * row_bytes / 5e6;
+    // short ranges, clipped at both ends; one buffer for MX (run_variant)
+    if (wgrad && t.v == kLds128x128) full *= FMT == kNVFP4 ? 1.15 : 0.85;
     const double most = full > alone ? (full > read ? full : read) : (alone > read ? alone : read);
     const double us = most + 0.3 * (full + alone + read - most);
     if (us < least) {
