@@ -166,7 +166,7 @@ bsq_status moe_rows_of(int64_t tokens, int experts, int k, int align, int64_t* r
 bsq_status mover_checks(int64_t tokens, int64_t cols, int k, int64_t rows) {
   if (tokens < 0 || cols < 0 || k < 1 || rows < 0 || rows > 0x7FFFFFFF) return BSQ_EINVAL;
   if (tokens > 0x7FFFFFFF / k || too_many(tokens, cols) || too_many(rows, cols)) return BSQ_EINVAL;
-  return BSQ_OK;
+  return cols > (1 << 30) ? BSQ_EUNSUPPORTED : BSQ_OK;  // the kernels' column indexes are 32 bits
 }
 
 bsq_status grouped_format(bsq_format fmt, bsq::Fmt* f) {

@@ -16,82 +16,6 @@ namespace bsq {
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
-// 16 bytes at an address of 2, 4 or 16-byte alignment.
-template <int A>
-struct Piece;
-template <>
-struct Piece<2> { typedef u32x4 type __attribute__((aligned(2))); };
-template <>
-struct Piece<4> { typedef u32x4 type __attribute__((aligned(4))); };
-template <>
-struct Piece<16> { typedef u32x4 type; };
-
-// 8 columns of a row as stored: 16 bytes of BF16, 32 of FP32.
-template <typename T>
-struct Raw {
-  u32x4 v[sizeof(T) / 2];
-};
-
-// Piece at column col of a row of cols columns, zeros past its end.  AL: rows
-// are 16-byte aligned and cols % 8 == 0; else any element alignment (one
-// unaligned 16-byte access per piece, single elements in the row's last piece:
-// 3.5 times faster on odd widths than lanes striding over single elements).
-template <bool AL, typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* row, int col, int cols) {
-  Raw<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
-  if (AL ? col < cols : col + 8 <= cols) {
-    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const U*>(row + col)[i];
-  } else if (!AL && col < cols) {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (col + j < cols) {
-        if constexpr (sizeof(T) == 2) r.v[0][j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
-        else r.v[j >> 2][j & 3] = f2u(row[col + j]);
-      }
-  }
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ float raw_at(const Raw<T>& r, int j) {
-  if constexpr (sizeof(T) == 2) return (j & 1) ? bf16_hi(r.v[0][j >> 1]) : bf16_lo(r.v[0][j >> 1]);
-  else return u2f(r.v[j >> 2][j & 3]);
-}
-// Makes the compiler forget what it unpacked from r: a piece is unpacked again
-// where it is used next, instead of being held as 8 FP32 registers meanwhile.
-template <typename T>
-__device__ __forceinline__ void forget(Raw<T>& r) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) asm volatile("" : "+v"(r.v[i]));
-}
-template <bool AL, typename T>
-__device__ __forceinline__ void store8(T* row, int col, int cols, const float (&y)[8]) {
-  Raw<T> r;
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.v[0][j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.v[j >> 2][j & 3] = f2u(y[j]);
-  }
-  if (AL ? col < cols : col + 8 <= cols) {
-    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<U*>(row + col)[i] = r.v[i];
-  } else if (!AL && col < cols) {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (col + j < cols) {
-        if constexpr (sizeof(T) == 2) row[col + j] = (uint16_t)(r.v[0][j >> 1] >> (16 * (j & 1)));
-        else row[col + j] = y[j];
-      }
-  }
-}
 // Weights of a piece, `fill` where there are none.
 template <bool AL>
 __device__ __forceinline__ void load_w(const float* w, int col, int cols, float fill, float (&y)[8]) {

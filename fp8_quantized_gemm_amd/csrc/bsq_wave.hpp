@@ -50,16 +50,86 @@ __device__ __forceinline__ float float_of_key(uint32_t k) {
 
 __device__ __forceinline__ uint16_t bf16_rne(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
 
-// Eight BF16 values of a 16-byte piece <-> FP32.
-__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float* y) {
-  y[0] = bf16_lo(v.x); y[1] = bf16_hi(v.x);
-  y[2] = bf16_lo(v.y); y[3] = bf16_hi(v.y);
-  y[4] = bf16_lo(v.z); y[5] = bf16_hi(v.z);
-  y[6] = bf16_lo(v.w); y[7] = bf16_hi(v.w);
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes at an address of 2, 4 or 16-byte alignment.
+template <int A>
+struct Piece;
+template <>
+struct Piece<2> { typedef u32x4 type __attribute__((aligned(2))); };
+template <>
+struct Piece<4> { typedef u32x4 type __attribute__((aligned(4))); };
+template <>
+struct Piece<16> { typedef u32x4 type; };
+
+// 8 columns of a row as stored: 16 bytes of BF16, 32 of FP32.
+template <typename T>
+struct Raw {
+  u32x4 v[sizeof(T) / 2];
+};
+
+// Piece at column col of a row of cols columns, zeros past its end.  AL: rows
+// are 16-byte aligned and cols % 8 == 0; else any element alignment (one
+// unaligned 16-byte access per piece, single elements in the row's last piece:
+// 3.5 times faster on odd widths than lanes striding over single elements).
+template <bool AL, typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* row, int col, int cols) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = u32x4{0u, 0u, 0u, 0u};
+  if (AL ? col < cols : col + 8 <= cols) {
+    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const U*>(row + col)[i];
+  } else if (!AL && col < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) {
+        if constexpr (sizeof(T) == 2) r.v[0][j >> 1] |= (uint32_t)row[col + j] << (16 * (j & 1));
+        else r.v[j >> 2][j & 3] = f2u(row[col + j]);
+      }
+  }
+  return r;
 }
-__device__ __forceinline__ uint4 f32_to_bf16x8(const float* y) {
-  return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                    pack_bf16x2(y[6], y[7]));
+template <typename T>
+__device__ __forceinline__ float raw_at(const Raw<T>& r, int j) {
+  if constexpr (sizeof(T) == 2) return (j & 1) ? bf16_hi(r.v[0][j >> 1]) : bf16_lo(r.v[0][j >> 1]);
+  else return u2f(r.v[j >> 2][j & 3]);
+}
+// Makes the compiler forget what it unpacked from r: a piece is unpacked again
+// where it is used next, instead of being held as 8 FP32 registers meanwhile.
+template <typename T>
+__device__ __forceinline__ void forget(Raw<T>& r) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) asm volatile("" : "+v"(r.v[i]));
+}
+template <bool AL, typename T>
+__device__ __forceinline__ void store_raw(T* row, int col, int cols, const Raw<T>& r) {
+  if (AL ? col < cols : col + 8 <= cols) {
+    typedef typename Piece<AL ? 16 : (int)sizeof(T)>::type U;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<U*>(row + col)[i] = r.v[i];
+  } else if (!AL && col < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < cols) {
+        if constexpr (sizeof(T) == 2) row[col + j] = (uint16_t)(r.v[0][j >> 1] >> (16 * (j & 1)));
+        else row[col + j] = u2f(r.v[j >> 2][j & 3]);
+      }
+  }
+}
+// Eight FP32 values rounded to the row's type and stored.
+template <bool AL, typename T>
+__device__ __forceinline__ void store8(T* row, int col, int cols, const float (&y)[8]) {
+  Raw<T> r;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.v[0][j] = pack_bf16x2(y[2 * j], y[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j >> 2][j & 3] = f2u(y[j]);
+  }
+  store_raw<AL>(row, col, cols, r);
 }
 
 }  // namespace bsq

@@ -334,11 +334,10 @@ bsq_status bs_gemm_nvfp4_bx(int64_t M, int64_t N, int64_t K, const uint8_t* a_co
 
 /* ---------------------------------------------------------------------------
  * Around the MLP block: norms, gate and residual, and a mixture-of-experts MLP.
- * The pages' "Performance results" models are pre-norm transformers, and the HN
- * page's pasted paragraph names a sparse hybrid; the pages give no formulas for
- * these parts, so the usual definitions are used, written out below.  All
- * arithmetic is FP32 with one rounding at each store; no result depends on the
- * order of atomics.
+ * What surrounds the block-scaled products in a transformer layer.  The pages
+ * give no formulas for these parts, so the usual definitions are used, written
+ * out below.  All arithmetic is FP32 with one rounding at each store; no result
+ * depends on the order of atomics.
  * ------------------------------------------------------------------------- */
 
 /* Type of a residual stream or of router logits. */
@@ -451,6 +450,7 @@ bsq_status moe_route_backward(const void* logits, bsq_dtype type, int64_t tokens
  * Token rows to expert order: out[p] = x[src[p] / k], zeros where src[p] is not
  * in [0, tokens * k).  Its gradient is moe_combine without weights.
  *   x : in, BF16 [tokens, cols].  src : in, int32 [rows].  out : out, BF16 [rows, cols].
+ * The row movers take cols <= 2^30 (BSQ_EUNSUPPORTED above).
  */
 bsq_status moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
                       int64_t rows, void* out, void* stream);

@@ -114,6 +114,10 @@ def test_mover_refusals():
     assert L.moe_combine_backward(A, B, 4, 64, 2, C, D, None, 8, E_, F, None) == EINVAL
     assert L.moe_combine_backward(A, B, 4, 64, 2, C, D, G, 8, B, F, None) == EINVAL    # d_y over y
     assert L.moe_combine_backward(A, B, 4, 64, 2, None, D, G, 8, E_, F, None) == EINVAL
+    wide = (1 << 30) + 1
+    assert L.moe_gather(A, 1, wide, 2, B, 0, C, None) == EUNSUP
+    assert L.moe_combine(A, 0, wide, B, None, 1, 2, C, None) == EUNSUP
+    assert L.moe_combine_backward(A, B, 1, wide, 2, C, D, G, 0, E_, F, None) == EUNSUP
 
 
 def _grouped(**kw):

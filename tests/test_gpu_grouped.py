@@ -105,6 +105,76 @@ def test_rows(fmt, dyadic, sizes, past, N, K):
     assert torch.equal(got, out[:, :N].contiguous())
 
 
+def _bits(shape, fmt, seed):
+    """Random finite codes of any amount, made on the device."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(0, 0x7F if fmt == "mxfp8" else 256, shape, dtype=torch.uint8, device="cuda", generator=g)
+
+
+@pytest.mark.parametrize("fmt,E,N,K", [("nvfp4", 130, 8192, 8192), ("mxfp4", 130, 8192, 8192), ("mxfp8", 66, 8192, 8192)])
+def test_rows_with_weights_past_32_bit_offsets(fmt, E, N, K):
+    """Weights of more than 4 GiB: the last expert's products are those of the
+    expert alone, whatever kernel either size takes (every partial sum is exact)."""
+    announce("bs_gemm_grouped, weights past 4 GiB", fmt)
+    rng = np.random.default_rng(11)
+    sizes = [0] * E
+    sizes[0], sizes[E // 2], sizes[E - 1] = 3, 1, 40
+    ac, asc = _dev(*_operand(rng, 44, 64, fmt, True))
+    a = torch.zeros((44, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device="cuda")
+    a[:, -ac.shape[1]:] = ac                                 # the last 64 elements only: exact sums
+    unit = 0x38 if fmt == "nvfp4" else 127
+    asc = torch.full((44, K // BLK[fmt]), unit, dtype=torch.uint8, device="cuda")
+    b = _bits((E, N, a.shape[1]), fmt, 12)
+    b[:, :, -ac.shape[1]:] &= 0xBF if fmt == "mxfp8" else 0xFF
+    bs = torch.full((E, N, K // BLK[fmt]), unit, dtype=torch.uint8, device="cuda")
+    am = torch.tensor([2688.0], device="cuda") if fmt == "nvfp4" else None
+    got = bsq.bs_gemm_grouped(fmt, a, asc, b, bs, _offsets(sizes), am, am)
+    r = 0
+    for e, n in ((0, 3), (E // 2, 1), (E - 1, 40)):
+        tail = lambda t, d: np.ascontiguousarray(t[..., -d:].cpu().numpy())
+        d, sd = ac.shape[1], 64 // BLK[fmt]
+        want = _deq(tail(a[r:r + n], d), tail(asc[r:r + n], sd), fmt) @ _deq(tail(b[e], d), tail(bs[e], sd), fmt).T
+        _judge(got[r:r + n], want, fmt != "mxfp8", (fmt, e))
+        r += n
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+def test_reductions_of_more_than_2_24(fmt):
+    """Rows of 2^24 + 64 elements (64-bit offsets inside a tile): ones at both ends
+    and in the middle of K, by small whole numbers."""
+    announce("grouped products, K past 2^24", fmt)
+    K = (1 << 24) + 64
+    rng = np.random.default_rng(13)
+    at = np.array([0, 1, K // 2, K - 33, K - 1])
+    one = {"nvfp4": 2, "mxfp4": 2, "mxfp8": 0x38}[fmt]       # the code of 1.0
+    val = {"nvfp4": [2, 4, 6], "mxfp4": [2, 4, 6], "mxfp8": [0x38, 0x40, 0x48]}[fmt]      # 1, 2, 4
+
+    def sparse(rows, pick):
+        t = torch.zeros((rows, K if fmt == "mxfp8" else K // 2), dtype=torch.uint8, device="cuda")
+        v = np.zeros((rows, len(at)))
+        for r in range(rows):
+            for i, k in enumerate(at):
+                c = pick()
+                v[r, i] = 1.0 if c == one else 2.0 ** (val.index(c))
+                if fmt == "mxfp8":
+                    t[r, k] = c
+                else:
+                    t[r, k // 2] += c << (4 * (int(k) & 1))
+        s = torch.full((rows, K // BLK[fmt]), 0x38 if fmt == "nvfp4" else 127, dtype=torch.uint8, device="cuda")
+        return t, s, v
+    a, asc, av = sparse(5, lambda: one)
+    b, bsc, bv = sparse(6, lambda: int(rng.choice(val)))
+    am = torch.tensor([2688.0], device="cuda") if fmt == "nvfp4" else None
+    got = bsq.bs_gemm_grouped(fmt, a, asc, b.view(2, 3, -1), bsc.view(2, 3, -1), _offsets([4, 1]), am, am)
+    want = np.concatenate([av[:4] @ bv[:3].T, av[4:] @ bv[3:].T])
+    _judge(got, want, True, fmt)
+    cut = K // 2 // 32 * 32
+    got = bsq.bs_gemm_grouped_wgrad(fmt, a, asc, b, bsc, _offsets([cut, K - cut]), am, am)
+    lo = at < cut
+    want = np.stack([av[:, lo] @ bv[:, lo].T, av[:, ~lo] @ bv[:, ~lo].T])
+    _judge(got, want, True, fmt)
+
+
 def test_rows_nvfp4_half_block_and_shared_amax():
     announce("bs_gemm_grouped nvfp4 K = 16, 48, 272, one amax")
     rng = np.random.default_rng(1)

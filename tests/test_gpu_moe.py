@@ -124,6 +124,43 @@ def test_gather_and_combine(T, E, k, align, C):
     assert np.all(np.abs(dw.double().cpu().numpy() - ww) <= (C / 64 + 16) * U * mw)
 
 
+@pytest.mark.parametrize("C", [64, 1000, 1001])
+def test_rows_at_any_element_alignment(C):
+    """The same rows, one element off 16-byte alignment, give the same bits."""
+    announce("movers, unaligned", C)
+    off = lambda t: torch.cat([t.new_zeros(1), t.flatten()])[1:].view(t.shape)
+    f = bsq.moe_route(_logits(57, 16, torch.float32, C), 3, align=16)
+    x, y, d = (torch.randn((n, C), device="cuda").bfloat16() for n in (57, len(f["src"]), 57))
+    assert torch.equal(bsq.moe_gather(off(x), f["src"], 3), bsq.moe_gather(x, f["src"], 3))
+    for w in (None, f["weights"]):
+        assert torch.equal(bsq.moe_combine(off(y), f["row_of"], w), bsq.moe_combine(y, f["row_of"], w))
+    got = bsq.moe_combine_backward(off(d), off(y), f["src"], f["row_of"], f["weights"])
+    want = bsq.moe_combine_backward(d, y, f["src"], f["row_of"], f["weights"])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_rows_past_32_bit_offsets():
+    """2^20 + 8 rows of 4,096: elements past 2^32."""
+    announce("movers, rows past 2^32 elements")
+    T, k, C, rows = 8, 2, 4096, (1 << 20) + 8
+    x = torch.randn((T, C), device="cuda").bfloat16()
+    src = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    place = torch.tensor([0, 1, 1 << 18, (1 << 19) - 1, 1 << 19, (1 << 19) + 3, 5, 6, 7, 8, 9, 10, 11,
+                          1 << 20, (1 << 20) + 1, rows - 1], dtype=torch.int32, device="cuda")
+    src[place.long()] = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    xp = bsq.moe_gather(x, src, k)
+    assert torch.equal(xp[place.long()], x.repeat_interleave(k, 0))
+    assert int(torch.count_nonzero(xp[12:1 << 18])) == 0 and int(torch.count_nonzero(xp[(1 << 20) + 2:rows - 1])) == 0
+    row_of, w = place.view(T, k), torch.rand((T, k), device="cuda")
+    small = torch.arange(T * k, dtype=torch.int32, device="cuda")
+    y = xp[place.long()]
+    assert torch.equal(bsq.moe_combine(xp, row_of, w), bsq.moe_combine(y, small.view(T, k), w))
+    want = bsq.moe_combine_backward(x, y, small, small.view(T, k), w)
+    del y
+    got = bsq.moe_combine_backward(x, xp, src, row_of, w)
+    assert torch.equal(got[0][place.long()], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_indices_out_of_range_are_no_assignment():
     announce("gather / combine with out-of-range indices")
     x = torch.randn((4, 64), device="cuda").bfloat16()
