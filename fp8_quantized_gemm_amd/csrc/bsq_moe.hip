@@ -383,7 +383,10 @@ __global__ __launch_bounds__(256) void k_moe_gather(const uint16_t* __restrict__
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = load_raw<AL>(xr, c + i * 512, have);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store_raw<AL>(o, c + i * 512, n, v[i]);
+      for (int i = 0; i < 4; ++i) {
+        end_piece<AL>(v[i], c + i * 512, have);
+        store_raw<AL>(o, c + i * 512, n, v[i]);
+      }
     }
   }
 }
@@ -408,8 +411,9 @@ __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict_
       const int p = row_of[t * k + j];
       const bool on = p >= 0 && p < rows;
       const float wj = on ? (w ? w[t * k + j] : 1.0f) : 0.0f;
-      const Raw<uint16_t> v = load_raw<AL>(y + (on ? (int64_t)p : 0) * cols, c, on ? n : 0);
+      Raw<uint16_t> v = load_raw<AL>(y + (on ? (int64_t)p : 0) * cols, c, on ? n : 0);
       if (on) {
+        end_piece<AL>(v, c, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(wj, raw_at(v, e), acc[e]);
       }
@@ -451,6 +455,8 @@ __global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restr
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        end_piece<AL>(gv[i], c + i * 512, have);
+        end_piece<AL>(yv[i], c + i * 512, have);
         float z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -469,8 +475,8 @@ __global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restr
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Workgroups for `waves` waves of work, four per workgroup, at most 64 per
-// compute unit: with 8 the last ones to finish show (combine of 8,000 x 2 rows
-// of 4,095: 47 us, with 64 38 us; even widths within 3% either way).
+// compute unit (against 8, with whole rows left over for some: combine of 8,192 x
+// 2 rows of 4,096 30.4 us against 31.3, its gradient 61.9 against 62.9).
 unsigned wave_grid(int64_t waves) {
   const int64_t n = (waves + 3) / 4, cap = (int64_t)(device_cus() > 0 ? device_cus() : 256) * 64;
   return (unsigned)(n < cap ? n : cap);

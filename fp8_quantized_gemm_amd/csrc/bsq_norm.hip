@@ -24,7 +24,8 @@ __device__ __forceinline__ void load_w(const float* w, int col, int cols, float 
     for (int j = 0; j < 8; ++j) y[j] = fill;
     return;
   }
-  const Raw<float> r = load_raw<AL>(w, col, cols);
+  Raw<float> r = load_raw<AL>(w, col, cols);
+  end_piece<AL>(r, col, cols);
 #pragma unroll
   for (int j = 0; j < 8; ++j) y[j] = raw_at(r, j);
 }
@@ -116,6 +117,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_block_norm(NormFwd
     const int64_t row = b * RPB + sub;
     const bool live = row < a.rows;
     const int64_t base = (live ? row : a.rows - 1) * a.cols;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      end_piece<AL>(xr[c], col(c), cols);
+      if (has_o) end_piece<AL>(orow[c], col(c), cols);
+      if (gf) end_piece<AL>(gr[c], col(c), cols);
+    }
     float r[CH][8];
     float rq = 1.0f;
     if (a.w_post) {
@@ -281,6 +288,14 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
     const float rs = pre ? a.rstd_pre[rw] : 0.0f;
     const float rp = post ? a.rstd_post[rw] : 1.0f;
     const float grow = a.gate_kind == kGateRow ? static_cast<const float*>(a.gate)[rw] : 1.0f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      if (d_r) end_piece<AL>(dr[c], col(c), cols);
+      if (pre) end_piece<AL>(dh[c], col(c), cols);
+      if (pre) end_piece<AL>(rr[c], col(c), cols);
+      if (has_o) end_piece<AL>(orow[c], col(c), cols);
+      if (gf) end_piece<AL>(gr[c], col(c), cols);
+    }
     const float one = live ? 1.0f : 0.0f;           // rows past the last add nothing to the column sums
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
