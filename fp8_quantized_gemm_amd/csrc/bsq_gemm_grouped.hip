@@ -603,13 +603,13 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 
 // The kernel with the least estimated time for `tiles` tiles of `steps` steps:
 // the longest of the chip's throughput over all tiles, one workgroup's own way
-// through K, and reading B once per row tile at 5 TB/s (rows), plus 0.3 of the
-// other two, which overlap it only in part.  The sizes of the groups are on the
+// through K, and reading B at 5 TB/s (rows; a group's further row tiles find half
+// of it in cache), plus 0.3 of the other two, which overlap it only in part.  The sizes of the groups are on the
 // device; their average and 0.6 tiles of padding each are taken; a 256 x 256
 // reduction starts and ends at whole 512-element periods (MX).  Against the best
 // kernel of each shape, over 183 shapes of 1 to 1,024 rows per expert, 4 to
 // 64 experts, N 256 to 28,672, all formats and both products: within 10% of it
-// in 147, within 30% in all but one (a 6 us call); the 128 x 128 tile alone would
+// in 160, within 28% in all; the 128 x 128 tile alone would
 // take 2 to 5 times as long for single tokens, the 16 x 128 tile 2 to 4 times for
 // 1,024 rows per expert.
 template <int FMT>
@@ -632,7 +632,7 @@ int pick(const GroupedArgs& a, bool wgrad) {
     const double tm = wgrad ? groups * (double)((a.M + t.mt - 1) / t.mt) : groups * (in_group > 1 ? in_group : 1.0);
     double full = tm * tn / cus * (steps * t.step[f] + t.tile);
     const double alone = steps / t.wk * t.alone[f] + t.tile;
-    const double read = wgrad ? 0.0 : tm * (double)a.N * row_bytes / 5e6;
+    const double read = wgrad ? 0.0 : 0.5 * (groups + tm) * (double)a.N * row_bytes / 5e6;
     // short ranges, clipped at both ends; one buffer for MX (run_variant)
     if (wgrad && t.v == kLds128x128) full *= FMT == kNVFP4 ? 1.15 : 0.85;
     const double most = full > alone ? (full > read ? full : read) : (alone > read ? alone : read);
