@@ -359,34 +359,49 @@ __global__ __launch_bounds__(256) void k_moe_route_bwd(const void* logits, bool 
 // Rows move in pieces of 8 columns per lane, 512 per wave (AL: 16-byte aligned
 // rows; else pieces of any alignment, see load_raw).
 
-// out[p] = x[src[p] / k], zeros where src[p] is no assignment.  One wave per
-// row, four pieces in flight; bound by HBM writes (an input row's further reads
-// come from cache).  8,192 tokens x 2, 4,096 columns into 16,896 rows: 41 us,
-// 5.0 TB/s of rows read once per token and written once.  Stores past the cache
-// are 3% faster here and send the product that reads the rows to HBM, so they
-// are not used.
-template <bool AL>
+// out[p] = x[src[p] / k], zeros where src[p] is no assignment.  A token's rows
+// are far apart in expert order, so each XCD takes one of `slabs` column slabs (of
+// slab pieces) over all rows, eight slabs at a time: the tokens' part of it, read k
+// times, stays in its L2.  LR lanes per row, 64 / LR rows per wave; four pieces in
+// flight, of as many rows (AL) or of one.  Bound by HBM writes: 8,192 tokens x 2,
+// 4,096 columns into 16,896 rows 38 us, 5.5 TB/s of rows read once per token and
+// written once.  Stores past the cache are 3% faster here and send the product
+// that reads the rows to HBM, so they are not used.
+template <bool AL, int LR>
 __global__ __launch_bounds__(256) void k_moe_gather(const uint16_t* __restrict__ x, int64_t tokens, int64_t cols,
                                                     int k, const int32_t* __restrict__ src, int64_t rows,
-                                                    uint16_t* __restrict__ out) {
-  const int lane = threadIdx.x & 63, n = (int)cols;
-  const int64_t nw = (int64_t)gridDim.x * 4;
-  for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += nw) {
-    const int a = __builtin_amdgcn_readfirstlane(src[p]);
-    const int64_t t = a >= 0 ? a / k : -1;
-    const bool on = t >= 0 && t < tokens;
-    const uint16_t* xr = x + (on ? t : 0) * cols;
-    const int have = on ? n : 0;
-    uint16_t* o = out + p * cols;
-    for (int c = lane * 8; c < n; c += 4 * 512) {
-      Raw<uint16_t> v[4];
+                                                    uint16_t* __restrict__ out, int slabs, int slab) {
+  constexpr int RW = 64 / LR, U = AL ? 4 : 1, V = 4 / U;
+  const int lane = threadIdx.x & (LR - 1), n = (int)cols;
+  const int across = slabs < 8 ? slabs : 8;
+  const unsigned per = gridDim.x / slabs, q = blockIdx.x / across;
+  const int c0 = (int)(q / per * across + blockIdx.x % across) * slab * 8, c1 = min(n, c0 + slab * 8);
+  const int64_t wave = (int64_t)(q % per) * 4 + (threadIdx.x >> 6), nw = (int64_t)per * 4;
+  for (int64_t p0 = wave * (U * RW) + (threadIdx.x & 63) / LR; p0 < rows; p0 += nw * (U * RW)) {
+    const uint16_t* xr[U];
+    int have[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = load_raw<AL>(xr, c + i * 512, have);
+    for (int i = 0; i < U; ++i) {
+      const int64_t p = p0 + i * RW;
+      int a = p < rows ? src[p] : -1;
+      if (LR == 64) a = __builtin_amdgcn_readfirstlane(a);
+      const int64_t t = a >= 0 ? a / k : -1;
+      have[i] = t >= 0 && t < tokens ? n : 0;
+      xr[i] = x + (have[i] ? t : 0) * cols;
+    }
+    for (int c = c0 + lane * 8; c < c1; c += V * LR * 8) {
+      Raw<uint16_t> v[U][V];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        end_piece<AL>(v[i], c + i * 512, have);
-        store_raw<AL>(o, c + i * 512, n, v[i]);
-      }
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[i][j] = load_raw<AL>(xr[i], c + j * LR * 8, have[i]);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          end_piece<AL>(v[i][j], c + j * LR * 8, have[i]);
+          if (p0 + i * RW < rows) store_raw<AL>(out + (p0 + i * RW) * cols, c + j * LR * 8, n, v[i][j]);
+        }
     }
   }
 }
@@ -529,13 +544,40 @@ hipError_t launch_moe_route_bwd(const void* logits, bool f32, int64_t tokens, in
 
 hipError_t launch_moe_gather(const void* x, int64_t tokens, int64_t cols, int k, const int32_t* src,
                              int64_t rows, void* out, hipStream_t s) {
-  const dim3 grid(wave_grid(rows)), block(256);
   const uint16_t* xp = static_cast<const uint16_t*>(x);
   uint16_t* op = static_cast<uint16_t*>(out);
-  if (cols % 8 == 0 && al16(x) && al16(out))
-    hipLaunchKernelGGL(k_moe_gather<true>, grid, block, 0, s, xp, tokens, cols, k, src, rows, op);
-  else
-    hipLaunchKernelGGL(k_moe_gather<false>, grid, block, 0, s, xp, tokens, cols, k, src, rows, op);
+  const bool al = cols % 8 == 0 && al16(x) && al16(out);
+  // Column slabs where no two share a 128-byte line (4,093 tokens x 4 of 2,048:
+  // 16.6 us against 20.8 with whole rows; odd widths lose 3-13%, their lines being
+  // written from two XCDs), as narrow as keeps the tokens' part in 3 MiB of an L2
+  // (8,192 x 6 of 2,048: 43 us in 16 slabs, 50 in 8), but at least 128 columns
+  // (16,384 x 8 of 2,048: 207 us in 32 slabs, 140 in 8) and only while the output
+  // fits the 256 MiB behind the L2s, past which short pieces cost more than they
+  // save (8,192 x 16 of 2,048, 545 MB: 162 us in 16 slabs, 132 in 8).
+  int slabs = 1;
+  if (al && cols % 64 == 0 && (reinterpret_cast<uintptr_t>(out) & 127) == 0) {
+    slabs = cols >= 1024 ? 8 : cols >= 512 ? 4 : cols >= 256 ? 2 : 1;
+    if (slabs == 8 && rows * cols * 2 <= (int64_t)256 << 20) {
+      int64_t m = 1;
+      const auto fits = [&] { return tokens * cols * 2 <= 8 * m * ((int64_t)3 << 20); };
+      while (!fits() && cols / (8 * m) >= 256) m *= 2;
+      if (fits()) slabs = (int)(8 * m);
+    }
+  }
+  const int slab = (int)((cols + 64 * (int64_t)slabs - 1) / (64 * (int64_t)slabs)) * 8;
+#define BSQ_GATHER(LR)                                                                              \
+  {                                                                                                  \
+    const dim3 grid(wave_grid((rows + 256 / LR - 1) / (256 / LR)) * slabs), block(256);               \
+    if (al)                                                                                          \
+      hipLaunchKernelGGL((k_moe_gather<true, LR>), grid, block, 0, s, xp, tokens, cols, k, src, rows, op, slabs, slab);  \
+    else                                                                                             \
+      hipLaunchKernelGGL((k_moe_gather<false, LR>), grid, block, 0, s, xp, tokens, cols, k, src, rows, op, slabs, slab); \
+  }
+  if (slab <= 8) BSQ_GATHER(8)
+  else if (slab <= 16) BSQ_GATHER(16)
+  else if (slab <= 32) BSQ_GATHER(32)
+  else BSQ_GATHER(64)
+#undef BSQ_GATHER
   return hipGetLastError();
 }
 

@@ -139,6 +139,20 @@ def test_rows_at_any_element_alignment(C):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("T,k,C", [(7001, 2, 2048), (1700, 3, 8192), (900, 2, 16384 + 64), (515, 4, 1088), (65, 8, 320)])
+def test_gather_in_column_slabs(T, k, C):
+    """Every column is moved once, however the columns are divided."""
+    announce("moe_gather, many columns", T, k, C)
+    f = bsq.moe_route(_logits(T, 8, torch.float32, C), k, align=16)
+    x = torch.randn((T, C), device="cuda").bfloat16()
+    out = torch.full((len(f["src"]), C), 7.0, device="cuda").bfloat16()
+    bsq.moe_gather(x, f["src"], k, out=out)
+    src = f["src"].long()
+    want = x[src.clamp(min=0) // k]
+    want[src < 0] = 0
+    assert torch.equal(out, want)
+
+
 def test_rows_past_32_bit_offsets():
     """2^20 + 8 rows of 4,096: elements past 2^32."""
     announce("movers, rows past 2^32 elements")
