@@ -358,8 +358,10 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_gemm_grouped(GroupedArgs 
 // while the step before is multiplied, one barrier per step.  16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7), so that 16
 // consecutive rows of one chunk fall on distinct banks.  Scales are staged as
 // dwords.  Steps start at a multiple of the step in a row; a step that holds K
-// elements outside [lo, hi) (the range's ends) is clipped: its A codes there are
-// zeroed in LDS, and their products with finite B values vanish.
+// elements outside [lo, hi) (the range's ends) is clipped in LDS: the scales there
+// become 0 (2^-127 for MX) on both sides, and the codes too where that leaves
+// something to add (MXFP4: A's; MXFP8: both), so that the rows of another group
+// add exact zeros whatever they hold, NaN included.
 constexpr int kGlThreads = 256;
 template <int FMT, int MT, int NT>
 constexpr int gl_buf() { return (MT + NT) * (128 + gs_scales<FMT>()); }
@@ -464,13 +466,21 @@ __global__ __launch_bounds__(kGlThreads, NB == 1 ? 3 : 2) void k_gemm_grouped_ld
     if (NB == 2 && s + 1 < steps) stage(s + 1);
     uint8_t* b = smem + (s & (NB - 1)) * BUF;
     if (s * STEP < lo || s * STEP + STEP > hi) {
-      for (int q = threadIdx.x; q < MT * 8; q += kGlThreads) {
-        const int r = q >> 3, ch = q & 7;
-        const int k = s * STEP + ch * (STEP / 8);          // FP8: 16 elements per chunk
+      // codes: MXFP4's A, MXFP8's A and B (whose codes can be NaN); scales: all
+      if constexpr (FMT != kNVFP4) {
+        for (int q = threadIdx.x; q < (FMT == kMXFP8 ? MT + NT : MT) * 8; q += kGlThreads) {
+          const int r = q >> 3, ch = q & 7, k = s * STEP + ch * (STEP / 8);
+          if (k < lo || k >= hi) *reinterpret_cast<u32x4*>(b + r * 128 + ((ch ^ gl_swz(r)) << 4)) = u32x4{0u, 0u, 0u, 0u};
+        }
+      }
+      for (int q = threadIdx.x; q < (MT + NT) * S / 4; q += kGlThreads) {
+        uint32_t* sc = reinterpret_cast<uint32_t*>(b + SA) + q;
+        const int k = s * STEP + q % (S / 4) * 4 * SB;
+        uint32_t keep = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)                        // NVFP4 blocks are half a chunk
-          if (k + h * (STEP / 16) < lo || k + h * (STEP / 16) >= hi)
-            *reinterpret_cast<uint2*>(b + r * 128 + ((ch ^ gl_swz(r)) << 4) + 8 * h) = make_uint2(0, 0);
+        for (int i = 0; i < 4; ++i)
+          if (k + i * SB >= lo && k + i * SB < hi) keep |= 0xFFu << (8 * i);
+        *sc &= keep;
       }
       lds_barrier();
     }

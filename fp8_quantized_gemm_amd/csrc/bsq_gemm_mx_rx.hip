@@ -217,21 +217,40 @@ __device__ __forceinline__ void mr_steps(floatx16 (&acc)[4][4], const MrFrag<FMT
 
 // K range of a reduction that starts or ends inside a scale period (RANGE: K
 // elements lo <= k < hi count, multiples of 32; the units start at a period
-// boundary at or below lo): once unit u has landed, and before its fragments are
-// read, the A codes of the blocks outside are zeroed in LDS, one row per thread.
-// Their products with finite B values and scales are exact zeros.  Only units of
-// the first and the last period can need it.
+// boundary at or below lo): once unit u has landed, and before its fragments and
+// scales are read, the scales of the blocks outside become 2^-127 on both sides
+// and their codes zero on A's (MXFP8: on both, a code can be NaN), one row of each
+// operand per thread, so that the blocks add exact zeros whatever they hold.  Only
+// units of the first and the last period can need it.
 template <int FMT>
 __device__ __forceinline__ void mr_clip(uint8_t* smem, int u, int NU, int lo, int hi) {
   constexpr int KU = fp8_elems(FMT) ? 128 : 256, CB = fp8_elems(FMT) ? 2 : 1;   // K per unit, chunks per block
   const int k0 = u * KU;
   if (u >= NU || (k0 >= lo && k0 + KU <= hi)) return;
+  constexpr int P = mr_period<FMT>();
   const int row = threadIdx.x;
-  uint8_t* r = smem + (u & 1) * kMrUnitB + row * kMrRowB;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    const int k = k0 + c / CB * 32;
-    if (k < lo || k >= hi) *reinterpret_cast<u32x4*>(r + ((c ^ mr_swz(row)) << 4)) = u32x4{0u, 0u, 0u, 0u};
+  for (int op = 0; op < 2; ++op) {
+    if (op == 0 || fp8_elems(FMT)) {
+      uint8_t* r = smem + (u & 1) * kMrUnitB + op * kMrCodeB + row * kMrRowB;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int k = k0 + c / CB * 32;
+        if (k < lo || k >= hi) *reinterpret_cast<u32x4*>(r + ((c ^ mr_swz(row)) << 4)) = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+    uint32_t* sc = reinterpret_cast<uint32_t*>(smem + kMrScOff + (u / P & 1) * (2 * kMrScOpB) + op * kMrScOpB + row * 16 +
+                                               u % P * (KU / 32));
+#pragma unroll
+    for (int d = 0; d < KU / 128; ++d) {
+      uint32_t keep = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int k = k0 + d * 128 + b * 32;
+        if (k >= lo && k < hi) keep |= 0xFFu << (8 * b);
+      }
+      sc[d] &= keep;
+    }
   }
   lds_barrier();
 }

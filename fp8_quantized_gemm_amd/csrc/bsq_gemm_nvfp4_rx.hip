@@ -357,22 +357,23 @@ __device__ __forceinline__ void rx_kstep(floatx4 (&acc)[8][8], RxRegs& r, const 
 
 // K range of a reduction that starts or ends inside a pair (RANGE: K elements
 // lo <= k < hi count, multiples of 16; the units start at a pair boundary at or
-// below lo).  Once pair p has landed, and before its scales are read, the A
-// scales of the blocks outside are zeroed in LDS, one row per thread: an
-// expansion by a zero scale is an exact zero, and the B values it meets are
-// finite.  Only the first and the last pair can need it.
+// below lo).  Once pair p has landed, and before its scales are read, the scales
+// of the blocks outside are zeroed in LDS, one row of each operand per thread: an
+// expansion by a zero scale is an exact zero, also of a block whose own scale is
+// NaN.  Only the first and the last pair can need it.
 __device__ __forceinline__ void rx_clip(uint8_t* smem, int p, int NU, int lo, int hi) {
   const int k0 = p * 256;
   if (2 * p >= NU || (k0 >= lo && k0 + 256 <= hi)) return;
-  uint4* row = reinterpret_cast<uint4*>(smem + (p & 1) * kRxUnitB + kRxCodeB) + threadIdx.x;
-  const uint4 v = *row;
-  uint32_t sc[4] = {v.x, v.y, v.z, v.w};
+  uint32_t keep[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int b = 0; b < 16; ++b) {
-    const int k = k0 + 16 * b;
-    if (k < lo || k >= hi) sc[b >> 2] &= ~(0xFFu << (8 * (b & 3)));
+  for (int b = 0; b < 16; ++b)
+    if (k0 + 16 * b >= lo && k0 + 16 * b < hi) keep[b >> 2] |= 0xFFu << (8 * (b & 3));
+#pragma unroll
+  for (int op = 0; op < 2; ++op) {
+    uint4* row = reinterpret_cast<uint4*>(smem + (p & 1) * kRxUnitB + op * kRxOpB + kRxCodeB) + threadIdx.x;
+    const uint4 v = *row;
+    *row = make_uint4(v.x & keep[0], v.y & keep[1], v.z & keep[2], v.w & keep[3]);
   }
-  *row = make_uint4(sc[0], sc[1], sc[2], sc[3]);
   lds_barrier();
 }
 

@@ -248,6 +248,42 @@ def test_wgrad(fmt, dyadic, blocks, past, M, N):
         _judge(got[e], want[e], dyadic, (fmt, blocks, M, N, e))
 
 
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+@pytest.mark.parametrize("blocks,M,N", [((3, 4, 2), 40, 30), ((5, 9, 30), 128, 200), ((41, 3, 70), 300, 257),
+                                        ((60, 10, 60), 1024, 1500)])
+def test_wgrad_of_a_group_does_not_see_its_neighbours_nan(fmt, blocks, M, N):
+    """NaN scales (and codes, where the format has them) in one group's rows, of
+    either operand or both, leave the other groups' products as they are."""
+    announce("bs_gemm_grouped_wgrad, NaN in one group", fmt, blocks, M, N)
+    rng = np.random.default_rng(21)
+    B = BLK[fmt]
+    K = sum(blocks) * B
+    K = -(-K // 512) * 512                       # aligned rows: the 256 x 256 kernels take them too
+    off = _offsets([b * B for b in blocks])
+    o = off.cpu().numpy()
+    a, b = _operand(rng, M, K, fmt, False), _operand(rng, N, K, fmt, False)
+    am = torch.tensor([3.0], device="cuda") if fmt == "nvfp4" else None
+    want = bsq.bs_gemm_grouped_wgrad(fmt, *_dev(*a), *_dev(*b), off, am, am)
+    assert torch.isfinite(want).all()
+    per = 1 if fmt == "mxfp8" else 2
+    nan_scale = 0x7F if fmt == "nvfp4" else 0xFF
+    for bad in range(-1, len(blocks)):           # -1: the rows past the last group
+        k0, k1 = (o[bad], o[bad + 1]) if bad >= 0 else (o[-1], K)
+        for which in (1, 2, 3):
+            ops = []
+            for i, (codes, scales) in enumerate((a, b)):
+                codes, scales = codes.copy(), scales.copy()
+                if which >> i & 1:
+                    scales[:, k0 // B:k1 // B] = nan_scale
+                    if fmt == "mxfp8":
+                        codes[:, k0 // per:k1 // per] = 0x7F
+                ops += _dev(codes, scales)
+            got = bsq.bs_gemm_grouped_wgrad(fmt, *ops, off, am, am)
+            for e in range(len(blocks)):
+                if e != bad:
+                    assert torch.equal(got[e], want[e]), (bad, which, e)
+
+
 def test_wgrad_offsets_inside_a_block_are_rounded_down():
     announce("bs_gemm_grouped_wgrad unaligned offsets")
     rng = np.random.default_rng(3)
