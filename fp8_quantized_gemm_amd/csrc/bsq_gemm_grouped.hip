@@ -420,6 +420,15 @@ __global__ __launch_bounds__(kGlThreads, NB == 1 ? 3 : 2) void k_gemm_grouped_ld
     m0 = (int64_t)tm * MT;
     mend = a.M;
     group_range<SB, STEP>(ref, e, a.K, lo, hi, t);
+    // a short range starts at a whole dword of scales instead where that saves a
+    // step (32 experts of 125 rows, 2048 x 1408: NVFP4 93 -> 74 us, MXFP4 48 -> 43);
+    // a long one keeps whole lines (MXFP4 up to 1.3 times slower without)
+    const int cut = lo / (4 * SB) * (4 * SB);
+    if (hi <= 3 * STEP && (hi - cut + STEP - 1) / STEP < (hi + STEP - 1) / STEP) {
+      t.row0 += cut;
+      lo -= cut;
+      hi -= cut;
+    }
     kc = (uint32_t)(t.row0 / PB);
     ks = (uint32_t)(t.row0 / SB);
     c += (int64_t)e * a.M * a.ldc;
