@@ -614,7 +614,7 @@ constexpr TileCost kCosts[] = {
     {kLds64x128, 64, 128, 1, {1.15f, 0.42f, 0.49f}, {1.44f, 0.65f, 0.60f}, 0.7f},
     {kLds128x128, 128, 128, 1, {1.85f, 0.78f, 0.75f}, {2.1f, 0.90f, 0.75f}, 1.1f},
     {k256x256, 256, 256, 1, {5.4f, 1.8f, 1.66f}, {4.25f, 1.6f, 1.1f}, 6.0f},    // rows
-    {k256x256, 256, 256, 1, {5.3f, 2.1f, 2.6f}, {5.3f, 2.1f, 2.6f}, 10.0f},     // wgrad
+    {k256x256, 256, 256, 1, {4.8f, 1.4f, 1.7f}, {4.8f, 1.4f, 1.7f}, 12.0f},     // wgrad
 };
 
 constexpr int kRows256 = 7;
@@ -626,11 +626,10 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 // of it in cache), plus 0.3 of the other two, which overlap it only in part.  The sizes of the groups are on the
 // device; their average and 0.6 tiles of padding each are taken; a 256 x 256
 // reduction starts and ends at whole 512-element periods (MX).  Against the best
-// kernel of each shape, over 183 shapes of 1 to 1,024 rows per expert, 4 to
+// kernel of each shape, over 210 shapes of 1 to 8,192 rows per expert, 2 to
 // 64 experts, N 256 to 28,672, all formats and both products: within 10% of it
-// in 160, within 28% in all; the 128 x 128 tile alone would
-// take 2 to 5 times as long for single tokens, the 16 x 128 tile 2 to 4 times for
-// 1,024 rows per expert.
+// in 184, within 28% in all; the 128 x 128 tile alone would take 2 to 5 times as
+// long for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per expert.
 template <int FMT>
 int pick(const GroupedArgs& a, bool wgrad) {
   if (!gl_fits<FMT>(a)) return !wgrad && a.M / a.experts <= 16 ? kDirect16x64 : kDirect64x64;
