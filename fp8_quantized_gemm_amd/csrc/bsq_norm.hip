@@ -209,13 +209,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, 4) void k_block_norm(NormFwd
 //   G = d_r + rs (a - rn m1),  m1 = mean(a rn)
 //   mean(G q) = mean(d_r q) + rs (mean(a q) - m1 mean(rn q)).
 template <typename T, bool AL, int TPR, int CH>
-__global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(NormBwd a) {
+__global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block_norm_bwd(NormBwd a) {
   constexpr int BT = TPR < 512 ? 512 : TPR, RPB = BT / TPR;
   __shared__ float red[2][4 * 16];
-  // CH 1: [8][BT], the fold over the row groups.  CH 2: the column sums themselves
+  // CH 1: [8][BT], the fold over the row groups.  CH 2: the columns' weights
   // ([2][CH][2][BT] of float4, a thread's own), whose registers would spill.
   extern __shared__ __attribute__((aligned(16))) float fold[];
-  float4* sums = reinterpret_cast<float4*>(fold);
+  float4* held = reinterpret_cast<float4*>(fold);
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
@@ -223,38 +223,37 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
   const T *d_r = static_cast<const T*>(a.d_r), *r = static_cast<const T*>(a.r);
   const uint16_t *d_h = static_cast<const uint16_t*>(a.d_h), *o = static_cast<const uint16_t*>(a.o);
   const uint16_t* gf = a.gate_kind == kGateFull ? static_cast<const uint16_t*>(a.gate) : nullptr;
+  // two ones: with more than one piece a missing full gate is all ones, because a
+  // choice per piece kept all pieces' gates unpacked (91 spilled registers)
+  constexpr uint32_t kOnes = 0x3F803F80u;
   const auto col = [&](int c) { return (c * TPR + t) * 8; };
-  // the columns' weights: in registers with one piece per thread, read again
-  // (from the L2) where they are used with two, whose registers would spill
-  float wq1[8], wp1[8], sp[8], st[8];
-  const auto load_sums = [&](int k, int c, float (&v)[8]) {
-    const float4 x = sums[((k * CH + c) * 2) * BT + threadIdx.x], y = sums[((k * CH + c) * 2 + 1) * BT + threadIdx.x];
+  // the columns' weights: in registers with one piece per thread, in LDS with two
+  float wq1[8], wp1[8], sp[CH][8], st[CH][8];
+  const auto hold = [&](int k, int c, const float (&v)[8]) {
+    held[((k * CH + c) * 2) * BT + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
+    held[((k * CH + c) * 2 + 1) * BT + threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
+  };
+  const auto take = [&](int k, int c, float (&v)[8]) {
+    const float4 x = held[((k * CH + c) * 2) * BT + threadIdx.x], y = held[((k * CH + c) * 2 + 1) * BT + threadIdx.x];
     v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
     v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
   };
-  const auto store_sums = [&](int k, int c, const float (&v)[8]) {
-    sums[((k * CH + c) * 2) * BT + threadIdx.x] = make_float4(v[0], v[1], v[2], v[3]);
-    sums[((k * CH + c) * 2 + 1) * BT + threadIdx.x] = make_float4(v[4], v[5], v[6], v[7]);
-  };
-  const auto weights = [&](int c, float (&wq)[8], float (&wp)[8]) {
-    load_w<AL>(a.w_post, col(c), cols, 1.0f, wq);
-    load_w<AL>(a.w_pre, col(c), cols, 0.0f, wp);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    load_w<AL>(a.w_post, col(c), cols, 1.0f, wq1);
+    load_w<AL>(a.w_pre, col(c), cols, 0.0f, wp1);
     if (a.gate_kind == kGateChannel) {
       float g[8];
       load_w<AL>(static_cast<const float*>(a.gate), col(c), cols, 1.0f, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) wq[j] *= g[j];
+      for (int j = 0; j < 8; ++j) wq1[j] *= g[j];
     }
-  };
-  if constexpr (CH == 1) weights(0, wq1, wp1);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) sp[j] = st[j] = 0.0f;
-  if constexpr (CH > 1) {
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      store_sums(0, c, sp);
-      store_sums(1, c, st);
+    if constexpr (CH > 1) {
+      hold(0, c, wq1);
+      hold(1, c, wp1);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sp[c][j] = st[c][j] = 0.0f;
   }
   int par = 0;
   const int64_t trips = (a.rows + RPB - 1) / RPB;
@@ -284,6 +283,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
       if (has_o) orow[c] = load_raw<AL>(o + base, col(c), cols);
       else orow[c].v[0] = u32x4{0u, 0u, 0u, 0u};
       if (gf) gr[c] = load_raw<AL>(gf + base, col(c), cols);
+      else if (CH > 1) gr[c].v[0] = u32x4{kOnes, kOnes, kOnes, kOnes};
     }
     const float rs = pre ? a.rstd_pre[rw] : 0.0f;
     const float rp = post ? a.rstd_post[rw] : 1.0f;
@@ -301,22 +301,22 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if constexpr (CH > 1) {
-        __builtin_amdgcn_sched_barrier(0);              // one piece at a time: fewer registers
-        weights(c, wq1, wp1);
-        load_sums(0, c, sp);
+        asm volatile("" ::: "memory");                   // one piece at a time: fewer registers
+        __builtin_amdgcn_sched_barrier(0);
+        take(0, c, wq1);
+        take(1, c, wp1);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float h = raw_at(dh[c], j), rn = raw_at(rr[c], j) * rs, av = h * wp1[j];
         float q = raw_at(orow[c], j) * rp * wq1[j];
-        if (gf) q *= raw_at(gr[c], j);
-        sp[j] = __builtin_fmaf(h * one, rn, sp[j]);
+        if (CH > 1 || gf) q *= raw_at(gr[c], j);
+        sp[c][j] = __builtin_fmaf(h * one, rn, sp[c][j]);
         s[0] = __builtin_fmaf(av, rn, s[0]);
         s[1] = __builtin_fmaf(raw_at(dr[c], j), q, s[1]);
         s[2] = __builtin_fmaf(av, q, s[2]);
         s[3] = __builtin_fmaf(rn, q, s[3]);
       }
-      if constexpr (CH > 1) store_sums(0, c, sp);
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -324,7 +324,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
       forget(rr[c]);
       forget(dh[c]);
       forget(orow[c]);
-      if (gf) forget(gr[c]);
+      if (CH > 1 || gf) forget(gr[c]);
     }
     group_sum<TPR, 4>(s, red[par]);
     const float m1 = s[0] * inv;
@@ -334,9 +334,10 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       if constexpr (CH > 1) {
+        asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        weights(c, wq1, wp1);
-        load_sums(1, c, st);
+        take(0, c, wq1);
+        take(1, c, wp1);
       }
       float y[8], z[8], dg[8];
 #pragma unroll
@@ -345,14 +346,13 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
         const float G = __builtin_fmaf(rs, __builtin_fmaf(-m1, rn, av), raw_at(dr[c], j));
         y[j] = has_o ? a.alpha * G : G;
         const float on = raw_at(orow[c], j) * rp;
-        const float g = gf ? raw_at(gr[c], j) : grow;
+        const float g = CH > 1 ? raw_at(gr[c], j) * grow : gf ? raw_at(gr[c], j) : grow;
         const float Gg = G * g;
-        st[j] = __builtin_fmaf(Gg * one, on, st[j]);
+        st[c][j] = __builtin_fmaf(Gg * one, on, st[c][j]);
         dg[j] = G * wq1[j] * on;                        // full gate
         z[j] = Gg * wq1[j];
         if (post) z[j] = rp * __builtin_fmaf(-m2, on, z[j]);
       }
-      if constexpr (CH > 1) store_sums(1, c, st);
       if (live) {
         store8<AL>(static_cast<T*>(a.d_x) + base, col(c), cols, y);
         if (has_o) store8<AL>(static_cast<uint16_t*>(a.d_o) + base, col(c), cols, z);
@@ -366,8 +366,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, 4) void k_block_norm_bwd(Nor
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       if (k == 0 ? !pre : !has_o) continue;
-      float (&v)[8] = k == 0 ? sp : st;
-      if constexpr (CH > 1) load_sums(k, c, v);
+      float (&v)[8] = k == 0 ? sp[c] : st[c];
       if constexpr (RPB > 1) {
         __syncthreads();
 #pragma unroll
@@ -416,7 +415,9 @@ __global__ __launch_bounds__(1024) void k_col_sum(const float* __restrict__ part
   }
 }
 
-// Threads per row and 8-column pieces per thread.
+// Threads per row and 8-column pieces per thread (the backward turns 1,024 x 2 into
+// 512 x 4, whose 256 registers per thread hold the column sums: 4,096 x 16,384,
+// BF16, 314 us -> 178 us).
 struct NormCfg {
   int tpr, ch;
 };
@@ -476,13 +477,13 @@ hipError_t pick_bwd(const NormBwd& a, unsigned grid, hipStream_t s) {
   if (c.tpr == 128) return run_bwd<T, AL, 128, 1>(a, grid, s);
   if (c.tpr == 256) return run_bwd<T, AL, 256, 1>(a, grid, s);
   if (c.tpr == 512) return run_bwd<T, AL, 512, 1>(a, grid, s);
-  return c.ch == 1 ? run_bwd<T, AL, 1024, 1>(a, grid, s) : run_bwd<T, AL, 1024, 2>(a, grid, s);
+  return c.ch == 1 ? run_bwd<T, AL, 1024, 1>(a, grid, s) : run_bwd<T, AL, 512, 4>(a, grid, s);
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Workgroups of the backward pass: at most 512 (two per compute unit of the
-// 256; one where the column sums fill its LDS), so that the partial column sums
+// 256; one where the weights fill its LDS), so that the partial column sums
 // stay small next to the tensors.
 unsigned bwd_grid(int64_t rows, int64_t cols) {
   const NormCfg c = norm_cfg(cols);

@@ -76,6 +76,9 @@ CASES = [  # rows, cols, residual, gate, post, pre, o
     (40, 1024, "bf16", "channel", True, True, True),
     (21, 8192, "f32", "full", True, True, True),
     (19, 12000, "bf16", "row", True, True, True),
+    (600, 9000, "f32", "channel", True, True, True),
+    (530, 16384, "bf16", "full", True, True, True),
+    (300, 8203, "bf16", None, False, True, True),
 ]
 
 
