@@ -139,22 +139,22 @@ def _check_amax(*amaxes):
             raise ValueError("amax arguments must be float32 tensors of at least one element")
 
 
-def _check_operand(what, codes, scales, K, fmt):
+def _check_operand(what, codes, scales, K, fmt, dim=2):
     """codes (uint8 [rows, K / elements-per-byte]) and scales (uint8 [rows, K /
-    block], None for per-tensor FP8) of one K-major GEMM operand.  The library
-    takes the row strides from K, so the widths must match exactly."""
+    block], None for per-tensor FP8) of one K-major GEMM operand (dim 3: of stacked
+    ones).  The library takes the row strides from K, so the widths must match
+    exactly."""
     per_byte = 1 if fmt in ("mxfp8", "fp8") else 2
     blk = {"nvfp4": 16, "mxfp4": 32, "mxfp8": 32, "fp8": None}[fmt]
-    if not (isinstance(codes, torch.Tensor) and codes.dtype == torch.uint8 and codes.dim() == 2):
-        raise ValueError(f"{what} codes must be a 2-D uint8 tensor")
-    if K < 0 or K % per_byte or codes.shape[1] != K // per_byte:
-        raise ValueError(f"{what} codes are [{codes.shape[0]}, {codes.shape[1]}]; "
-                         f"K = {K} needs [rows, {K // per_byte}]")
+    if not (isinstance(codes, torch.Tensor) and codes.dtype == torch.uint8 and codes.dim() == dim):
+        raise ValueError(f"{what} codes must be a {dim}-D uint8 tensor")
+    if K < 0 or K % per_byte or codes.shape[-1] != K // per_byte:
+        raise ValueError(f"{what} codes are {list(codes.shape)}; K = {K} needs rows of {K // per_byte}")
     if blk is None:
         return
-    if not (isinstance(scales, torch.Tensor) and scales.dtype == torch.uint8 and scales.dim() == 2
-            and scales.shape[0] == codes.shape[0] and scales.shape[1] == K // blk):
-        raise ValueError(f"{what} scales must be uint8 [{codes.shape[0]}, {K // blk}]")
+    if not (isinstance(scales, torch.Tensor) and scales.dtype == torch.uint8 and scales.dim() == dim
+            and scales.shape[:-1] == codes.shape[:-1] and scales.shape[-1] == K // blk):
+        raise ValueError(f"{what} scales must be uint8 {list(codes.shape[:-1]) + [K // blk]}")
 
 
 def _check_out(out, M, N, dtype):
@@ -459,7 +459,7 @@ def _check_like(t, what, shape, dtype, device):
     """None, or a contiguous copy of a tensor that must have this shape, type and device."""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and tuple(t.shape) == tuple(shape)
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
             and t.device == device):
         raise ValueError(f"{what} must be a {dtype} {list(shape)} tensor on {device}")
     return t.contiguous()
@@ -495,7 +495,7 @@ def block_norm(x, o=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-
     w_post = _check_like(w_post, "w_post", (C,), torch.float32, dev)
     kind, gate = _check_gate(gate, R, C, dev)
     r = torch.empty_like(x) if o is not None else None
-    h = torch.empty((R, C), dtype=torch.bfloat16, device=dev) if w_pre is not None else None
+    h = torch.empty(R, C, dtype=torch.bfloat16, device=dev) if w_pre is not None else None
     f32 = lambda n: torch.empty(n, dtype=torch.float32, device=dev)
     rq = f32(R) if w_post is not None else None
     rp = f32(R) if w_pre is not None else None
@@ -573,9 +573,9 @@ def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0
     bias = _check_like(bias, "bias", (E,), torch.float32, dev)
     sc, rows = _scoring(scoring), moe_rows(T, E, k, align)
     need = _size("moe_route_workspace", T, E, k)
-    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=dev)
+    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)
     ids, row_of, off, src = i32(T, k), i32(T, k), i32(E + 1), i32(rows)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
+    w = torch.empty(T, k, dtype=torch.float32, device=dev)
     ws = i32(need // 4) if need else None
     st = lib().moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
                          1 if normalize else 0, float(scale), int(align), rows, _ptr(ids), _ptr(w), _ptr(off),
@@ -616,7 +616,7 @@ def moe_gather(x, src, k, out=None):
     T, C = x.shape
     src = _check_index(src, "src", 1, x.device)
     if out is None:
-        out = torch.empty((src.shape[0], C), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty(src.shape[0], C, dtype=torch.bfloat16, device=x.device)
     else:
         _check_out(out, src.shape[0], C, torch.bfloat16)
     _check_device(x, src, out)
@@ -634,7 +634,7 @@ def moe_combine(y, row_of, weights=None, out=None):
     T, k = row_of.shape
     weights = _check_like(weights, "weights", (T, k), torch.float32, y.device)
     if out is None:
-        out = torch.empty((T, C), dtype=torch.bfloat16, device=y.device)
+        out = torch.empty(T, C, dtype=torch.bfloat16, device=y.device)
     else:
         _check_out(out, T, C, torch.bfloat16)
     _check_device(y, row_of, out)
@@ -690,7 +690,7 @@ def bs_gemm_grouped(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=N
     _check_device(a_codes, a_scales, b_codes, b_scales, offsets, a_amax, b_amax, out=out)
     K = a_codes.shape[1] * (1 if fmt == "mxfp8" else 2)
     _check_operand("A", a_codes, a_scales, K, fmt)
-    _check_operand("B", b_codes.flatten(0, 1), b_scales.flatten(0, 1), K, fmt)
+    _check_operand("B", b_codes, b_scales, K, fmt, 3)
     if fmt == "nvfp4" and (a_amax is None or b_amax is None):
         raise ValueError("nvfp4 needs both per-tensor amaxes")
     _check_amax(a_amax, b_amax)
@@ -701,7 +701,7 @@ def bs_gemm_grouped(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=N
             raise ValueError(f"b_amax must have 1 or {E} elements")
     M, N = a_codes.shape[0], b_codes.shape[1]
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a_codes.device)
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=a_codes.device)
     else:
         _check_out(out, M, N, torch.bfloat16)
     st = lib().bs_gemm_grouped(FORMATS[fmt], E, _ptr(offsets), M, N, K, _ptr(a_codes), _ptr(a_scales),
@@ -731,7 +731,7 @@ def bs_gemm_grouped_wgrad(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_
     _check_amax(a_amax, b_amax)
     M, N = a_codes.shape[0], b_codes.shape[0]
     if out is None:
-        out = torch.empty((E, M, N), dtype=torch.bfloat16, device=a_codes.device)
+        out = torch.empty(E, M, N, dtype=torch.bfloat16, device=a_codes.device)
     elif not (out.dtype == torch.bfloat16 and tuple(out.shape) == (E, M, N)):
         raise ValueError(f"out must be a bfloat16 [{E}, {M}, {N}] tensor")
     _check_device(a_codes, out)
