@@ -249,6 +249,32 @@ def test_wgrad(fmt, dyadic, blocks, past, M, N):
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
+@pytest.mark.parametrize("sizes,N,K", [((2, 1, 3), 100, 160), ((40, 30, 50), 260, 512), ((300, 200, 520), 520, 1024)])
+def test_rows_of_a_group_do_not_see_its_neighbours_nan(fmt, sizes, N, K):
+    """NaN scales in one group's rows, or in one expert's weights, stay there."""
+    announce("bs_gemm_grouped, NaN in one group", fmt, sizes, N, K)
+    rng = np.random.default_rng(22)
+    E, R = len(sizes), sum(sizes) + 5
+    o = np.concatenate([[0], np.cumsum(sizes)])
+    a, b = _operand(rng, R, K, fmt, False), _operand(rng, E * N, K, fmt, False)
+    am = torch.tensor([3.0], device="cuda") if fmt == "nvfp4" else None
+    run = lambda a, b: bsq.bs_gemm_grouped(fmt, *_dev(*a), *(t.view(E, N, -1) for t in _dev(*b)), _offsets(sizes), am, am)
+    want = run(a, b)
+    assert torch.isfinite(want).all()
+    nan = 0x7F if fmt == "nvfp4" else 0xFF
+    for bad in range(E):
+        for which in (0, 1):
+            ops = [list(a), list(b)]
+            ops[which][1] = ops[which][1].copy()
+            rows = slice(o[bad], o[bad + 1]) if which == 0 else slice(bad * N, bad * N + N)
+            ops[which][1][rows] = nan
+            got = run(*ops)
+            keep = torch.ones(R, dtype=torch.bool, device="cuda")
+            keep[o[bad]:o[bad + 1]] = False
+            assert torch.equal(got[keep], want[keep]) and torch.isnan(got[~keep]).all(), (bad, which)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4", "mxfp8"])
 @pytest.mark.parametrize("blocks,M,N", [((3, 4, 2), 40, 30), ((5, 9, 30), 128, 200), ((41, 3, 70), 300, 257),
                                         ((60, 10, 60), 1024, 1500)])
 def test_wgrad_of_a_group_does_not_see_its_neighbours_nan(fmt, blocks, M, N):
