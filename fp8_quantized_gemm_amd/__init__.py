@@ -497,9 +497,12 @@ def block_norm(x, o=None, w_pre=None, w_post=None, gate=None, alpha=1.0, eps=1e-
     r = torch.empty_like(x) if o is not None else None
     h = torch.empty(R, C, dtype=torch.bfloat16, device=dev) if w_pre is not None else None
     f32 = lambda n: torch.empty(n, dtype=torch.float32, device=dev)
-    rq = f32(R) if w_post is not None else None
-    rp = f32(R) if w_pre is not None else None
-    am = f32(1) if amax and w_pre is not None else None
+    if w_post is not None and w_pre is not None and amax:
+        rq, rp, am = f32(2 * R + 1).split_with_sizes((R, R, 1))    # one allocation: 1 us less
+    else:
+        rq = f32(R) if w_post is not None else None
+        rp = f32(R) if w_pre is not None else None
+        am = f32(1) if amax and w_pre is not None else None
     st = lib().block_norm(_ptr(x), int(x.dtype == torch.float32), _ptr(o), R, C, _ptr(w_post), kind,
                           _ptr(gate), float(alpha), _ptr(w_pre), float(eps), _ptr(r), _ptr(h), _ptr(rq),
                           _ptr(rp), _ptr(am), _stream(dev))
@@ -573,8 +576,9 @@ def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0
     bias = _check_like(bias, "bias", (E,), torch.float32, dev)
     sc, rows = _scoring(scoring), moe_rows(T, E, k, align)
     need = _size("moe_route_workspace", T, E, k)
-    i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)
-    ids, row_of, off, src = i32(T, k), i32(T, k), i32(E + 1), i32(rows)
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+    ids, row_of, off, src = i32(2 * T * k + E + 1 + rows).split_with_sizes((T * k, T * k, E + 1, rows))
+    ids, row_of = ids.view(T, k), row_of.view(T, k)
     w = torch.empty(T, k, dtype=torch.float32, device=dev)
     ws = i32(need // 4) if need else None
     st = lib().moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
