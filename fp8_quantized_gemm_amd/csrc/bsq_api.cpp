@@ -23,7 +23,10 @@ hipError_t set_lds_limit(const void* fn, int bytes) {
   const auto it = done.find(key);
   if (it != done.end()) return it->second;
   const hipError_t r = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  done.emplace(key, r);
+  try {
+    done.emplace(key, r);
+  } catch (...) {   // no host memory to remember it: set again by the next call (nothing is thrown through the C entry)
+  }
   return r;
 }
 
