@@ -628,8 +628,10 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 // reduction starts and ends at whole 512-element periods (MX).  Against the best
 // kernel of each shape, over 210 shapes of 1 to 8,192 rows per expert, 2 to
 // 64 experts, N 256 to 28,672, all formats and both products: within 10% of it
-// in 184, within 28% in all; the 128 x 128 tile alone would take 2 to 5 times as
-// long for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per expert.
+// in 184, within 28% in all, and within 10% in 86 of 90 random shapes that no
+// constant was chosen by (36% at most; constants fitted more closely to the 210
+// did worse on these).  The 128 x 128 tile alone would take 2 to 5 times as long
+// for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per expert.
 template <int FMT>
 int pick(const GroupedArgs& a, bool wgrad) {
   if (!gl_fits<FMT>(a)) return !wgrad && a.M / a.experts <= 16 ? kDirect16x64 : kDirect64x64;
