@@ -3,8 +3,9 @@
 Usage: python -m fp8_quantized_gemm_amd._build   (or __graft_entry__.build()).
 Each translation unit is compiled to an object under _build/ in parallel,
 then linked into fp8_quantized_gemm_amd/libbsq.so.  The measurement kernels
-of the two GEMM routes' inner-loop ceilings go into a library of their own,
-libbsq_ceiling.so, so the product ABI stays what include/bsq.h declares.
+of the two GEMM routes' inner-loop ceilings, and the entry that runs a grouped
+product on a chosen kernel (linked against libbsq.so), go into a library of their
+own, libbsq_ceiling.so, so the product ABI stays what include/bsq.h declares.
 """
 
 import os
@@ -24,7 +25,7 @@ CEILING_LIB = os.path.join(PKG, "libbsq_ceiling.so")
 SOURCES = ["bsq_api.cpp", "bsq_quantize.hip", "bsq_gemm.hip", "bsq_gemm_nvfp4.hip",
            "bsq_gemm_nvfp4_rx.hip", "bsq_gemm_mx_rx.hip", "bsq_norm.hip", "bsq_moe.hip",
            "bsq_gemm_grouped.hip"]
-CEILING_SOURCES = ["route_a_ceiling.hip"]
+CEILING_SOURCES = ["route_a_ceiling.hip", "grouped_kernels.cpp"]
 
 ARCH = "gfx950"
 FLAGS = [
@@ -56,9 +57,9 @@ def _compile(src):
     return obj, "\n".join(warn)
 
 
-def _link(objs, out):
+def _link(objs, out, extra=()):
     tmp = out + ".tmp"
-    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
+    cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs + list(extra)
     r = subprocess.run(cmd, capture_output=True, text=True, cwd=BUILD)
     if r.returncode != 0:
         raise RuntimeError(f"link of {os.path.basename(out)} failed:\n{r.stdout}\n{r.stderr}")
@@ -75,7 +76,8 @@ def build(verbose=True):
             print(f"[bsq build] {s}:\n{w}", file=sys.stderr)
     objs = dict(zip(srcs, (o for o, _ in results)))
     _link([objs[s] for s in SOURCES], LIB)
-    _link([objs[s] for s in CEILING_SOURCES], CEILING_LIB)
+    _link([objs[s] for s in CEILING_SOURCES], CEILING_LIB,
+          [f"-L{PKG}", "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"])
     if verbose:
         print(f"[bsq build] wrote {LIB} and {CEILING_LIB}", file=sys.stderr)
     return LIB

@@ -564,19 +564,6 @@ hipError_t run_rx(const GroupedArgs& a, bool wgrad, hipStream_t s) {
   return FMT == kNVFP4 ? launch_gemm_nvfp4_rx_grouped(a, wgrad, s) : launch_gemm_mx_rx_grouped(a, wgrad, s);
 }
 
-// The kernels to choose from, by output tile.
-enum Variant {
-  kDirect16x64,            // direct loads, K over four waves: any alignment
-  kDirect64x64,
-  kDirect16x32,            // direct loads, K over eight waves: few tiles and a long K
-  kLds16x128,
-  kLds32x128,
-  kLds64x64,
-  kLds64x128,
-  kLds128x128,
-  k256x256
-};
-
 template <int FMT, bool WGRAD>
 hipError_t run_variant(const GroupedArgs& a, int v, hipStream_t s) {
   if (v == k256x256) return run_rx<FMT>(a, WGRAD, s);
@@ -677,7 +664,32 @@ hipError_t run_any(const GroupedArgs& a, bool wgrad, hipStream_t s) {
   return run_picked<kMXFP8>(a, wgrad, s);
 }
 
+// Whether kernel v is one of those that compute this product of these operands.
+template <int FMT>
+bool takes(const GroupedArgs& a, bool wgrad, int v) {
+  if (v < kDirect16x64 || v > k256x256) return false;
+  if (wgrad && v < kLds64x64 && v != kDirect64x64) return false;
+  if (v == k256x256) return rx_fits<FMT>(a, wgrad);
+  return v < kLds16x128 ? narrow(a) : gl_fits<FMT>(a);
+}
+
+template <int FMT>
+hipError_t run_on(const GroupedArgs& a, bool wgrad, int v, hipStream_t s) {
+  if (!takes<FMT>(a, wgrad, v)) return hipErrorInvalidValue;
+  return wgrad ? run_variant<FMT, true>(a, v, s) : run_variant<FMT, false>(a, v, s);
+}
+
 }  // namespace
+
+int grouped_kernel(const GroupedArgs& a, bool wgrad) {
+  if (a.fmt == kNVFP4) return pick<kNVFP4>(a, wgrad);
+  return a.fmt == kMXFP4 ? pick<kMXFP4>(a, wgrad) : pick<kMXFP8>(a, wgrad);
+}
+
+hipError_t launch_gemm_grouped_on(const GroupedArgs& a, bool wgrad, int kernel, hipStream_t s) {
+  if (a.fmt == kNVFP4) return run_on<kNVFP4>(a, wgrad, kernel, s);
+  return a.fmt == kMXFP4 ? run_on<kMXFP4>(a, wgrad, kernel, s) : run_on<kMXFP8>(a, wgrad, kernel, s);
+}
 
 hipError_t launch_gemm_grouped(const GroupedArgs& a, hipStream_t s) { return run_any(a, false, s); }
 hipError_t launch_gemm_grouped_wgrad(const GroupedArgs& a, hipStream_t s) { return run_any(a, true, s); }

@@ -230,6 +230,23 @@ struct GroupedArgs {
   void* c;                        // rows: [M, N]; wgrad: [experts][M, N]
   int64_t ldc;
 };
+// The kernels of the grouped products, by output tile.
+enum GroupedKernel {
+  kDirect16x64,            // direct loads, K over four waves: any alignment
+  kDirect64x64,
+  kDirect16x32,            // direct loads, K over eight waves: few tiles and a long K
+  kLds16x128,
+  kLds32x128,
+  kLds64x64,
+  kLds64x128,
+  kLds128x128,
+  k256x256
+};
+// The kernel the launches below choose for these sizes and alignments, and a launch
+// on a given one (hipErrorInvalidValue where it does not take these operands): for
+// the tests and measurements of each kernel.
+int grouped_kernel(const GroupedArgs& a, bool wgrad);
+hipError_t launch_gemm_grouped_on(const GroupedArgs& a, bool wgrad, int kernel, hipStream_t s);
 // C rows of group e = alpha A rows . B_e^T; rows of no group are zeroed.
 hipError_t launch_gemm_grouped(const GroupedArgs& a, hipStream_t s);
 // C_e = alpha A[:, group e] . B[:, group e]^T.

@@ -1,0 +1,215 @@
+"""Every kernel of the expert-grouped products by itself, against the oracle: the
+library chooses by size, so each one is run here through the measurement library's
+entry (libbsq's own launches) on ragged, empty and unassigned groups.  With dyadic
+operands every FP32 partial sum is exact and the result must be the RNE of the
+float64 one bit for bit; random operands use the GEMMs' stated tolerance."""
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_quantized_gemm_amd as bsq
+from oracle import gemm as OG
+from oracle import moe as OM
+
+from _gpu import announce, gpu
+from test_gpu_grouped import BLK, _deq, _dev, _judge, _offsets, _operand
+
+pytestmark = gpu
+
+NAMES = ("direct 16x64", "direct 64x64", "direct 16x32", "lds 16x128", "lds 32x128", "lds 64x64", "lds 64x128",
+         "lds 128x128", "256x256")
+WGRAD_NAMES = ("direct 64x64", "lds 64x64", "lds 64x128", "lds 128x128", "256x256")
+FMTS = ("nvfp4", "mxfp4", "mxfp8")
+
+
+def grouped_on(name, wgrad, fmt, a, b, offsets, aa=None, ba=None, out=None):
+    """bs_gemm_grouped[_wgrad] on the named kernel (None: the number of the chosen one)."""
+    L = ctypes.CDLL(os.path.join(os.path.dirname(bsq.LIB_PATH), "libbsq_ceiling.so"))
+    P, I, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    L.bsq_grouped_on.argtypes = [I, I, I, I, P, I64, I64, I64, P, P, P, P, P, P, I, P, I64, P]
+    E, K = len(offsets) - 1, a[0].shape[1] * (1 if fmt == "mxfp8" else 2)
+    M, N = a[0].shape[0], b[0].shape[-2]
+    if out is None:
+        out = torch.full((E, M, N) if wgrad else (M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    p = lambda t: None if t is None else t.data_ptr()
+    v = -1 if name is None else NAMES.index(name)
+    rc = L.bsq_grouped_on(v, int(wgrad), bsq.FORMATS[fmt], E, p(offsets), M, N, K, p(a[0]), p(a[1]), p(aa), p(b[0]),
+                          p(b[1]), p(ba), 1 if ba is None else ba.numel(), p(out), N if wgrad else out.stride(0),
+                          torch.cuda.current_stream().cuda_stream)
+    if name is None:
+        return rc
+    assert rc == 0, (name, rc)
+    return out
+
+
+ROWS = [  # sizes, rows past the last group, N, K
+    ([64, 1, 129, 0, 63], 7, 257, 512),
+    ([257, 0, 511, 256, 3], 100, 520, 1024),
+    ([1, 300], 0, 33, 1536),
+]
+
+
+def _rows_case(fmt, dyadic, sizes, past, N, K, seed=0):
+    rng = np.random.default_rng(seed + N + K)
+    E, R = len(sizes), sum(sizes) + past
+    ac, asc = _operand(rng, R, K, fmt, dyadic)
+    bc, bsc = _operand(rng, E * N, K, fmt, dyadic)
+    am = np.array([2688.0], np.float32)
+    bm = np.array([2688.0 * 2.0 ** (e % 3) for e in range(E)], np.float32) if dyadic else rng.uniform(1, 9, E).astype(np.float32)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    want, _ = OM.grouped(_deq(ac, asc, fmt), _deq(bc, bsc, fmt).reshape(E, N, K), off)
+    if fmt == "nvfp4":
+        for e in range(E):
+            want[off[e]:off[e + 1]] *= OG.nvfp4_alpha(am[0], bm[e])
+    ta, tb = _dev(am, bm) if fmt == "nvfp4" else (None, None)
+    return _dev(ac, asc), _dev(bc.reshape(E, N, -1), bsc.reshape(E, N, -1)), ta, tb, want
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dyadic", [True, False])
+@pytest.mark.parametrize("sizes,past,N,K", ROWS)
+def test_rows(name, fmt, dyadic, sizes, past, N, K):
+    announce("grouped rows on", name, fmt, dyadic, sizes, past, N, K)
+    a, b, ta, tb, want = _rows_case(fmt, dyadic, sizes, past, N, K)
+    out = torch.full((len(want), N + 3), 7.0, dtype=torch.bfloat16, device="cuda")
+    grouped_on(name, False, fmt, a, b, _offsets(sizes), ta, tb, out[:, :N])
+    _judge(out[:, :N], want, dyadic, (name, fmt, sizes, N, K))
+    assert torch.all(out[:, N:] == 7), "wrote past the columns"
+    whole = grouped_on(name, False, fmt, a, b, _offsets(sizes), ta, tb)
+    assert torch.equal(whole, out[:, :N].contiguous())
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_whole_pieces_and_one_amax(name, fmt):
+    """N % 8 == 0: the stores of whole 16-byte pieces; one amax for all experts."""
+    announce("grouped rows on", name, fmt, "whole pieces")
+    sizes, N, K = [70, 0, 330], 264, 512
+    a, b, ta, _, _ = _rows_case(fmt, True, sizes, 3, N, K, 5)
+    off = np.concatenate([[0], np.cumsum(sizes)])
+    want, _ = OM.grouped(_deq(*(t.cpu().numpy() for t in a), fmt),
+                         np.stack([_deq(*(t[e].cpu().numpy() for t in b), fmt) for e in range(3)]), off)
+    _judge(grouped_on(name, False, fmt, a, b, _offsets(sizes), ta, ta), want, True, (name, fmt))
+
+
+# groups in scale blocks of 16 (NVFP4) or 32 rows: starts and ends inside a K step,
+# a pair and a period of every kernel; blocks past the last group
+WGRAD = [
+    ([3, 0, 5, 1, 40], 15, 100, 130),
+    ([17, 15, 33, 31, 64, 0, 1, 95], 0, 260, 300),
+    ([1, 30, 0, 1], 0, 257, 64),
+]
+
+
+def _wgrad_case(fmt, dyadic, blocks, past, M, N):
+    rng = np.random.default_rng(len(blocks) * 10 + M + N)
+    B = BLK[fmt]
+    sizes = [v * B for v in blocks]
+    R = -(-(sum(sizes) + past * B) // 512) * 512             # whole periods, so that every kernel takes them
+    a, b = _operand(rng, M, R, fmt, dyadic), _operand(rng, N, R, fmt, dyadic)
+    am, bm = np.float32(2688.0), np.float32(1344.0 if dyadic else 5.0)
+    want, _ = OM.grouped_wgrad(_deq(*a, fmt), _deq(*b, fmt), np.concatenate([[0], np.cumsum(sizes)]))
+    ta = tb = None
+    if fmt == "nvfp4":
+        want *= OG.nvfp4_alpha(am, bm)
+        ta, tb = torch.tensor([am], device="cuda"), torch.tensor([bm], device="cuda")
+    return _dev(*a), _dev(*b), sizes, ta, tb, want
+
+
+@pytest.mark.parametrize("name", WGRAD_NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dyadic", [True, False])
+@pytest.mark.parametrize("blocks,past,M,N", WGRAD)
+def test_wgrad(name, fmt, dyadic, blocks, past, M, N):
+    announce("grouped wgrad on", name, fmt, dyadic, blocks, past, M, N)
+    a, b, sizes, ta, tb, want = _wgrad_case(fmt, dyadic, blocks, past, M, N)
+    got = grouped_on(name, True, fmt, a, b, _offsets(sizes), ta, tb)
+    for e in range(len(blocks)):
+        _judge(got[e], want[e], dyadic, (name, fmt, blocks, M, N, e))
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_nan_stays_in_its_group(name, fmt):
+    announce("grouped rows, NaN in one group, on", name, fmt)
+    sizes, N, K = (40, 3, 270), 130, 512
+    E, R, o = 3, sum(sizes) + 5, np.concatenate([[0], np.cumsum(sizes)])
+    a, b, ta, tb, _ = _rows_case(fmt, False, sizes, 5, N, K, 22)
+    run = lambda a, b: grouped_on(name, False, fmt, a, b, _offsets(sizes), ta, tb)
+    want = run(a, b)
+    assert torch.isfinite(want).all()
+    nan = 0x7F if fmt == "nvfp4" else 0xFF
+    for bad in range(E):
+        for which in (0, 1):
+            sc = [a[1].clone(), b[1].clone()]
+            if which == 0:
+                sc[0][o[bad]:o[bad + 1]] = nan
+            else:
+                sc[1][bad] = nan
+            got = run((a[0], sc[0]), (b[0], sc[1]))
+            keep = torch.ones(R, dtype=torch.bool, device="cuda")
+            keep[o[bad]:o[bad + 1]] = False
+            assert torch.equal(got[keep], want[keep]) and torch.isnan(got[~keep]).all(), (bad, which)
+
+
+@pytest.mark.parametrize("name", WGRAD_NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wgrad_nan_stays_in_its_group(name, fmt):
+    announce("grouped wgrad, NaN in one group, on", name, fmt)
+    blocks, M, N = (3, 21, 40), 130, 257
+    B, per = BLK[fmt], 1 if fmt == "mxfp8" else 2
+    a, b, sizes, ta, tb, _ = _wgrad_case(fmt, False, blocks, 2, M, N)
+    o = np.concatenate([[0], np.cumsum(sizes)])
+    K = a[0].shape[1] * per
+    run = lambda a, b: grouped_on(name, True, fmt, a, b, _offsets(sizes), ta, tb)
+    want = run(a, b)
+    assert torch.isfinite(want).all()
+    for bad in range(-1, len(blocks)):                       # -1: the rows past the last group
+        k0, k1 = (o[bad], o[bad + 1]) if bad >= 0 else (o[-1], K)
+        for which in (1, 2, 3):
+            ops = []
+            for i, (codes, scales) in enumerate((a, b)):
+                codes, scales = codes.clone(), scales.clone()
+                if which >> i & 1:
+                    scales[:, k0 // B:k1 // B] = 0x7F if fmt == "nvfp4" else 0xFF
+                    if fmt == "mxfp8":
+                        codes[:, k0:k1] = 0x7F
+                ops.append((codes, scales))
+            got = run(*ops)
+            for e in range(len(blocks)):
+                if e != bad:
+                    assert torch.equal(got[e], want[e]), (bad, which, e)
+                else:
+                    assert torch.isnan(got[e]).all(), (bad, which, e)
+
+
+def _chosen(wgrad, fmt, E, rows, N, K):
+    """The kernel of these sizes (rows spread evenly; nothing is computed)."""
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    z = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    per, B = (1 if fmt == "mxfp8" else 2), BLK[fmt]
+    v = lambda *s: z.as_strided(s, (0,) * len(s))            # shapes and an aligned address only
+    if wgrad:
+        return NAMES[grouped_on(None, True, fmt, (v(N, rows // per), v(N, rows // B)), (v(K, rows // per), v(K, rows // B)), off,
+                                out=v(1, 1))]
+    return NAMES[grouped_on(None, False, fmt, (v(rows, K // per), v(rows, K // B)), (v(E, N, K // per), v(E, N, K // B)), off,
+                            out=v(1, 1))]
+
+
+def test_every_kernel_is_chosen_somewhere():
+    """... by the library's own rule, at sizes of use: single tokens to training batches."""
+    announce("the choice of grouped kernel")
+    rows, wgrad = set(), set()
+    for fmt in FMTS:
+        for E in (2, 8, 64):
+            for per in (1, 4, 16, 48, 128, 400, 2048):
+                for N, K in ((256, 14336), (2048, 1408), (4096, 4096), (28672, 4096), (512, 512), (300, 96)):
+                    rows.add(_chosen(False, fmt, E, per * E, N, K))
+                    wgrad.add(_chosen(True, fmt, E, -(-per * E // 512) * 512, N, K))
+        wgrad.add(_chosen(True, fmt, 4, 96, 256, 256))
+    assert rows == set(NAMES) and wgrad == set(WGRAD_NAMES), (rows, wgrad)
