@@ -229,11 +229,13 @@ __device__ __forceinline__ void gs_store(const floatx4 (&acc)[MI][NI], uint8_t* 
   }
 }
 
-// alpha of an NVFP4 product with expert e's B (1 for MX).
+// alpha of an NVFP4 product with expert e's B (1 for MX).  A tile without a
+// reduction (the rows of no group, an empty group) is stored as exact zeros: 0
+// whatever the amaxes say, whose decode scales can be infinite or NaN.
 template <int FMT>
-__device__ __forceinline__ float gs_alpha(const GroupedArgs& a, int e) {
+__device__ __forceinline__ float gs_alpha(const GroupedArgs& a, int e, bool any) {
   if constexpr (FMT != kNVFP4) return 1.0f;
-  return nvfp4_s_dec(*a.aa) * nvfp4_s_dec(a.ba[a.ba_n > 1 && e > 0 ? e : 0]) * 16384.0f;
+  return any ? nvfp4_s_dec(*a.aa) * nvfp4_s_dec(a.ba[a.ba_n > 1 ? e : 0]) * 16384.0f : 0.0f;
 }
 
 // OFF: type of the lanes' byte offsets from the tile's first row (32 bits
@@ -346,8 +348,8 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_gemm_grouped(GroupedArgs 
     gs_multiply<FMT, MI, NI>(fa[0], fb[0], acc);
   }
 
-  gs_store<MI, NI, WM, WN, WK>(acc, smem, wk, wm, wn, gs_alpha<FMT>(a, e), c + m0 * a.ldc + n0, a.ldc, last_m, last_n,
-                               vec_store);
+  gs_store<MI, NI, WM, WN, WK>(acc, smem, wk, wm, wn, gs_alpha<FMT>(a, e, klen > 0), c + m0 * a.ldc + n0, a.ldc, last_m,
+                               last_n, vec_store);
 }
 
 // ---------------------------------------------------------------- LDS-staged kernel
@@ -509,8 +511,7 @@ __global__ __launch_bounds__(kGlThreads, NB == 1 ? 3 : 2) void k_gemm_grouped_ld
     gs_multiply<FMT, MI, NI>(fa, fb, acc);
   }
   lds_barrier();                                           // every wave is done with the buffers
-  gs_store<MI, NI, WM, WN, 1>(acc, smem, 0, wm, wn, gs_alpha<FMT>(a, e), c, a.ldc, last_m, last_n,
-                            vec_store);
+  gs_store<MI, NI, WM, WN, 1>(acc, smem, 0, wm, wn, gs_alpha<FMT>(a, e, steps > 0), c, a.ldc, last_m, last_n, vec_store);
 }
 
 // Whole dwords of scales per step and 16-byte aligned code rows; 32-bit offsets

@@ -213,3 +213,50 @@ def test_every_kernel_is_chosen_somewhere():
                     wgrad.add(_chosen(True, fmt, E, -(-per * E // 512) * 512, N, K))
         wgrad.add(_chosen(True, fmt, 4, 96, 256, 256))
     assert rows == set(NAMES) and wgrad == set(WGRAD_NAMES), (rows, wgrad)
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("amax", [float("inf"), float("nan"), 0.0])
+def test_rows_of_no_group_are_zero_whatever_the_amax(name, amax):
+    """Rows past the last group are zeros, not 0 times an infinite decode scale, and
+    no expert's amax reaches rows that are not its own."""
+    announce("grouped rows, amax", amax, "on", name)
+    sizes, N, K = (0, 20, 5), 130, 512
+    a, b, ta, tb, _ = _rows_case("nvfp4", False, sizes, 40, N, K, 31)
+    want = grouped_on(name, False, "nvfp4", a, b, _offsets(sizes), ta, tb)
+    tb[0] = amax                                             # an expert without rows
+    got = grouped_on(name, False, "nvfp4", a, b, _offsets(sizes), ta, tb)
+    assert torch.equal(got, want) and torch.isfinite(want).all() and not want[25:].any()
+    for bad in (ta, tb):                                     # everything that has a scale has this one
+        bad.fill_(amax)
+    got = grouped_on(name, False, "nvfp4", a, b, _offsets(sizes), ta, tb)
+    assert not got[25:].any()
+    if amax == float("inf"):                                 # its decode scale is infinite: the test tells
+        assert not torch.isfinite(got[:25]).any()
+
+
+@pytest.mark.parametrize("name", WGRAD_NAMES)
+@pytest.mark.parametrize("amax", [float("inf"), float("nan")])
+def test_wgrad_of_an_empty_group_is_zero_whatever_the_amax(name, amax):
+    announce("grouped wgrad, amax", amax, "on", name)
+    a, b, sizes, ta, tb, _ = _wgrad_case("nvfp4", False, (0, 5, 0, 30), 1, 130, 70)
+    for bad in (ta, tb):
+        keep = bad.clone()
+        bad.fill_(amax)
+        got = grouped_on(name, True, "nvfp4", a, b, _offsets(sizes), ta, tb)
+        assert not got[0].any() and not got[2].any()
+        if amax == float("inf"):
+            assert not torch.isfinite(got[1]).any()
+        bad.copy_(keep)
+
+
+@pytest.mark.parametrize("amax", [float("inf"), float("nan")])
+def test_products_without_a_reduction_are_zero_whatever_the_amax(amax):
+    announce("grouped products without a reduction, amax", amax)
+    z = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    bad = torch.tensor([amax], device="cuda")
+    out = torch.full((5, 9), 3.0, dtype=torch.bfloat16, device="cuda")
+    bsq.bs_gemm_grouped("nvfp4", z(5, 0), z(5, 0), z(2, 9, 0), z(2, 9, 0), _offsets([2, 3]), bad, bad, out=out)
+    assert not out.any()
+    got = bsq.bs_gemm_grouped_wgrad("nvfp4", z(6, 0), z(6, 0), z(7, 0), z(7, 0), _offsets([0, 0]), bad, bad)
+    assert got.shape == (2, 6, 7) and not got.any()
