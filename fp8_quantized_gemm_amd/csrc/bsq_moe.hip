@@ -440,7 +440,9 @@ __global__ __launch_bounds__(256) void k_moe_combine(const uint16_t* __restrict_
 // d_y[p] = w d_out[t], d_w[t, j] = <d_out[t], y[p]> for the assignment (t, j) of
 // row p; rows of none get zeros, slots of none d_w = 0.  One wave per row: a
 // row's gradient and its dot product come from one pass, and no two rows write
-// one place.  Bound by HBM: 8,192 tokens x 2, 4,096 columns 62 us, 5.5 TB/s.
+// one place: a row writes a slot that names it, and a slot whose row is out of
+// range or names another is cleared, so every d_w is written once whatever the
+// two arrays hold.  Bound by HBM: 8,192 tokens x 2, 4,096 columns 62 us, 5.5 TB/s.
 template <bool AL>
 __global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restrict__ d_out,
                                                          const uint16_t* __restrict__ y, int64_t tokens,
@@ -451,12 +453,13 @@ __global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restr
   const int lane = threadIdx.x & 63, n = (int)cols;
   const int64_t nw = (int64_t)gridDim.x * 4, slots = tokens * k;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < slots; i += nw * 64)
-    if (row_of[i] < 0) d_w[i] = 0.0f;
+    if (const int r = row_of[i]; r < 0 || r >= rows || src[r] != i) d_w[i] = 0.0f;
   for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < rows; p += nw) {
     const int a = __builtin_amdgcn_readfirstlane(src[p]);
     const bool on = a >= 0 && a < slots;
     const int64_t t = on ? a / k : 0;
     const float wa = on ? w[a] : 0.0f;
+    const bool own = on && row_of[a] == p;
     const uint16_t *g = d_out + t * cols, *yr = y + p * cols;
     const int have = on ? n : 0;
     uint16_t* o = d_y + p * cols;
@@ -483,7 +486,7 @@ __global__ __launch_bounds__(256) void k_moe_combine_bwd(const uint16_t* __restr
       }
     }
     dot = wave_sum(dot);
-    if (on && lane == 0) d_w[a] = dot;
+    if (own && lane == 0) d_w[a] = dot;
   }
 }
 

@@ -466,8 +466,10 @@ bsq_status moe_combine(const void* y, int64_t rows, int64_t cols, const int32_t*
 
 /*
  * Gradient of moe_combine: d_y[p] = weights[a] * d_out[a / k] with a = src[p]
- * (zeros where a is not in [0, tokens * k)), d_weights[a] = <d_out[a / k], y[p]>,
- * 0 for slots whose row_of is negative.  src and row_of come from one moe_route.
+ * (zeros where a is not in [0, tokens * k)), d_weights[a] = <d_out[a / k], y[p]>
+ * with p = row_of[a], 0 where p is not in [0, rows) or src[p] is not a.  src and
+ * row_of come from one moe_route; a buffer cut to a capacity (fewer rows, src cut
+ * alike) or slots taken out of either are slots without a row.
  */
 bsq_status moe_combine_backward(const void* d_out, const void* y, int64_t tokens, int64_t cols, int k,
                                 const int32_t* src, const int32_t* row_of, const float* weights,

@@ -136,7 +136,8 @@ def combine_backward(d_out, y, src, row_of, w):
     for p, a in enumerate(src):
         if 0 <= a < T * k:
             d_y[p] = w.reshape(-1)[a] * d_out[a // k]
-            d_w[a // k, a % k] = d_out[a // k] @ y[p]
+            if row_of[a // k, a % k] == p:
+                d_w[a // k, a % k] = d_out[a // k] @ y[p]
     return d_y, d_w
 
 
