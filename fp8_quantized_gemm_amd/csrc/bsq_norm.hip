@@ -259,7 +259,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block
   const int64_t trips = (a.rows + RPB - 1) / RPB;
   for (int64_t b = blockIdx.x; b < trips; b += gridDim.x, par ^= 1) {
     const int64_t row = b * RPB + sub;
-    const bool live = row < a.rows;
+    const bool live = RPB == 1 || row < a.rows;
     const int64_t rw = live ? row : a.rows - 1;
     const int64_t base = rw * a.cols;
     Raw<T> dr[CH], rr[CH];
@@ -296,7 +296,6 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block
       if (has_o) end_piece<AL>(orow[c], col(c), cols);
       if (gf) end_piece<AL>(gr[c], col(c), cols);
     }
-    const float one = live ? 1.0f : 0.0f;           // rows past the last add nothing to the column sums
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -311,11 +310,16 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block
         const float h = raw_at(dh[c], j), rn = raw_at(rr[c], j) * rs, av = h * wp1[j];
         float q = raw_at(orow[c], j) * rp * wq1[j];
         if (CH > 1 || gf) q *= raw_at(gr[c], j);
-        sp[c][j] = __builtin_fmaf(h * one, rn, sp[c][j]);
         s[0] = __builtin_fmaf(av, rn, s[0]);
         s[1] = __builtin_fmaf(raw_at(dr[c], j), q, s[1]);
         s[2] = __builtin_fmaf(av, q, s[2]);
         s[3] = __builtin_fmaf(rn, q, s[3]);
+      }
+      // rows past the last add nothing to the column sums (a factor of 0 would
+      // turn the last row's infinities into NaN)
+      if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sp[c][j] = __builtin_fmaf(raw_at(dh[c], j), raw_at(rr[c], j) * rs, sp[c][j]);
       }
     }
 #pragma unroll
@@ -339,7 +343,7 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block
         take(0, c, wq1);
         take(1, c, wp1);
       }
-      float y[8], z[8], dg[8];
+      float y[8], z[8], dg[8], Gg[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float av = raw_at(dh[c], j) * wp1[j], rn = raw_at(rr[c], j) * rs;
@@ -347,13 +351,14 @@ __global__ __launch_bounds__(TPR < 512 ? 512 : TPR, CH > 1 ? 2 : 4) void k_block
         y[j] = has_o ? a.alpha * G : G;
         const float on = raw_at(orow[c], j) * rp;
         const float g = CH > 1 ? raw_at(gr[c], j) * grow : gf ? raw_at(gr[c], j) : grow;
-        const float Gg = G * g;
-        st[c][j] = __builtin_fmaf(Gg * one, on, st[c][j]);
+        Gg[j] = G * g;
         dg[j] = G * wq1[j] * on;                        // full gate
-        z[j] = Gg * wq1[j];
+        z[j] = Gg[j] * wq1[j];
         if (post) z[j] = rp * __builtin_fmaf(-m2, on, z[j]);
       }
       if (live) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) st[c][j] = __builtin_fmaf(Gg[j], raw_at(orow[c], j) * rp, st[c][j]);
         store8<AL>(static_cast<T*>(a.d_x) + base, col(c), cols, y);
         if (has_o) store8<AL>(static_cast<uint16_t*>(a.d_o) + base, col(c), cols, z);
         if (gf) store8<AL>(static_cast<uint16_t*>(a.d_gate) + base, col(c), cols, dg);

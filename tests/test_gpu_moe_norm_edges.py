@@ -6,6 +6,7 @@ import torch
 
 import fp8_quantized_gemm_amd as bsq
 from oracle import moe as OM
+from oracle import norm as ON
 
 from _gpu import announce, gpu
 
@@ -64,3 +65,34 @@ def test_combine_backward_of_slots_without_a_row(T, C, what):
     for _ in range(3):
         again = _combine_backward(d, y, src, row_of, w)
         assert torch.equal(again[0], d_y) and torch.equal(again[1], d_w)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("C", [16, 100, 256, 600, 2048])
+@pytest.mark.parametrize("R", [1, 3, 65])
+@pytest.mark.parametrize("gate", [None, "channel", "row", "full"])
+def test_infinite_gradient_in_the_last_row(R, C, dtype, gate):
+    """Column sums are those of the rows there are, an infinite one included: the rows
+    that fill up a workgroup's last trip add nothing (not 0 times infinity)."""
+    announce("block_norm_backward, infinity in the last row", R, C, dtype, gate)
+    g = torch.Generator(device="cuda").manual_seed(R * 3 + C)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x, o = rn(R, C).to(dtype), rn(R, C).bfloat16()
+    wp, wq = 1 + 0.1 * rn(C), 1 + 0.1 * rn(C)
+    gt = {None: None, "channel": 1 + 0.1 * rn(C), "row": 1 + 0.1 * rn(R, 1), "full": (1 + 0.1 * rn(R, C)).bfloat16()}[gate]
+    f = bsq.block_norm(x, o, w_pre=wp, w_post=wq, gate=gt)
+    d_r, d_h = rn(R, C).to(dtype), rn(R, C).bfloat16()
+    d_h[R - 1, 3] = float("inf")
+    got = bsq.block_norm_backward(f["r"], o, d_r, d_h, wp, wq, gt, f["rstd_pre"], f["rstd_post"])
+    with np.errstate(invalid="ignore"):
+        want = ON.backward(_np(f["r"]), _np(o), _np(d_r), _np(d_h), _np(wp), _np(wq), None if gate is None else _np(gt),
+                           _np(f["rstd_pre"]), _np(f["rstd_post"]))
+    v, w, m = _np(got["d_w_pre"]), want["d_w_pre"], want["d_w_pre_"]
+    fine = np.isfinite(w)
+    assert fine.sum() == C - 1 and np.isinf(w[3]) and v[3] == w[3]
+    assert np.all(np.abs(v[fine] - w[fine]) <= (R + 12) * U * m[fine])          # R additions, 3 roundings a term
+    names = ["d_w_post"] + (["d_gate"] if gate == "channel" else [])
+    for n in names:                                                       # infinite but for column 3 (inf - inf)
+        v, w = _np(got[n]), want[n]
+        assert np.isnan(w[3]) and np.isinf(np.delete(w, 3)).all()
+        assert np.array_equal(v, w, equal_nan=True), n
