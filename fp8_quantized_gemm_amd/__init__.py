@@ -682,7 +682,7 @@ def _check_offsets(offsets):
 
 def bs_gemm_grouped(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=None, b_amax=None, out=None):
     """C [R, N] bf16: rows offsets[e] .. offsets[e + 1] - 1 of A [R, K] times B[e] [N, K]
-    transposed, zeros in the rows past the last group.  b_codes [E, N, K / per
+    transposed, zeros in the rows of no group.  b_codes [E, N, K / per
     byte], b_scales [E, N, K / block]; nvfp4: a_amax [1], b_amax [1] or [E]."""
     if fmt not in GROUPED_FORMATS:
         raise ValueError(f"unknown grouped format {fmt!r}")

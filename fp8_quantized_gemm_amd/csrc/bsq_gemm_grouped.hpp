@@ -46,8 +46,8 @@ __device__ __forceinline__ int lanes_prefix(int v) {
 }
 
 // Tile `pid` of the row-grouped product: row tiles of MT rows, groups in order,
-// each starting a new tile, then the rows past the last group (e = -1), in the
-// XCD-aware order of tile_of_block over all of them.  Returns false past the
+// each starting a new tile, then the rows of no group (e = -1: past the last, before
+// the first), in the XCD-aware order of tile_of_block over all of them.  Returns false past the
 // last tile (the grid covers the most there can be).  Every wave computes it
 // for itself, 64 experts at a time.
 template <int MT>
@@ -69,15 +69,20 @@ __device__ __forceinline__ bool group_tile_rows(const GroupRef& g, int64_t rows,
   }
   int64_t last = g.offsets[g.experts];
   last = last < 0 ? 0 : last > rows ? rows : last;
-  const int all = total + (int)((rows - last + MT - 1) / MT);
+  int64_t first = g.offsets[0];
+  first = first < 0 ? 0 : first > rows ? rows : first;
+  const int past = (int)((rows - last + MT - 1) / MT);
+  const int all = total + past + (int)((first + MT - 1) / MT);
   if ((int64_t)pid >= (int64_t)all * tiles_n) return false;
   int tm;
   tile_of_block(pid, all, tiles_n, tm, tn);
   if (tm >= total) {
+    const bool before = tm - total >= past;
+    const int64_t from = before ? 0 : last;
     t.e = -1;
-    t.row0 = last + (int64_t)(tm - total) * MT;
-    t.row1 = rows;
-    return t.row0 >= last && t.row0 < rows;
+    t.row0 = from + (int64_t)(tm - total - (before ? past : 0)) * MT;
+    t.row1 = before ? first : rows;
+    return t.row0 >= from && t.row0 < t.row1;
   }
   int before = 0;
   for (e0 = 0; e0 < g.experts; e0 += 64) {
@@ -124,9 +129,9 @@ __device__ __forceinline__ void group_range(const GroupRef& g, int e, int64_t ro
 }
 
 // Most row tiles of MT rows there can be: every group with rows (the rows of no
-// group count as one) has at most one partly filled tile.
+// group count as two) has at most one partly filled tile.
 inline int64_t max_row_tiles(int64_t rows, int experts, int MT) {
-  const int64_t g = rows < experts + 1 ? rows : experts + 1;
+  const int64_t g = rows < experts + 2 ? rows : experts + 2;
   return (rows - g) / MT + g;
 }
 

@@ -260,3 +260,23 @@ def test_products_without_a_reduction_are_zero_whatever_the_amax(amax):
     assert not out.any()
     got = bsq.bs_gemm_grouped_wgrad("nvfp4", z(6, 0), z(6, 0), z(7, 0), z(7, 0), _offsets([0, 0]), bad, bad)
     assert got.shape == (2, 6, 7) and not got.any()
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("first", [1, 64, 300])
+def test_rows_before_the_first_group_are_zero(name, fmt, first):
+    """Offsets of some of the experts (one rank's, say) over the whole buffer: the rows
+    before theirs belong to no group either."""
+    announce("grouped rows, first group at", first, "on", name, fmt)
+    sizes, past, N, K = [70, 0, 33], 20, 130, 512
+    a, b, ta, tb, want = _rows_case(fmt, True, [first] + sizes, past, N, K, 41)
+    off = _offsets([first] + sizes)
+    b1 = tuple(t[1:].contiguous() for t in b)
+    tb1 = None if tb is None else tb[1:].contiguous()
+    want[:first] = 0
+    _judge(grouped_on(name, False, fmt, a, b1, off[1:].contiguous(), ta, tb1), want, True, (name, fmt, first))
+    none = torch.full((4,), sum(sizes) + first + past, dtype=torch.int32, device="cuda")     # no group has rows
+    assert not grouped_on(name, False, fmt, a, b1, none, ta, tb1).any()
+    got = bsq.bs_gemm_grouped(fmt, *a, *b1, off[1:].contiguous(), ta, tb1)
+    _judge(got, want, True, (fmt, first))
