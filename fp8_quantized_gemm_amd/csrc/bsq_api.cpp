@@ -267,14 +267,14 @@ bsq_status quantize_transpose(const void* x, int64_t rows, int64_t cols, bsq_for
   if (rnd != BSQ_RNE && rnd != BSQ_SR) return BSQ_EINVAL;
   const bool do_row = codes_row || scales_row || (nv && amax_row);
   const bool do_col = codes_col || scales_col || (nv && amax_col);
-  if (!do_row && !do_col) return BSQ_EINVAL;
+  if (!do_row && !do_col && rows * cols != 0) return BSQ_EINVAL;   // empty tensors have null pointers
   if (!nv && (block_rows == 16 || rht_col)) return BSQ_EUNSUPPORTED;
   if (fmt == BSQ_MXFP8 && rnd == BSQ_SR) return BSQ_EUNSUPPORTED;
   if (block_rows == 16 && (rnd == BSQ_SR || rht_col)) return BSQ_EUNSUPPORTED;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows * cols == 0) {                      // empty tensor: only the amax outputs are defined
     if (nv && (!aligned4(amax_row) || !aligned4(amax_col))) return BSQ_EINVAL;
-    if (nv) return hip_status(bsq::launch_zero_amax(amax_row, amax_col, s));
+    if (nv && (amax_row || amax_col)) return hip_status(bsq::launch_zero_amax(amax_row, amax_col, s));
     return BSQ_OK;
   }
   if (do_row && (!codes_row || !scales_row || (nv && !amax_row))) return BSQ_EINVAL;
@@ -311,7 +311,7 @@ bsq_status fp8_quantize_transpose(const void* x, int64_t rows, int64_t cols, uin
   if (rows < 0 || cols < 0 || rows % 16 != 0 || cols % 16 != 0) return BSQ_EINVAL;
   if (too_many(rows, cols)) return BSQ_EINVAL;
   if (!amax || !aligned4(amax)) return BSQ_EINVAL;
-  if (!codes_row && !codes_col) return BSQ_EINVAL;
+  if (!codes_row && !codes_col && rows * cols != 0) return BSQ_EINVAL;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows * cols == 0) return hip_status(bsq::launch_zero_amax(amax, nullptr, s));
   if (!x || !aligned16(x) || !aligned16_or_null(codes_row) || !aligned16_or_null(codes_col))
@@ -334,7 +334,7 @@ bsq_status quantize_transpose_amax(const void* x, int64_t rows, int64_t cols, in
   if (rnd != BSQ_RNE && rnd != BSQ_SR) return BSQ_EINVAL;
   const bool do_row = codes_row || scales_row;
   const bool do_col = codes_col || scales_col;
-  if (!do_row && !do_col) return BSQ_EINVAL;
+  if (!do_row && !do_col && rows * cols != 0) return BSQ_EINVAL;   // empty tensors have null pointers
   if (block_rows == 16 && (rnd == BSQ_SR || rht_col)) return BSQ_EUNSUPPORTED;
   // 16x16 tiles encode both orientations under one amax (the codes of x^T
   // are the codes of x transposed), so the caller must pass that one amax

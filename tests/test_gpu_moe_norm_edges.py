@@ -1,10 +1,11 @@
-"""Edges of the norm, the router and the row movers."""
+"""Edges of the norm, the router and the row movers, and a layer without tokens."""
 
 import numpy as np
 import pytest
 import torch
 
 import fp8_quantized_gemm_amd as bsq
+from fp8_quantized_gemm_amd.moe import MoELayer
 from oracle import moe as OM
 from oracle import norm as ON
 
@@ -96,3 +97,37 @@ def test_infinite_gradient_in_the_last_row(R, C, dtype, gate):
         v, w = _np(got[n]), want[n]
         assert np.isnan(w[3]) and np.isinf(np.delete(w, 3)).all()
         assert np.array_equal(v, w, equal_nan=True), n
+
+
+def test_layer_without_tokens():
+    """A micro-batch of no tokens: empty activations, zero weight gradients."""
+    announce("MoELayer without tokens")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+    L = MoELayer(rn(4, 64, 48), rn(4, 48, 32), 2, dict(w_pre=1 + 0.1 * rn(48), w_post=1 + 0.1 * rn(48)))
+    x = rn(0, 48).bfloat16()
+    L.grad["W_gu"].fill_(3)
+    L.grad["W_down"].fill_(3)
+    r, h = L.open(x, x)
+    y = L.forward(h, rn(0, 4))
+    d_h, d_l = L.backward(y)
+    grads = L.close(r, d_h)
+    assert y.shape == (0, 48) and d_h.shape == (0, 48) and d_l.shape == (0, 4) and r.shape == (0, 48)
+    assert not L.grad["W_gu"].any() and not L.grad["W_down"].any()
+    assert grads["d_x"].shape == (0, 48) and not grads["d_w_pre"].any() and not grads["d_w_post"].any()
+    before = L.w32["W_gu"].clone()
+    L.update()
+    assert torch.equal(before, L.w32["W_gu"])
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (64, 0)])
+def test_quantizers_of_empty_tensors(shape):
+    announce("quantizers of empty tensors", shape)
+    x = torch.zeros(shape, device="cuda").bfloat16()
+    for fmt in ("nvfp4", "mxfp4", "mxfp8"):
+        q = bsq.quantize_transpose(x, fmt)
+        assert q["row_codes"].numel() == 0 and q["col_codes"].numel() == 0
+    assert not bsq.quantize_transpose(x)["row_amax"].any()
+    a = torch.ones(1, device="cuda")
+    assert bsq.quantize_transpose_amax(x, a, a)["row_scales"].shape == (shape[0], shape[1] // 16)
+    assert not bsq.fp8_quantize_transpose(x)["amax"].any()
