@@ -27,7 +27,7 @@ ABI_SYMBOLS = ("nvfp4_quantize", "mx_quantize", "quantize_transpose", "quantize_
                "master_weight_update", "nvfp4_expand", "bs_gemm", "bs_gemm_noalloc",
                "bs_gemm_nvfp4_bx", "block_norm", "block_norm_backward_workspace",
                "block_norm_backward", "moe_rows", "moe_route_workspace", "moe_route",
-               "moe_route_backward", "moe_gather", "moe_combine", "moe_combine_backward",
+               "moe_route_score_bias", "moe_route_backward", "moe_gather", "moe_combine", "moe_combine_backward",
                "bs_gemm_grouped", "bs_gemm_grouped_wgrad", "bsq_status_string")
 
 
@@ -72,6 +72,7 @@ def lib():
         L.moe_rows.argtypes = [I64, I, I, I, P]
         L.moe_route_workspace.argtypes = [I64, I, I, P]
         L.moe_route.argtypes = [P, I, I64, I, I, P, I, I, F, I, I64, P, P, P, P, P, P, I64, P]
+        L.moe_route_score_bias.argtypes = L.moe_route.argtypes
         L.moe_route_backward.argtypes = [P, I, I64, I, I, P, P, I, I, F, P, P]
         L.moe_gather.argtypes = [P, I64, I64, I, P, I64, P, P]
         L.moe_combine.argtypes = [P, I64, I64, P, P, I64, I, P, P]
@@ -564,8 +565,13 @@ def moe_rows(tokens, experts, k, align=1):
     return _size("moe_rows", int(tokens), int(experts), int(k), int(align))
 
 
-def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1):
+def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1, score_bias=None):
     """Top-k routing of logits [T, E] (bfloat16 or float32; -inf masks an expert).
+
+    bias, score_bias (float32 [E], one of them): steer the selection and not the
+    weights, which goes by logit + bias or by score + score_bias, the score being
+    sigmoid(logit) or softmax(logits).  The correction bias of a router balanced
+    without an auxiliary loss is a score_bias.
 
     Returns dict(experts int32 [T, k] (-1: no candidate left), weights float32 [T,
     k], offsets int32 [E + 1] (rows of each expert's padded group), row_of int32
@@ -573,7 +579,10 @@ def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0
     slot of the row, -1: padding))."""
     logits = _check_stream(logits, "logits")
     (T, E), dev, k = logits.shape, logits.device, int(k)
-    bias = _check_like(bias, "bias", (E,), torch.float32, dev)
+    if bias is not None and score_bias is not None:
+        raise ValueError("bias is added to the logits, score_bias to the scores: give one of them")
+    scored = score_bias is not None
+    bias = _check_like(score_bias if scored else bias, "score_bias" if scored else "bias", (E,), torch.float32, dev)
     sc, rows = _scoring(scoring), moe_rows(T, E, k, align)
     need = _size("moe_route_workspace", T, E, k)
     i32 = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
@@ -581,10 +590,11 @@ def moe_route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0
     ids, row_of = ids.view(T, k), row_of.view(T, k)
     w = torch.empty(T, k, dtype=torch.float32, device=dev)
     ws = i32(need // 4) if need else None
-    st = lib().moe_route(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
-                         1 if normalize else 0, float(scale), int(align), rows, _ptr(ids), _ptr(w), _ptr(off),
-                         _ptr(row_of), _ptr(src), _ptr(ws), need, _stream(dev))
-    _check("moe_route", st)
+    fn = "moe_route_score_bias" if scored else "moe_route"
+    st = getattr(lib(), fn)(_ptr(logits), int(logits.dtype == torch.float32), T, E, k, _ptr(bias), sc,
+                            1 if normalize else 0, float(scale), int(align), rows, _ptr(ids), _ptr(w), _ptr(off),
+                            _ptr(row_of), _ptr(src), _ptr(ws), need, _stream(dev))
+    _check(fn, st)
     return dict(experts=ids, weights=w, offsets=off, row_of=row_of, src=src)
 
 

@@ -165,6 +165,31 @@ bsq_status moe_rows_of(int64_t tokens, int experts, int k, int align, int64_t* r
   return BSQ_OK;
 }
 
+// moe_route; scored: moe_route_score_bias.
+bsq_status route_common(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                        const float* bias, bool scored, bsq_scoring scoring, int normalize, float scale,
+                        int align, int64_t rows, int32_t* experts_out, float* weights, int32_t* offsets,
+                        int32_t* row_of, int32_t* src, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  int64_t need = 0;
+  const bsq_status st = moe_rows_of(tokens, experts, k, align, &need);
+  if (st != BSQ_OK) return st;
+  if (!valid_dtype(type) || (scoring != BSQ_SOFTMAX && scoring != BSQ_SIGMOID)) return BSQ_EINVAL;
+  if (rows < need || rows > 0x7FFFFFFF) return BSQ_EINVAL;
+  if (!offsets || !aligned4(offsets) || (rows > 0 && !src) || !aligned4(src)) return BSQ_EINVAL;
+  if (scored && !bias) return BSQ_EINVAL;
+  if (tokens > 0 && (!logits || !experts_out || !weights || !row_of)) return BSQ_EINVAL;
+  if (!aligned_elem(logits, type == BSQ_F32) || !aligned4(bias) || !aligned4(experts_out) ||
+      !aligned4(weights) || !aligned4(row_of) || !aligned4(workspace))
+    return BSQ_EINVAL;
+  const int64_t hist = bsq::moe_route_hist_bytes(tokens, experts);
+  if (hist > 0 && (!workspace || workspace_bytes < hist)) return BSQ_EINVAL;
+  const bsq::RouteArgs a{logits, type == BSQ_F32, tokens, experts, k, bias, scored, scoring == BSQ_SIGMOID,
+                         normalize != 0, scale, align, rows, experts_out, weights, offsets, row_of,
+                         src, static_cast<int32_t*>(workspace)};
+  return hip_status(bsq::launch_moe_route(a, static_cast<hipStream_t>(stream)));
+}
+
 // Element counts and pointers of the token <-> expert row movers.
 bsq_status mover_checks(int64_t tokens, int64_t cols, int k, int64_t rows) {
   if (tokens < 0 || cols < 0 || k < 1 || rows < 0 || rows > 0x7FFFFFFF) return BSQ_EINVAL;
@@ -529,22 +554,17 @@ bsq_status moe_route(const void* logits, bsq_dtype type, int64_t tokens, int exp
                      int64_t rows, int32_t* experts_out, float* weights, int32_t* offsets,
                      int32_t* row_of, int32_t* src, void* workspace, int64_t workspace_bytes,
                      void* stream) {
-  int64_t need = 0;
-  const bsq_status st = moe_rows_of(tokens, experts, k, align, &need);
-  if (st != BSQ_OK) return st;
-  if (!valid_dtype(type) || (scoring != BSQ_SOFTMAX && scoring != BSQ_SIGMOID)) return BSQ_EINVAL;
-  if (rows < need || rows > 0x7FFFFFFF) return BSQ_EINVAL;
-  if (!offsets || !aligned4(offsets) || (rows > 0 && !src) || !aligned4(src)) return BSQ_EINVAL;
-  if (tokens > 0 && (!logits || !experts_out || !weights || !row_of)) return BSQ_EINVAL;
-  if (!aligned_elem(logits, type == BSQ_F32) || !aligned4(bias) || !aligned4(experts_out) ||
-      !aligned4(weights) || !aligned4(row_of) || !aligned4(workspace))
-    return BSQ_EINVAL;
-  const int64_t hist = bsq::moe_route_hist_bytes(tokens, experts);
-  if (hist > 0 && (!workspace || workspace_bytes < hist)) return BSQ_EINVAL;
-  const bsq::RouteArgs a{logits, type == BSQ_F32, tokens, experts, k, bias, scoring == BSQ_SIGMOID, normalize != 0,
-                         scale, align, rows, experts_out, weights, offsets, row_of, src,
-                         static_cast<int32_t*>(workspace)};
-  return hip_status(bsq::launch_moe_route(a, static_cast<hipStream_t>(stream)));
+  return route_common(logits, type, tokens, experts, k, bias, false, scoring, normalize, scale, align, rows,
+                      experts_out, weights, offsets, row_of, src, workspace, workspace_bytes, stream);
+}
+
+bsq_status moe_route_score_bias(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                                const float* score_bias, bsq_scoring scoring, int normalize, float scale,
+                                int align, int64_t rows, int32_t* experts_out, float* weights,
+                                int32_t* offsets, int32_t* row_of, int32_t* src, void* workspace,
+                                int64_t workspace_bytes, void* stream) {
+  return route_common(logits, type, tokens, experts, k, score_bias, true, scoring, normalize, scale, align, rows,
+                      experts_out, weights, offsets, row_of, src, workspace, workspace_bytes, stream);
 }
 
 bsq_status moe_route_backward(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,

@@ -189,6 +189,7 @@ struct RouteArgs {
   int64_t tokens;
   int experts, k;
   const float* bias;              // null: none
+  bool scored;                    // the bias is added to the score, not to the logit
   bool sigmoid, normalize;
   float scale;
   int align;

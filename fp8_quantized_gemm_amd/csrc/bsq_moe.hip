@@ -79,16 +79,21 @@ __device__ __forceinline__ void load_logits(const void* logits, bool f32, int64_
 }
 
 // Selection and weight of token t: lane j < k of the row gets slot j's expert
-// (-1: none left) and weight.
-template <int NV>
+// (-1: none left) and weight.  SCORED: the bias is added to the score (the FP32
+// value the unnormalised weight has), else to the logit.
+template <int NV, bool SCORED>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int lane, const float (&bias)[NV],
                                             int& id, float& w) {
   float l[NV];                                     // read again for the softmax over all: fewer registers
   load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
   uint32_t key[NV];
+  float m = 0.0f, sum = 1.0f;
+  if (SCORED && !a.sigmoid) full_softmax_stats<NV>(l, m, sum);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const float s = (l[j] + bias[j]) + 0.0f;       // -0 counts as +0
+    float s = l[j];                                // masked stays -inf
+    if (SCORED && s > kNegInf) s = a.sigmoid ? sigmoid(s) : expf(s - m) / sum;
+    s = (s + bias[j]) + 0.0f;                      // -0 counts as +0
     key[j] = s > kNegInf ? float_key(s) : 0u;
   }
   uint32_t mine = ~0u;
@@ -112,9 +117,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int l
   } else if (a.sigmoid) {
     w = on ? sigmoid(sel) : 0.0f;
   } else {
-    float m, sum;
-    load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
-    full_softmax_stats<NV>(l, m, sum);
+    if constexpr (!SCORED) {
+      load_logits<NV>(a.logits, a.f32, t, a.experts, lane, l);
+      full_softmax_stats<NV>(l, m, sum);
+    }
     w = on ? expf(sel - m) / sum : 0.0f;
   }
   w = on ? a.scale * w : 0.0f;
@@ -130,7 +136,7 @@ __host__ __device__ inline int route_span(int64_t tokens) {
 }
 
 // Selection, weights and per-expert counts of the workgroup's tokens.
-template <int NV>
+template <int NV, bool SCORED>
 __device__ __forceinline__ void route_select(const RouteArgs& a, int64_t t0, int64_t t1, int32_t* cnt) {
   const int lane = threadIdx.x & 15, row = threadIdx.x >> 4;
   float bias[NV];
@@ -143,7 +149,7 @@ __device__ __forceinline__ void route_select(const RouteArgs& a, int64_t t0, int
     const int64_t t = tb + row;
     int id;
     float w;
-    route_token<NV>(a, t < t1 ? t : t1 - 1, lane, bias, id, w);
+    route_token<NV, SCORED>(a, t < t1 ? t : t1 - 1, lane, bias, id, w);
     if (lane < a.k && t < t1) {
       a.ids[t * a.k + lane] = id;
       a.weights[t * a.k + lane] = w;
@@ -243,27 +249,27 @@ __device__ __forceinline__ void route_fill(const RouteArgs& a, const RouteLds& s
 }
 
 // Everything in one workgroup (few tokens: launches cost more than the work).
-template <int NV>
+template <int NV, bool SCORED>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route_small(RouteArgs a) {
   __shared__ RouteLds s;
   const int tid = threadIdx.x;
   for (int e = tid; e < a.experts; e += kRouteThreads) s.total[e] = s.run[0][e] = 0;
   __syncthreads();
-  route_select<NV>(a, 0, a.tokens, s.total);
+  route_select<NV, SCORED>(a, 0, a.tokens, s.total);
   __threadfence_block();                                 // ids written above are read below by other waves
   __syncthreads();
   route_place(a, 0, a.tokens, s, true);
   route_fill(a, s, 0, 1);
 }
 
-template <int NV>
+template <int NV, bool SCORED>
 __global__ __launch_bounds__(kRouteThreads) void k_moe_select(RouteArgs a) {
   __shared__ int32_t cnt[kMoeMaxExperts];
   const int span = route_span(a.tokens);
   const int64_t t0 = (int64_t)blockIdx.x * span, t1 = t0 + span < a.tokens ? t0 + span : a.tokens;
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) cnt[e] = 0;
   __syncthreads();
-  route_select<NV>(a, t0, t1, cnt);
+  route_select<NV, SCORED>(a, t0, t1, cnt);
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.hist[(int64_t)blockIdx.x * a.experts + e] = cnt[e];
 }
@@ -508,15 +514,18 @@ int64_t moe_route_hist_bytes(int64_t tokens, int experts) {
   return blocks > 1 ? blocks * experts * (int64_t)sizeof(int32_t) : 0;
 }
 
-hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
+namespace {
+
+template <bool SCORED>
+hipError_t run_route(const RouteArgs& a, hipStream_t s) {
   const int span = route_span(a.tokens);
   const unsigned blocks = (unsigned)((a.tokens + span - 1) / span);
 #define BSQ_ROUTE(NV)                                                                              \
   if (blocks <= 1) {                                                                                \
-    hipLaunchKernelGGL(k_moe_route_small<NV>, dim3(1), dim3(kRouteThreads), 0, s, a);                \
+    hipLaunchKernelGGL((k_moe_route_small<NV, SCORED>), dim3(1), dim3(kRouteThreads), 0, s, a);      \
     return hipGetLastError();                                                                       \
   }                                                                                                 \
-  hipLaunchKernelGGL(k_moe_select<NV>, dim3(blocks), dim3(kRouteThreads), 0, s, a)
+  hipLaunchKernelGGL((k_moe_select<NV, SCORED>), dim3(blocks), dim3(kRouteThreads), 0, s, a)
   if (a.experts <= 16) { BSQ_ROUTE(1); }
   else if (a.experts <= 32) { BSQ_ROUTE(2); }
   else if (a.experts <= 64) { BSQ_ROUTE(4); }
@@ -526,6 +535,12 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
 #undef BSQ_ROUTE
   hipLaunchKernelGGL(k_moe_place, dim3(blocks), dim3(kRouteThreads), 0, s, a);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s) {
+  return a.scored ? run_route<true>(a, s) : run_route<false>(a, s);
 }
 
 hipError_t launch_moe_route_bwd(const void* logits, bool f32, int64_t tokens, int experts, int k,

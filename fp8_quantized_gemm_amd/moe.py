@@ -42,10 +42,11 @@ ALIGN = 32
 class MoELayer:
     """w_gu: FP32 masters [E, 2F, hidden] (gate rows first); w_down: [E, hidden, F]; both
     copied.  norm: dict of block_norm's w_pre, w_post, gate, alpha, eps (w_pre
-    required).  hidden % 16 == 0, F % 16 == 0."""
+    required).  scoring, normalize, scale, bias, score_bias: moe_route's.  hidden %
+    16 == 0, F % 16 == 0."""
 
     def __init__(self, w_gu, w_down, k, norm, scoring="softmax", normalize=True, scale=1.0, bias=None,
-                 rht=True, rht_signs=0, sr_seed=0, lr=1e-4):
+                 rht=True, rht_signs=0, sr_seed=0, lr=1e-4, score_bias=None):
         if not (w_gu.is_cuda and w_down.is_cuda and w_gu.device == w_down.device):
             raise ValueError("the master weights must be CUDA tensors on one device")
         E, F2, Hd = w_gu.shape
@@ -55,7 +56,7 @@ class MoELayer:
         if norm.get("w_pre") is None:
             raise ValueError("norm needs w_pre: the block's input is normalised")
         self.dev, self.E, self.F, self.Hd, self.k = w_gu.device, E, F, Hd, int(k)
-        self.norm, self.bias = dict(norm), bias
+        self.norm, self.bias, self.score_bias = dict(norm), bias, score_bias
         self.routing = dict(scoring=scoring, normalize=normalize, scale=scale)
         self.rht, self.signs, self.seed, self.lr, self.it = bool(rht), int(rht_signs), int(sr_seed), float(lr), 0
         self.w32 = {"W_gu": w_gu.detach().float().contiguous().clone(),
@@ -111,7 +112,7 @@ class MoELayer:
     def forward(self, h, logits):
         """y [T, hidden] (bfloat16) of h [T, hidden] and the router's logits [T, E]."""
         self.logits = logits
-        self.route = moe_route(logits, self.k, bias=self.bias, align=ALIGN, **self.routing)
+        self.route = moe_route(logits, self.k, bias=self.bias, score_bias=self.score_bias, align=ALIGN, **self.routing)
         xp = moe_gather(h, self.route["src"], self.k)
         self.qx = self._quantize(xp, "rne", 0)
         self._quantize_weight("W_gu")

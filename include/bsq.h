@@ -415,7 +415,9 @@ bsq_status moe_route_workspace(int64_t tokens, int experts, int k, int64_t* byte
  *   softmax            : softmax over all unmasked logits
  *   sigmoid, normalize : sigmoid(l) over the sum of the selected sigmoids
  *   sigmoid            : sigmoid(l)
- * (the bias steers the selection only).  A slot without a candidate left gets
+ * (the bias steers the selection only, and is added to the logit: a correction
+ * bias trained to be added to the score goes to moe_route_score_bias, which takes
+ * other experts under the same numbers).  A slot without a candidate left gets
  * expert -1, weight 0 and row -1.  Rows: the assignments sorted by expert, then
  * token, then slot, each expert's group padded to a multiple of align rows.
  *   logits  : in, [tokens, experts] of type.  bias : in, FP32 [experts] or NULL.
@@ -434,6 +436,20 @@ bsq_status moe_route(const void* logits, bsq_dtype type, int64_t tokens, int exp
                      int64_t rows, int32_t* experts_out, float* weights, int32_t* offsets,
                      int32_t* row_of, int32_t* src, void* workspace, int64_t workspace_bytes,
                      void* stream);
+
+/*
+ * moe_route with the selection bias of routers balanced without an auxiliary loss:
+ * per token the k experts with the largest score + score_bias (FP32 sum), the score
+ * being sigmoid(l), or softmax(l) over all experts whose logit is not masked, as
+ * FP32 (within a few units in the last place of the exact value, so scores closer
+ * than that can change places).  Masks, ties, weights (without the bias), rows and
+ * outputs as for moe_route; score_bias is FP32 [experts], not NULL.
+ */
+bsq_status moe_route_score_bias(const void* logits, bsq_dtype type, int64_t tokens, int experts, int k,
+                                const float* score_bias, bsq_scoring scoring, int normalize, float scale,
+                                int align, int64_t rows, int32_t* experts_out, float* weights,
+                                int32_t* offsets, int32_t* row_of, int32_t* src, void* workspace,
+                                int64_t workspace_bytes, void* stream);
 
 /*
  * Gradient of moe_route's weights with respect to its logits; the selection is

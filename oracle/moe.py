@@ -2,7 +2,8 @@
 
 Test infrastructure only (see oracle/__init__.py).  The source pages name no
 formulas for a mixture-of-experts layer; the definitions are those include/bsq.h
-writes out.  Selection is exact (FP32 logit + bias, ties to the lowest expert);
+writes out.  Selection is exact (FP32 logit + bias, or the rounded score +
+score_bias; ties to the lowest expert);
 weights, gradients and products are float64.
 """
 
@@ -29,6 +30,22 @@ def select(logits, bias, k):
             out[t, j] = best
             left.remove(best)
     return out
+
+
+def scores(logits, scoring):
+    """float64 scores [T, E] of the logits that are not masked (0 for the others)."""
+    l = logits.astype(np.float64)
+    ok = l > -np.inf
+    if scoring == "sigmoid":
+        return np.where(ok, _sigmoid(np.where(ok, l, 0)), 0)
+    z = np.where(ok, np.exp(np.where(ok, l, -np.inf) - np.max(np.where(ok, l, -1e300), axis=1, keepdims=True)), 0)
+    return z / np.maximum(z.sum(1, keepdims=True), 1e-300)
+
+
+def select_by_score(logits, score_bias, k, scoring):
+    """experts [T, k] by FP32 score + score_bias."""
+    s = scores(logits, scoring).astype(np.float32)
+    return select(np.where(logits > -np.inf, s, np.float32(-np.inf)), score_bias, k)
 
 
 def _sigmoid(l):
@@ -60,9 +77,9 @@ def probabilities(l, ids, scoring, normalize):
     return p
 
 
-def route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1):
+def route(logits, k, bias=None, scoring="softmax", normalize=True, scale=1.0, align=1, score_bias=None):
     T, E = logits.shape
-    ids = select(logits, bias, k)
+    ids = select(logits, bias, k) if score_bias is None else select_by_score(logits, score_bias, k, scoring)
     w = np.zeros((T, k))
     for t in range(T):
         p = probabilities(logits[t], ids[t], scoring, normalize)
