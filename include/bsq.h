@@ -409,10 +409,12 @@ bsq_status moe_route_workspace(int64_t tokens, int experts, int k, int64_t* byte
 
 /*
  * The router.  Per token: the k experts with the largest logit + bias (FP32
- * sum), in descending order, ties to the lowest expert; a logit or sum that is
- * -inf or NaN is masked and never taken.  Weights, times scale:
+ * sum), in descending order, ties to the lowest expert; an expert whose logit or
+ * sum is -inf or NaN is masked and never taken.  Weights, times scale:
  *   softmax, normalize : softmax over the selected logits
- *   softmax            : softmax over all unmasked logits
+ *   softmax            : softmax over all logits but those that are -inf or NaN
+ *                        themselves (one that only the bias masks keeps its share,
+ *                        and its gradient)
  *   sigmoid, normalize : sigmoid(l) over the sum of the selected sigmoids
  *   sigmoid            : sigmoid(l)
  * (the bias steers the selection only, and is added to the logit: a correction
@@ -453,8 +455,8 @@ bsq_status moe_route_score_bias(const void* logits, bsq_dtype type, int64_t toke
 
 /*
  * Gradient of moe_route's weights with respect to its logits; the selection is
- * constant.  Logits of no slot get 0, except for softmax without normalize
- * (masked ones, and tokens without any expert, 0 there too).
+ * constant.  Logits of no slot get 0, except for softmax without normalize (there
+ * 0 for logits of -inf or NaN and for tokens without any expert).
  *   experts_in : in, moe_route's experts.  d_weights : in, FP32 [tokens, k].
  *   d_logits   : out, [tokens, experts] of type.
  */

@@ -131,3 +131,37 @@ def test_quantizers_of_empty_tensors(shape):
     a = torch.ones(1, device="cuda")
     assert bsq.quantize_transpose_amax(x, a, a)["row_scales"].shape == (shape[0], shape[1] // 16)
     assert not bsq.fp8_quantize_transpose(x)["amax"].any()
+
+
+@pytest.mark.parametrize("E", [8, 100])
+@pytest.mark.parametrize("scoring,normalize", [("softmax", False), ("softmax", True), ("sigmoid", True)])
+def test_an_expert_masked_by_the_bias_keeps_its_share_of_the_full_softmax(E, scoring, normalize):
+    """A bias of -inf takes an expert out of the selection and leaves its logit in the
+    softmax over all, forward and backward (the selection is constant there)."""
+    announce("moe_route, bias of -inf", E, scoring, normalize)
+    g = torch.Generator(device="cuda").manual_seed(E)
+    T, k = 90, 3
+    l, d = torch.randn((T, E), generator=g, device="cuda"), torch.randn((T, k), generator=g, device="cuda")
+    l[5, 2:] = float("-inf")                             # what is left is masked by the bias
+    b = torch.zeros(E, device="cuda")
+    b[:2] = float("-inf")
+    f = bsq.moe_route(l, k, b, scoring, normalize)
+    got = bsq.moe_route_backward(l, f["experts"], d, scoring, normalize)
+    ln = l.cpu().numpy()
+    want = OM.route(ln, k, b.cpu().numpy(), scoring, normalize)
+    assert np.array_equal(f["experts"].cpu().numpy(), want["experts"]) and (f["experts"] > 1).any()
+    assert torch.all(f["experts"][5] == -1) and not f["weights"][5].any() and not got[5].any()
+    # the bounds of the router's own tests: 64 roundings of a weight, 128 of a term
+    assert np.all(np.abs(_np(f["weights"]) - want["weights"]) <= 64 * U * want["weights"] + 1e-37)
+    dl = OM.route_backward(ln, want["experts"], _np(d), scoring, normalize)
+    mag = np.abs(_np(d)).max(1)[:, None] * (np.abs(dl) > 0)
+    assert np.all(np.abs(_np(got) - dl) <= 128 * U * mag + U * np.abs(dl) + 1e-37)
+    assert (np.abs(dl[:, :2]).max() > 0) == (scoring == "softmax" and not normalize)
+    if not normalize:                                    # ... which is the difference quotient's answer too
+        h, t = 1e-6, 7
+        for e in (0, 1, int(want["experts"][t, 0])):
+            up, dn = ln[t].astype(np.float64), ln[t].astype(np.float64)
+            up[e] += h
+            dn[e] -= h
+            p = [OM.probabilities(v, want["experts"][t], scoring, normalize)[want["experts"][t]] for v in (up, dn)]
+            assert abs(((p[0] - p[1]) * _np(d)[t]).sum() / (2 * h) - dl[t, e]) < 1e-7
