@@ -499,8 +499,10 @@ bsq_status moe_combine_backward(const void* d_out, const void* y, int64_t tokens
  * offsets[e + 1],
  *   C[p, n] = alpha_e * sum_k deq(A)[p, k] * deq(B_e)[n, k]
  * and zeros in the rows of no group (before offsets[0] and from offsets[experts]
- * on).  FP32 accumulation, one BF16 rounding.  Operands as for bs_gemm: A [rows,
- * K], B [experts, N, K], contiguous.
+ * on).  FP32 accumulation, one BF16 rounding; MXFP8: the matrix instruction adds
+ * eight neighbouring products (k = 8 i .. 8 i + 7) with an error of up to 2^-13 of
+ * the largest each, in bs_gemm too.  Operands as for bs_gemm: A [rows, K], B
+ * [experts, N, K], contiguous.
  *   fmt     : BSQ_NVFP4 (K % 16 == 0), BSQ_MXFP4 or BSQ_MXFP8 (K % 32 == 0);
  *             BSQ_FP8 is BSQ_EUNSUPPORTED.
  *   offsets : in, device int32 [experts + 1], ascending (values outside [0,

@@ -280,3 +280,31 @@ def test_rows_before_the_first_group_are_zero(name, fmt, first):
     assert not grouped_on(name, False, fmt, a, b1, none, ta, tb1).any()
     got = bsq.bs_gemm_grouped(fmt, *a, *b1, off[1:].contiguous(), ta, tb1)
     _judge(got, want, True, (fmt, first))
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("cancel", [False, True])
+def test_mxfp8_sums_of_eight(name, cancel):
+    """The stated error of MXFP8: 2^-13 of the largest of eight neighbouring products
+    for each of them, the FP32 sum over K, and half a BF16 step; also where the large
+    products cancel, in the same eight or in other ones."""
+    announce("mxfp8 sums of eight on", name, cancel)
+    rng = np.random.default_rng(51)
+    R, N, K = 70, 130, 512
+    ac, asc = _operand(rng, R, K, "mxfp8", False)
+    bc, bsc = _operand(rng, N, K, "mxfp8", False)
+    asc[:], bsc[:] = 127, 127
+    if cancel:                                               # 256 * 256 - 256 * 256 in one eight and across two
+        for i, j in ((0, 5), (40, 50), (300, 500)):
+            ac[:, i], ac[:, j] = 0x78, 0xF8
+            bc[:, i] = bc[:, j] = 0x78
+    a, b = _deq(ac, asc, "mxfp8"), _deq(bc, bsc, "mxfp8")
+    want, eights = a @ b.T, np.zeros((R, N))
+    for g in range(0, K, 8):
+        eights += np.abs(a[:, None, g:g + 8] * b[None, :, g:g + 8]).max(2)
+    mag = np.abs(a) @ np.abs(b).T
+    da, db = _dev(ac, asc), tuple(t[None] for t in _dev(bc, bsc))
+    got = grouped_on(name, False, "mxfp8", da, db, _offsets([R])).double().cpu().numpy()
+    # exact - got before the rounding: 8 products of each eight, K / 8 + 8 FP32 additions
+    off = 8 * 2.0 ** -13 * eights + (K / 8 + 8) * 2.0 ** -24 * mag
+    assert np.all(np.abs(got - want) <= off + 2.0 ** -8 * (np.abs(want) + off))
