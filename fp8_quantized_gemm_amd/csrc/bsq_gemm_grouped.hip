@@ -618,15 +618,20 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 // The kernel with the least estimated time for `tiles` tiles of `steps` steps:
 // the longest of the chip's throughput over all tiles, one workgroup's own way
 // through K, and reading B at 5 TB/s (rows; a group's further row tiles find half
-// of it in cache), plus 0.3 of the other two, which overlap it only in part.  The sizes of the groups are on the
-// device; their average and 0.6 tiles of padding each are taken; a 256 x 256
-// reduction starts and ends at whole 512-element periods (MX).  Against the best
-// kernel of each shape, over 210 shapes of 1 to 8,192 rows per expert, 2 to
-// 64 experts, N 256 to 28,672, all formats and both products: within 10% of it
-// in 184, within 28% in all, and within 10% in 86 of 90 random shapes that no
-// constant was chosen by (36% at most; constants fitted more closely to the 210
-// did worse on these).  The 128 x 128 tile alone would take 2 to 5 times as long
-// for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per expert.
+// of it in cache), plus 0.3 of the other two, which overlap it only in part.  The
+// sizes of the groups are on the device; their average and 0.6 tiles of padding
+// each are taken; a 256 x 256 reduction starts and ends at whole 512-element periods
+// (MX).  The constants were chosen on 138 row products (K in multiples of 128, N of
+// 64) and 72 WGRAD ones.  On shapes that none was chosen by, the choice is within
+// 10% of the best kernel in 86 of 90 and 53 of 60 row products of such K and N (36%
+// at most), in 51 of 60 WGRAD products of M and N in multiples of 4 (38% at most),
+// and in 39 of 60 row products of any other K (twice at most).
+// Where scales are not whole dwords (gl_fits) only the direct kernels are to choose
+// from, and from 256 rows per expert on the 64 x 64 one takes 2 to 5 times as long
+// as the neighbouring multiple of 128 (8 experts of 2,048 rows, N 4,096, MXFP4: K
+// 2,880 579 us, K 2,944 155 us).  The 128 x 128 tile alone would take 2 to 5 times
+// as long for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per
+// expert.
 template <int FMT>
 int pick(const GroupedArgs& a, bool wgrad) {
   if (!gl_fits<FMT>(a)) return !wgrad && a.M / a.experts <= 16 ? kDirect16x64 : kDirect64x64;
