@@ -627,7 +627,7 @@ static_assert(kCosts[kRows256].v == k256x256 && kCosts[kRows256 + 1].v == k256x2
 // at most), in 51 of 60 WGRAD products of M and N in multiples of 4 (38% at most),
 // and in 39 of 60 row products of any other K (twice at most).
 // Where scales are not whole dwords (gl_fits) only the direct kernels are to choose
-// from, and from 256 rows per expert on the 64 x 64 one takes 2 to 5 times as long
+// from, and from 256 rows per expert on the 64 x 64 one takes 1.8 to 5 times as long
 // as the neighbouring multiple of 128 (8 experts of 2,048 rows, N 4,096, MXFP4: K
 // 2,880 579 us, K 2,944 155 us).  The 128 x 128 tile alone would take 2 to 5 times
 // as long for single tokens, the 16 x 128 tile 2 to 4 times for 1,024 rows per
