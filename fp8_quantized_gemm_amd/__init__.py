@@ -28,7 +28,10 @@ ABI_SYMBOLS = ("nvfp4_quantize", "mx_quantize", "quantize_transpose", "quantize_
                "bs_gemm_nvfp4_bx", "block_norm", "block_norm_backward_workspace",
                "block_norm_backward", "moe_rows", "moe_route_workspace", "moe_route",
                "moe_route_score_bias", "moe_route_backward", "moe_gather", "moe_combine", "moe_combine_backward",
-               "bs_gemm_grouped", "bs_gemm_grouped_wgrad", "bsq_status_string")
+               "bs_gemm_grouped", "bs_gemm_grouped_wgrad", "int8_quantize",
+               "int8_quantize_transpose_workspace", "int8_quantize_transpose", "int8_gemm",
+               "int8_linear_workspace", "int8_linear", "orthogonalize_workspace", "orthogonalize",
+               "muon_update", "bsq_status_string")
 
 
 class BsqError(RuntimeError):
@@ -79,6 +82,15 @@ def lib():
         L.moe_combine_backward.argtypes = [P, P, I64, I64, I, P, P, P, I64, P, P, P]
         L.bs_gemm_grouped.argtypes = [I, I, P, I64, I64, I64, P, P, P, P, P, P, I, P, I64, P]
         L.bs_gemm_grouped_wgrad.argtypes = [I, I, P, I64, I64, I64, P, P, P, P, P, P, P, P]
+        L.int8_quantize.argtypes = [P, I64, I64, P, P, P]
+        L.int8_quantize_transpose_workspace.argtypes = [I64, I64, P]
+        L.int8_quantize_transpose.argtypes = [P, I64, I64, P, P, P, P, P, I64, P]
+        L.int8_gemm.argtypes = [I64, I64, I64, P, P, P, P, P, P, I64, P]
+        L.int8_linear_workspace.argtypes = [I64, I64, P]
+        L.int8_linear.argtypes = [P, I64, I64, I64, P, P, P, P, I64, P, I64, P]
+        L.orthogonalize_workspace.argtypes = [I64, I64, I64, P]
+        L.orthogonalize.argtypes = [P, I, I64, I64, I64, I, P, F, P, P, I64, P]
+        L.muon_update.argtypes = [P, P, P, I64, I64, I64, F, F, I, F, F, I, P, F, P, P, P, I64, P]
         for fn in ABI_SYMBOLS[:-1]:
             getattr(L, fn).restype = I
         L.bsq_status_string.argtypes = [I]
@@ -754,3 +766,175 @@ def bs_gemm_grouped_wgrad(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_
                                      _stream(out.device))
     _check("bs_gemm_grouped_wgrad", st)
     return out
+
+
+# ---------------------------------------------------------------- 8-bit integers
+
+def int8_quantize(x):
+    """Codes of the rows of x [R, C] (bfloat16) -> (codes int8 [R, C], scales float32 [R])."""
+    x = _check_input(x)
+    R, C = x.shape
+    codes = torch.empty(R, C, dtype=torch.int8, device=x.device)
+    scales = torch.empty(R, dtype=torch.float32, device=x.device)
+    _check("int8_quantize", lib().int8_quantize(_ptr(x), R, C, _ptr(codes), _ptr(scales), _stream(x.device)))
+    return codes, scales
+
+
+def int8_quantize_transpose(x, row=True, col=True):
+    """int8_quantize of x [R, C] and of x^T.
+
+    Returns dict(row_codes int8 [R, C], row_scales float32 [R], col_codes int8 [C, R],
+    col_scales float32 [C]); the entries of a skipped orientation are None."""
+    x = _check_input(x)
+    if not (row or col):
+        raise ValueError("nothing to compute: row and col are both false")
+    (R, C), dev = x.shape, x.device
+    i8 = lambda on, *s: torch.empty(s, dtype=torch.int8, device=dev) if on else None
+    f32 = lambda on, n: torch.empty(n, dtype=torch.float32, device=dev) if on else None
+    out = dict(row_codes=i8(row, R, C), row_scales=f32(row, R), col_codes=i8(col, C, R), col_scales=f32(col, C))
+    need = _size("int8_quantize_transpose_workspace", R, C)
+    ws = _u8(need, dev)
+    _check("int8_quantize_transpose",
+           lib().int8_quantize_transpose(_ptr(x), R, C, _ptr(out["row_codes"]), _ptr(out["row_scales"]),
+                                         _ptr(out["col_codes"]), _ptr(out["col_scales"]), _ptr(ws), need, _stream(dev)))
+    return out
+
+
+def _check_int8(what, codes, scales, K):
+    """(rows) of one int8 operand: codes [rows, K] and scales float32 [rows]."""
+    if not (isinstance(codes, torch.Tensor) and codes.dtype == torch.int8 and codes.dim() == 2 and codes.shape[1] == K):
+        raise ValueError(f"{what} codes must be an int8 [rows, {K}] tensor")
+    if not (isinstance(scales, torch.Tensor) and scales.dtype == torch.float32 and scales.dim() == 1
+            and scales.shape[0] == codes.shape[0]):
+        raise ValueError(f"{what} scales must be a float32 [{codes.shape[0]}] tensor")
+    return codes.shape[0]
+
+
+def _check_bias(bias, N):
+    if bias is not None and not (isinstance(bias, torch.Tensor) and bias.dtype == torch.float32
+                                 and tuple(bias.shape) == (N,)):
+        raise ValueError(f"bias must be a float32 [{N}] tensor")
+
+
+def int8_gemm(a_codes, a_scales, b_codes, b_scales, bias=None, out=None):
+    """C [M, N] bfloat16 = (A . B^T) * a_scales[:, None] * b_scales + bias of int8 A [M, K]
+    and B [N, K] with float32 scales [M] and [N]; bias float32 [N] or None."""
+    if not (isinstance(a_codes, torch.Tensor) and a_codes.dim() == 2):
+        raise ValueError("A codes must be an int8 [rows, K] tensor")
+    K = a_codes.shape[1]
+    M, N = _check_int8("A", a_codes, a_scales, K), _check_int8("B", b_codes, b_scales, K)
+    _check_bias(bias, N)
+    if out is not None:
+        _check_out(out, M, N, torch.bfloat16)
+    _check_device(a_codes, a_scales, b_codes, b_scales, bias, out=out)
+    dev = a_codes.device
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    _check("int8_gemm", lib().int8_gemm(M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
+                                        _ptr(bias), _ptr(out), max(out.stride(0), N), _stream(dev)))
+    return out
+
+
+def int8_linear(x, w_codes, w_scales, bias=None, out=None):
+    """x [M, K] (bfloat16) quantized by rows, times int8 weights w_codes [N, K] with
+    scales [N]: [M, N] bfloat16 (int8_quantize and int8_gemm in one call)."""
+    x = _check_input(x)
+    M, K = x.shape
+    N = _check_int8("weight", w_codes, w_scales, K)
+    _check_bias(bias, N)
+    if out is not None:
+        _check_out(out, M, N, torch.bfloat16)
+    _check_device(x, w_codes, w_scales, bias, out=out)
+    dev = x.device
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+    need = _size("int8_linear_workspace", M, K)
+    ws = _u8(need, dev)
+    _check("int8_linear", lib().int8_linear(_ptr(x), M, N, K, _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(out),
+                                            max(out.stride(0), N), _ptr(ws), need, _stream(dev)))
+    return out
+
+
+# ---------------------------------------------------------------- orthogonalised updates
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+@functools.lru_cache(maxsize=64)
+def _coefs(steps, coefs):
+    """(steps, host array of 3 * steps floats) of one triple for every step or one each."""
+    try:
+        one = [tuple(float(v) for v in c) for c in (coefs if isinstance(coefs[0], tuple) else (coefs,) * steps)]
+    except (TypeError, ValueError, IndexError):
+        one = []
+    if steps < 1 or len(one) != steps or any(len(c) != 3 for c in one):
+        raise ValueError(f"coefs must be one triple (a, b, c), or one for each of the {steps} steps")
+    return (ctypes.c_float * (3 * steps))(*[v for c in one for v in c])
+
+
+def _coef_key(coefs):
+    c = tuple(coefs)
+    return tuple(tuple(v) for v in c) if c and isinstance(c[0], (tuple, list)) else c
+
+
+def _check_stack(x, what, dtypes, shape=None):
+    """(batch, rows, cols) of a contiguous matrix or stack of matrices."""
+    names = " or ".join(str(d) for d in dtypes)
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() in (2, 3) and x.dtype in dtypes and x.is_contiguous()
+            and (shape is None or x.shape == shape)):
+        want = f" {list(shape)}" if shape is not None else " 2-D or 3-D"
+        raise ValueError(f"{what} must be a contiguous{want} {names} CUDA tensor")
+    return (x.shape if x.dim() == 3 else (1, *x.shape))
+
+
+def orthogonalize(x, steps=5, coefs=NEWTON_SCHULZ, eps=1e-7, out=None):
+    """The matrix x [R, C], or each of a stack [E, R, C] (bfloat16 or float32), moved
+    towards the nearest orthogonal one by `steps` Newton-Schulz steps, bfloat16.
+
+    coefs: (a, b, c) of X <- (a I + b A + c A^2) X with A = X X^T, or one triple for
+    each step."""
+    if isinstance(x, torch.Tensor) and x.is_cuda:
+        x = x.contiguous()
+    B, R, C = _check_stack(x, "x", (torch.bfloat16, torch.float32))
+    host = _coefs(int(steps), _coef_key(coefs))
+    dev = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_stack(out, "out", (torch.bfloat16,), x.shape)
+    _check_device(x, out)
+    need = _size("orthogonalize_workspace", B, R, C)
+    ws = _u8(need, dev)
+    _check("orthogonalize", lib().orthogonalize(_ptr(x), int(x.dtype == torch.float32), B, R, C, int(steps), host,
+                                                float(eps), _ptr(out), _ptr(ws), need, _stream(dev)))
+    return out
+
+
+def muon_update(w32, momentum, grad, lr, mu=0.95, nesterov=True, weight_decay=0.0, scale=None, steps=5,
+                coefs=NEWTON_SCHULZ, eps=1e-7, w_bf16=None, amax=True):
+    """In place momentum <- mu * momentum + grad and w32 <- (1 - lr * weight_decay) * w32
+    - lr * scale * orthogonalize(u), u = grad + mu * momentum (nesterov) or momentum.
+
+    w32, momentum float32 and grad bfloat16, [R, C] or a stack [E, R, C]; scale None:
+    0.2 * sqrt(max(R, C)), which gives the update of a weight a root mean square of
+    about 0.2.  Returns dict(w_bf16, amax) as master_weight_update does."""
+    B, R, C = _check_stack(w32, "w32", (torch.float32,))
+    _check_stack(momentum, "momentum", (torch.float32,), w32.shape)
+    if not (isinstance(grad, torch.Tensor) and grad.is_cuda and grad.dtype == torch.bfloat16
+            and grad.shape == w32.shape):
+        raise ValueError("grad must be a bfloat16 CUDA tensor shaped like w32")
+    g = grad.contiguous()
+    host = _coefs(int(steps), _coef_key(coefs))
+    dev = w32.device
+    wb = torch.empty(w32.shape, dtype=torch.bfloat16, device=dev) if w_bf16 is None else w_bf16
+    _check_stack(wb, "w_bf16", (torch.bfloat16,), w32.shape)
+    _check_device(w32, momentum, g, wb)
+    a = torch.empty(1, dtype=torch.float32, device=dev) if amax else None
+    if scale is None:
+        scale = 0.2 * max(R, C) ** 0.5
+    need = _size("orthogonalize_workspace", B, R, C)
+    ws = _u8(need, dev)
+    _check("muon_update", lib().muon_update(_ptr(w32), _ptr(momentum), _ptr(g), B, R, C, float(lr), float(mu),
+                                            1 if nesterov else 0, float(weight_decay), float(scale), int(steps), host,
+                                            float(eps), _ptr(wb), _ptr(a), _ptr(ws), need, _stream(dev)))
+    return dict(w_bf16=wb, amax=a)

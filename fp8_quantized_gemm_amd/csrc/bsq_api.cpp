@@ -204,6 +204,41 @@ bsq_status grouped_format(bsq_format fmt, bsq::Fmt* f) {
   return BSQ_OK;
 }
 
+// Checks shared by int8_gemm and int8_linear (a: the codes or x, elem bytes each).
+bsq_status int8_checks(int64_t M, int64_t N, int64_t K, const void* a, int elem, const int8_t* b,
+                       const float* b_scales, const float* bias, const void* c, int64_t ldc) {
+  if (M < 0 || N < 0 || K < 0 || ldc < N) return BSQ_EINVAL;
+  if (K >= (1 << 17)) return BSQ_EUNSUPPORTED;
+  if (too_many(M, K) || too_many(N, K) || too_many(M, ldc)) return BSQ_EINVAL;
+  if (M > ((int64_t)1 << 34) || N > ((int64_t)1 << 34)) return BSQ_EINVAL;
+  if (M == 0 || N == 0) return BSQ_OK;
+  if (!b_scales || !c || !aligned4(b_scales) || !aligned4(bias) || !aligned2(c)) return BSQ_EINVAL;
+  if (K > 0 && (!a || !b || !aligned16(a) || !aligned16(b))) return BSQ_EINVAL;
+  const int64_t cb = ((M - 1) * ldc + N) * 2;
+  if (overlap(c, cb, a, M * K * elem) || overlap(c, cb, b, N * K) || overlap(c, cb, b_scales, N * 4) ||
+      (bias && overlap(c, cb, bias, N * 4)))
+    return BSQ_EINVAL;
+  return BSQ_OK;
+}
+
+int64_t int8_linear_bytes(int64_t M, int64_t K) { return (M * K + 15) / 16 * 16 + M * 4; }
+
+// Sizes of orthogonalize and muon_update; *bytes is the workspace's size (0: nothing to do).
+bsq_status ortho_checks(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes) {
+  if (batch < 0 || rows < 0 || cols < 0 || too_many(rows, cols) || too_many(batch, rows * cols)) return BSQ_EINVAL;
+  *bytes = 0;
+  if (batch == 0 || rows == 0 || cols == 0) return BSQ_OK;
+  if (rows >= ((int64_t)1 << 22) || cols >= ((int64_t)1 << 22) || batch > 65535) return BSQ_EUNSUPPORTED;
+  *bytes = bsq::ortho_workspace_bytes(batch, rows, cols);
+  return *bytes < 0 ? BSQ_EUNSUPPORTED : BSQ_OK;
+}
+
+bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+bsq_status ortho_params(int steps, const float* coefs, float eps) {
+  return steps < 1 || steps > 32 || !coefs || !(eps > 0.0f) ? BSQ_EINVAL : BSQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -671,6 +706,142 @@ bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* off
   const bsq::GroupedArgs a{f, experts, offsets, M, N, rows, a_codes, a_scales, a_amax,
                            b_codes, b_scales, b_amax, 1, c, N};
   return hip_status(bsq::launch_gemm_grouped_wgrad(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status int8_quantize(const void* x, int64_t rows, int64_t cols, int8_t* codes, float* scales, void* stream) {
+  if (rows < 0 || cols < 0 || too_many(rows, cols)) return BSQ_EINVAL;
+  if (rows == 0) return BSQ_OK;
+  if (!scales || !aligned4(scales)) return BSQ_EINVAL;
+  if (cols > 0 && (!x || !codes || !aligned16(x) || !aligned16(codes))) return BSQ_EINVAL;
+  if (overlap(codes, rows * cols, x, rows * cols * 2) || overlap(scales, rows * 4, x, rows * cols * 2) ||
+      overlap(scales, rows * 4, codes, rows * cols))
+    return BSQ_EINVAL;
+  return hip_status(bsq::launch_i8_rows(x, rows, cols, reinterpret_cast<uint8_t*>(codes), scales,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+bsq_status int8_quantize_transpose_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  if (!bytes || rows < 0 || cols < 0 || too_many(rows, cols)) return BSQ_EINVAL;
+  *bytes = rows * cols == 0 ? 0 : (rows + cols) * 4;
+  return BSQ_OK;
+}
+
+bsq_status int8_quantize_transpose(const void* x, int64_t rows, int64_t cols, int8_t* codes_row, float* scales_row,
+                                   int8_t* codes_col, float* scales_col, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+  int64_t need = 0;
+  const bsq_status st = int8_quantize_transpose_workspace(rows, cols, &need);
+  if (st != BSQ_OK) return st;
+  if (!aligned4(scales_row) || !aligned4(scales_col)) return BSQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows * cols == 0) {                      // rows (columns) of nothing have scale 1
+    if (rows > 0 && scales_row) {
+      if (bsq::launch_i8_rows(nullptr, rows, 0, nullptr, scales_row, s) != hipSuccess) return BSQ_EHIP;
+    }
+    if (cols > 0 && scales_col) return hip_status(bsq::launch_i8_rows(nullptr, cols, 0, nullptr, scales_col, s));
+    return BSQ_OK;
+  }
+  if ((codes_row == nullptr) != (scales_row == nullptr) || (codes_col == nullptr) != (scales_col == nullptr) ||
+      (!codes_row && !codes_col))
+    return BSQ_EINVAL;
+  if (!x || !aligned16(x) || !aligned16_or_null(codes_row) || !aligned16_or_null(codes_col)) return BSQ_EINVAL;
+  if (!workspace || !aligned4(workspace) || workspace_bytes < need) return BSQ_EINVAL;
+  const void* part[] = {x, codes_row, scales_row, codes_col, scales_col, workspace};
+  const int64_t size[] = {rows * cols * 2, rows * cols, rows * 4, rows * cols, cols * 4, need};
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (part[i] && part[j] && overlap(part[i], size[i], part[j], size[j])) return BSQ_EINVAL;
+  return hip_status(bsq::launch_i8_qt(x, rows, cols, reinterpret_cast<uint8_t*>(codes_row), scales_row,
+                                      reinterpret_cast<uint8_t*>(codes_col), scales_col,
+                                      static_cast<uint32_t*>(workspace), s));
+}
+
+bsq_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a_codes, const float* a_scales,
+                     const int8_t* b_codes, const float* b_scales, const float* bias, void* c, int64_t ldc,
+                     void* stream) {
+  const bsq_status st = int8_checks(M, N, K, a_codes, 1, b_codes, b_scales, bias, c, ldc);
+  if (st != BSQ_OK || M == 0 || N == 0) return st;
+  if (!a_scales || !aligned4(a_scales) || overlap(c, ((M - 1) * ldc + N) * 2, a_scales, M * 4)) return BSQ_EINVAL;
+  const bsq::Int8Args a{M, N, K, reinterpret_cast<const uint8_t*>(a_codes), a_scales,
+                        reinterpret_cast<const uint8_t*>(b_codes), b_scales, bias, c, ldc};
+  return hip_status(bsq::launch_i8_gemm(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes) {
+  if (!bytes || M < 0 || K < 0 || too_many(M, K)) return BSQ_EINVAL;
+  *bytes = int8_linear_bytes(M, K);
+  return BSQ_OK;
+}
+
+bsq_status int8_linear(const void* x, int64_t M, int64_t N, int64_t K, const int8_t* w_codes, const float* w_scales,
+                       const float* bias, void* c, int64_t ldc, void* workspace, int64_t workspace_bytes,
+                       void* stream) {
+  const bsq_status st = int8_checks(M, N, K, x, 2, w_codes, w_scales, bias, c, ldc);
+  if (st != BSQ_OK || M == 0 || N == 0) return st;
+  const int64_t need = int8_linear_bytes(M, K);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return BSQ_EINVAL;
+  if (overlap(workspace, need, x, M * K * 2) || overlap(workspace, need, w_codes, N * K) ||
+      overlap(workspace, need, w_scales, N * 4) || (bias && overlap(workspace, need, bias, N * 4)) ||
+      overlap(workspace, need, c, ((M - 1) * ldc + N) * 2))
+    return BSQ_EINVAL;
+  uint8_t* codes = static_cast<uint8_t*>(workspace);
+  float* scales = reinterpret_cast<float*>(codes + (M * K + 15) / 16 * 16);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (bsq::launch_i8_rows(x, M, K, codes, scales, s) != hipSuccess) return BSQ_EHIP;
+  const bsq::Int8Args a{M, N, K, codes, scales, reinterpret_cast<const uint8_t*>(w_codes), w_scales, bias, c, ldc};
+  return hip_status(bsq::launch_i8_gemm(a, s));
+}
+
+bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes) {
+  return bytes ? ortho_checks(batch, rows, cols, bytes) : BSQ_EINVAL;
+}
+
+bsq_status orthogonalize(const void* x, bsq_dtype type, int64_t batch, int64_t rows, int64_t cols, int steps,
+                         const float* coefs, float eps, void* out, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  int64_t need = 0;
+  bsq_status st = ortho_checks(batch, rows, cols, &need);
+  if (st == BSQ_OK) st = ortho_params(steps, coefs, eps);
+  if (st != BSQ_OK) return st;
+  if (!valid_dtype(type)) return BSQ_EINVAL;
+  if (need == 0) return BSQ_OK;
+  if (!x || !out || !aligned_elem(x, type == BSQ_F32) || !aligned2(out)) return BSQ_EINVAL;
+  if (!workspace || !aligned256(workspace) || workspace_bytes < need) return BSQ_EINVAL;
+  const int64_t n = batch * rows * cols, xb = n * (type == BSQ_F32 ? 4 : 2);
+  if (overlap(out, n * 2, x, xb) || overlap(workspace, need, x, xb) || overlap(workspace, need, out, n * 2))
+    return BSQ_EINVAL;
+  bsq::OrthoArgs a{};
+  a.batch = batch, a.rows = rows, a.cols = cols, a.steps = steps, a.coefs = coefs, a.eps = eps;
+  a.workspace = workspace, a.x = x, a.f32 = type == BSQ_F32, a.out = out;
+  return hip_status(bsq::launch_ortho(a, static_cast<hipStream_t>(stream)));
+}
+
+bsq_status muon_update(float* w32, float* momentum, const void* grad, int64_t batch, int64_t rows, int64_t cols,
+                       float lr, float mu, int nesterov, float weight_decay, float scale, int steps,
+                       const float* coefs, float eps, void* w_bf16, float* amax, void* workspace,
+                       int64_t workspace_bytes, void* stream) {
+  int64_t need = 0;
+  bsq_status st = ortho_checks(batch, rows, cols, &need);
+  if (st == BSQ_OK) st = ortho_params(steps, coefs, eps);
+  if (st != BSQ_OK) return st;
+  if (!aligned4(amax)) return BSQ_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (need == 0) return amax ? hip_status(bsq::launch_zero_amax(amax, nullptr, s)) : BSQ_OK;
+  if (!w32 || !momentum || !grad || !w_bf16 || !aligned4(w32) || !aligned4(momentum) || !aligned2(grad) ||
+      !aligned2(w_bf16))
+    return BSQ_EINVAL;
+  if (!workspace || !aligned256(workspace) || workspace_bytes < need) return BSQ_EINVAL;
+  const int64_t n = batch * rows * cols;
+  const void* part[] = {w32, momentum, grad, w_bf16, amax, workspace};
+  const int64_t size[] = {n * 4, n * 4, n * 2, n * 2, 4, need};
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (part[i] && part[j] && overlap(part[i], size[i], part[j], size[j])) return BSQ_EINVAL;
+  bsq::OrthoArgs a{};
+  a.batch = batch, a.rows = rows, a.cols = cols, a.steps = steps, a.coefs = coefs, a.eps = eps;
+  a.workspace = workspace, a.w = w32, a.momentum = momentum, a.grad = grad, a.mu = mu, a.nesterov = nesterov != 0;
+  a.keep = 1.0f - lr * weight_decay, a.step = lr * scale, a.w_bf16 = w_bf16, a.amax = amax;
+  return hip_status(bsq::launch_ortho(a, s));
 }
 
 }  // extern "C"

@@ -1,0 +1,323 @@
+// 8-bit integer quantizers and products for gfx950 (contract in include/bsq.h):
+//   codes = RNE(x s_enc), s_enc = 127 / amax of the row (or column)
+//   C = BF16(FP32(A . B^T) (sa sb) + bias)
+#include "bsq_device.hpp"
+#include "bsq_nt.hpp"
+#include "bsq_wave.hpp"
+
+namespace bsq {
+
+namespace {
+
+// ---------------------------------------------------------------- encode
+
+__device__ __forceinline__ float i8_enc(uint32_t amax_bits) {
+  const float amax = u2f(amax_bits);
+  return amax == 0.0f ? 1.0f : fminf(127.0f / amax, kFltMax);
+}
+// x s rounded to the nearest even integer, in the low byte: adding 1.5 2^23 leaves
+// no bits below the unit.  |x s| <= 127.5 by the choice of s, so nothing saturates.
+__device__ __forceinline__ uint32_t i8_code(float x, float s) { return f2u(x * s + 12582912.0f); }
+__device__ __forceinline__ uint32_t i8_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint32_t lo = __builtin_amdgcn_perm(b, a, 0x0C0C0400u), hi = __builtin_amdgcn_perm(d, c, 0x0C0C0400u);
+  return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+__device__ __forceinline__ uint32_t max_abs(const Raw<uint16_t>& r) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, r.v[0][i] & 0x7FFF7FFFu));
+  return (uint32_t)max(m.x, m.y) << 16;
+}
+
+// Rows: a group of T threads per row, which stays in registers (P pieces of eight
+// columns each) between the maximum and the encoding, so x is read once.  Bound by
+// HBM: 2 bytes in, 1 out.
+template <bool AL, int T, int P>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_i8_rows(const uint16_t* __restrict__ x, int64_t rows, int cols,
+                                                             uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  constexpr int WG = T < 256 ? 256 : T, G = WG / T;
+  __shared__ uint32_t part[WG / 64];
+  const int t = threadIdx.x % T, w = threadIdx.x >> 6;
+  const int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / T;
+  const bool live = row < rows;                            // G > 1: T is one wave, so a group leaves together
+  if (T <= 64 && !live) return;
+  const uint16_t* src = x + row * cols;
+  Raw<uint16_t> r[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) r[p] = load_raw<AL>(src, (p * T + t) * 8, cols);
+  uint32_t m = 0;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    end_piece<AL>(r[p], (p * T + t) * 8, cols);
+    m = max(m, max_abs(r[p]));
+  }
+  m = wave_max_dpp(m);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) part[w] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < T / 64; ++i) m = max(m, part[i]);
+  }
+  const float s = i8_enc(m);
+  if (t == 0) scales[row] = 1.0f / s;
+  uint8_t* dst = codes + row * cols;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int col = (p * T + t) * 8;
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = i8_code(raw_at(r[p], j), s);
+    if (col + 8 <= cols) {
+      typedef ntu2 Any __attribute__((aligned(1)));
+      const ntu2 v = {i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7])};
+      if (AL) *reinterpret_cast<ntu2*>(dst + col) = v;
+      else *reinterpret_cast<Any*>(dst + col) = v;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (col + j < cols) dst[col + j] = (uint8_t)c[j];
+    }
+  }
+}
+
+// Rows longer than a workgroup's registers hold: two passes, the second mostly from cache.
+__global__ __launch_bounds__(1024) void k_i8_rows_long(const uint16_t* __restrict__ x, int64_t cols,
+                                                      uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ uint32_t part[16];
+  const int64_t row = blockIdx.x;
+  const uint16_t* src = x + row * cols;
+  uint32_t m = 0;
+  for (int64_t c = threadIdx.x; c < cols; c += 1024) m = max(m, (uint32_t)(src[c] & 0x7FFF) << 16);
+  m = wave_max_dpp(m);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = max(m, part[i]);
+  const float s = i8_enc(m);
+  if (threadIdx.x == 0) scales[row] = 1.0f / s;
+  for (int64_t c = threadIdx.x; c < cols; c += 1024)
+    codes[row * cols + c] = (uint8_t)i8_code(u2f((uint32_t)src[c] << 16), s);
+}
+
+template <bool AL, int T, int P>
+hipError_t run_rows(const void* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales, hipStream_t s) {
+  constexpr int WG = T < 256 ? 256 : T, G = WG / T;
+  const int64_t blocks = (rows + G - 1) / G;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_i8_rows<AL, T, P>), dim3((unsigned)blocks), dim3(WG), 0, s, static_cast<const uint16_t*>(x), rows,
+                     (int)cols, codes, scales);
+  return hipGetLastError();
+}
+template <bool AL>
+hipError_t run_rows_any(const void* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales, hipStream_t s) {
+  if (cols <= 512) return run_rows<AL, 64, 1>(x, rows, cols, codes, scales, s);
+  if (cols <= 1024) return run_rows<AL, 64, 2>(x, rows, cols, codes, scales, s);
+  if (cols <= 2048) return run_rows<AL, 64, 4>(x, rows, cols, codes, scales, s);
+  if (cols <= 8192) return run_rows<AL, 256, 4>(x, rows, cols, codes, scales, s);
+  if (cols <= 16384) return run_rows<AL, 256, 8>(x, rows, cols, codes, scales, s);
+  if (cols <= 65536) return run_rows<AL, 1024, 8>(x, rows, cols, codes, scales, s);
+  if (rows > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(k_i8_rows_long, dim3((unsigned)rows), dim3(1024), 0, s, static_cast<const uint16_t*>(x), cols, codes,
+                     scales);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- rows and columns
+
+__global__ __launch_bounds__(256) void k_i8_zero(uint32_t* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) p[i] = 0;
+}
+
+// Maxima of 256 rows x 512 columns into amax_row [rows] and amax_col [cols] (bits of
+// FP32, cleared before; a maximum does not depend on the order of the atomics).
+constexpr int kAmaxRows = 256, kAmaxCols = 512;
+template <bool AL>
+__global__ __launch_bounds__(256) void k_i8_amax(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int strips,
+                                                 uint32_t* amax_row, uint32_t* amax_col) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  __shared__ uint32_t rmax[kAmaxRows];
+  __shared__ uint32_t cmax[4][kAmaxCols / 2];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t r0 = (int64_t)(blockIdx.x / strips) * kAmaxRows, c0 = (int64_t)(blockIdx.x % strips) * kAmaxCols;
+  const int nr = (int)min((int64_t)kAmaxRows, rows - r0);
+  const int64_t col = c0 + lane * 8;
+  u16x2 cm[4] = {{0, 0}, {0, 0}, {0, 0}, {0, 0}};
+  constexpr int U = 8;
+  for (int i0 = w; i0 < kAmaxRows; i0 += 4 * U) {
+    ntu4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + 4 * u;
+      v[u] = ntu4{0u, 0u, 0u, 0u};
+      if (i < nr && col < cols) {
+        const uint16_t* src = x + (r0 + i) * cols + col;
+        if (AL) {
+          v[u] = *reinterpret_cast<const ntu4*>(src);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col + j < cols) v[u][j >> 1] |= (uint32_t)src[j] << (16 * (j & 1));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      u16x2 rm = {0, 0};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const u16x2 a = __builtin_bit_cast(u16x2, v[u][k] & 0x7FFF7FFFu);
+        cm[k] = __builtin_elementwise_max(cm[k], a);
+        rm = __builtin_elementwise_max(rm, a);
+      }
+      const uint32_t m = wave_max_dpp((uint32_t)max(rm.x, rm.y));
+      if (lane == 0 && i0 + 4 * u < kAmaxRows) rmax[i0 + 4 * u] = m << 16;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) cmax[w][lane * 4 + k] = __builtin_bit_cast(uint32_t, cm[k]);
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < nr) atomicMax(amax_row + r0 + t, rmax[t]);
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, cmax[i][t]));
+  const int64_t c = c0 + 2 * t;
+  if (c < cols) atomicMax(amax_col + c, (uint32_t)m.x << 16);
+  if (c + 1 < cols) atomicMax(amax_col + c + 1, (uint32_t)m.y << 16);
+}
+
+// Codes of a 128 x 128 tile under the rows' and the columns' maxima.  A thread owns 8
+// rows x 8 columns: the row codes go straight out as 128-byte pieces; the column
+// codes, which have scales of their own, are packed along the rows and turned in LDS.
+constexpr int kQtT = 128, kQtLd = kQtT + 8;
+template <bool AL>
+__global__ __launch_bounds__(256) void k_i8_qt(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int tiles_c,
+                                               const uint32_t* __restrict__ amax_row, const uint32_t* __restrict__ amax_col,
+                                               uint8_t* __restrict__ codes_row, float* __restrict__ scales_row,
+                                               uint8_t* __restrict__ codes_col, float* __restrict__ scales_col) {
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kQtT * kQtLd];
+  __shared__ float enc[2 * kQtT];
+  const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
+  const int tr = (int)(blockIdx.x / tiles_c), tc = (int)(blockIdx.x % tiles_c);
+  const int64_t r0 = (int64_t)tr * kQtT, c0 = (int64_t)tc * kQtT;
+  const int64_t col = c0 + tx * 8;
+  ntu4 v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + ty * 8 + i;
+    v[i] = ntu4{0u, 0u, 0u, 0u};
+    if (r < rows && col < cols) {
+      const uint16_t* src = x + r * cols + col;
+      if (AL) {
+        v[i] = *reinterpret_cast<const ntu4*>(src);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < cols) v[i][j >> 1] |= (uint32_t)src[j] << (16 * (j & 1));
+      }
+    }
+  }
+  {
+    const bool is_row = t < kQtT;
+    const int64_t i = is_row ? r0 + t : c0 + t - kQtT, n = is_row ? rows : cols;
+    const float s = i < n ? i8_enc(is_row ? amax_row[i] : amax_col[i]) : 0.0f;
+    enc[t] = s;
+    if (i < n && is_row && tc == 0 && codes_row) scales_row[i] = 1.0f / s;
+    if (i < n && !is_row && tr == 0 && codes_col) scales_col[i] = 1.0f / s;
+  }
+  __syncthreads();
+  const auto at = [&](int i, int j) { return (j & 1) ? bf16_hi(v[i][j >> 1]) : bf16_lo(v[i][j >> 1]); };
+  if (codes_row) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + ty * 8 + i;
+      const float s = enc[ty * 8 + i];
+      uint32_t c[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c[j] = i8_code(at(i, j), s);
+      if (r >= rows || col >= cols) continue;
+      uint8_t* dst = codes_row + r * cols + col;
+      if (AL) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < cols) dst[j] = (uint8_t)c[j];
+      }
+    }
+  }
+  if (codes_col) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = enc[kQtT + tx * 8 + j];
+      uint32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = i8_code(at(i, j), s);
+      *reinterpret_cast<uint2*>(tile + (tx * 8 + j) * kQtLd + ty * 8) =
+          make_uint2(i8_pack4(c[0], c[1], c[2], c[3]), i8_pack4(c[4], c[5], c[6], c[7]));
+    }
+    __syncthreads();
+    const bool whole = (rows & 7) == 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = i * 16 + ty;                           // the tile's column
+      const int64_t c = c0 + q, r = r0 + tx * 8;
+      if (c >= cols || r >= rows) continue;
+      const uint2 u = *reinterpret_cast<const uint2*>(tile + q * kQtLd + tx * 8);
+      uint8_t* dst = codes_col + c * rows + r;
+      if (whole) {
+        *reinterpret_cast<uint2*>(dst) = u;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (r + j < rows) dst[j] = (uint8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3)));
+      }
+    }
+  }
+}
+
+template <int MI, int NI, int WM, int WN, int WK>
+hipError_t run_direct(const Int8Args& a, hipStream_t s) {
+  const NtArgs g{a.ac, a.bc, a.M, a.N, (uint32_t)a.K, 0, 0, 1, false};
+  const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+  const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec};
+  return run_nt_direct<kNtI8, MI, NI, WM, WN, WK>(g, e, s);
+}
+
+}  // namespace
+
+hipError_t launch_i8_rows(const void* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales, hipStream_t s) {
+  const bool al = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
+  return al ? run_rows_any<true>(x, rows, cols, codes, scales, s) : run_rows_any<false>(x, rows, cols, codes, scales, s);
+}
+
+hipError_t launch_i8_qt(const void* x, int64_t rows, int64_t cols, uint8_t* codes_row, float* scales_row,
+                        uint8_t* codes_col, float* scales_col, uint32_t* amax, hipStream_t s) {
+  const int64_t n = rows + cols, strips = (cols + kAmaxCols - 1) / kAmaxCols;
+  const int64_t ab = strips * ((rows + kAmaxRows - 1) / kAmaxRows), tiles_c = (cols + kQtT - 1) / kQtT;
+  const int64_t qb = tiles_c * ((rows + kQtT - 1) / kQtT);
+  if (ab > 0x7FFFFFFF || qb > 0x7FFFFFFF || (n + 255) / 256 > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const uint16_t* xp = static_cast<const uint16_t*>(x);
+  uint32_t *ar = amax, *ac = amax + rows;
+  hipLaunchKernelGGL(k_i8_zero, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, amax, n);
+  const bool al = cols % 8 == 0;
+  if (al) {
+    hipLaunchKernelGGL(k_i8_amax<true>, dim3((unsigned)ab), dim3(256), 0, s, xp, rows, cols, (int)strips, ar, ac);
+    hipLaunchKernelGGL(k_i8_qt<true>, dim3((unsigned)qb), dim3(256), 0, s, xp, rows, cols, (int)tiles_c, ar, ac, codes_row,
+                       scales_row, codes_col, scales_col);
+  } else {
+    hipLaunchKernelGGL(k_i8_amax<false>, dim3((unsigned)ab), dim3(256), 0, s, xp, rows, cols, (int)strips, ar, ac);
+    hipLaunchKernelGGL(k_i8_qt<false>, dim3((unsigned)qb), dim3(256), 0, s, xp, rows, cols, (int)tiles_c, ar, ac, codes_row,
+                       scales_row, codes_col, scales_col);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s) {
+  if (a.M <= 16) return run_direct<1, 4, 1, 1, 4>(a, s);
+  return run_direct<4, 4, 1, 1, 4>(a, s);
+}
+
+}  // namespace bsq

@@ -261,4 +261,50 @@ hipError_t launch_gemm_nvfp4_rx_grouped(const GroupedArgs& a, bool wgrad, hipStr
 bool gemm_mx_rx_grouped_fits(const GroupedArgs& a, bool wgrad);
 hipError_t launch_gemm_mx_rx_grouped(const GroupedArgs& a, bool wgrad, hipStream_t s);
 
+// ---------------------------------------------------------------- 8-bit integers
+
+// Codes [rows, cols] and decode scales [rows] of the rows of x (BF16).
+hipError_t launch_i8_rows(const void* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales, hipStream_t s);
+// Row codes [rows, cols] and column codes [cols, rows] (either pair may be null)
+// under maxima formed in amax, rows + cols words of device memory.  x 16-byte aligned.
+hipError_t launch_i8_qt(const void* x, int64_t rows, int64_t cols, uint8_t* codes_row, float* scales_row,
+                        uint8_t* codes_col, float* scales_col, uint32_t* amax, hipStream_t s);
+
+struct Int8Args {
+  int64_t M, N, K;                // 0 < K < 2^17
+  const uint8_t* ac;              // [M, K]
+  const float* as;                // [M]
+  const uint8_t* bc;              // [N, K]
+  const float* bs;                // [N]
+  const float* bias;              // [N] or null
+  void* c;                        // BF16 [M, N]
+  int64_t ldc;
+};
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s);
+
+// ---------------------------------------------------------------- orthogonalisation
+
+struct OrthoArgs {
+  int64_t batch, rows, cols;      // a stack of matrices, contiguous
+  int steps;
+  const float* coefs;             // host: 3 per step
+  float eps;
+  void* workspace;
+  // the matrix to orthogonalise: x (BF16, or FP32 when f32), or the moment of an update
+  const void* x;
+  bool f32;
+  void* out;                      // BF16
+  // an update (w not null)
+  float* w;
+  float* momentum;
+  const void* grad;               // BF16
+  float mu;
+  bool nesterov;
+  float keep, step;               // w <- keep w - step O
+  void* w_bf16;
+  float* amax;                    // or null; cleared here
+};
+int64_t ortho_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);   // -1: too large
+hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);
+
 }  // namespace bsq

@@ -530,6 +530,100 @@ bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* off
                                  const float* a_amax, const uint8_t* b_codes, const uint8_t* b_scales,
                                  const float* b_amax, void* c, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit integers: another baseline of the block's products, with a scale for each
+ * token (row of A) and each output channel (row of B) instead of one per tensor or
+ * block.  The pages give no formulas, so the usual definitions are used.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Codes of the rows of x[rows, cols] (BF16), one scale per row:
+ *   amax = max|x| of the row; s_enc = 127/amax (FP32; 1 if amax == 0; <= FLT_MAX);
+ *   scale = 1/s_enc; code = RNE(x * s_enc), in [-127, 127]
+ * (FP32 IEEE RNE at every step).  NaN and infinities touch their own row only.
+ *   codes  : out, int8 [rows, cols].  scales : out, FP32 [rows].
+ * Any rows, any cols.
+ */
+bsq_status int8_quantize(const void* x, int64_t rows, int64_t cols, int8_t* codes, float* scales,
+                         void* stream);
+
+/* Bytes of device workspace int8_quantize_transpose needs. */
+bsq_status int8_quantize_transpose_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * int8_quantize of x and of x^T, for products over either dimension (FPROP, DGRAD
+ * and WGRAD of a training step):
+ *   codes_row [rows, cols], scales_row [rows]; codes_col [cols, rows], scales_col [cols].
+ * Either pair may be NULL (not both).  workspace: device memory, 4-byte aligned.
+ */
+bsq_status int8_quantize_transpose(const void* x, int64_t rows, int64_t cols, int8_t* codes_row,
+                                   float* scales_row, int8_t* codes_col, float* scales_col,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * C[m, n] = BF16(FP32(sum_k A[m, k] B[n, k]) * (a_scales[m] * b_scales[n]) + bias[n])
+ * with A int8 [M, K] and B int8 [N, K], the sum exact, so that the result depends on
+ * the operands alone.  K == 0: the bias (or zeros).
+ *   bias : in, FP32 [N] or NULL.   c : out, BF16 [M, N], row stride ldc >= N.
+ * K < 2^17 (the sums are 32 bits): BSQ_EUNSUPPORTED above.  C must not alias an input.
+ */
+bsq_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a_codes, const float* a_scales,
+                     const int8_t* b_codes, const float* b_scales, const float* bias, void* c,
+                     int64_t ldc, void* stream);
+
+/* Bytes of device workspace int8_linear needs (the codes and scales of x). */
+bsq_status int8_linear_workspace(int64_t M, int64_t K, int64_t* bytes);
+
+/*
+ * The serving form: C = int8_gemm of int8_quantize(x) with weights quantized
+ * beforehand, for one token or many.
+ *   x : in, BF16 [M, K].   w_codes, w_scales, bias, c, ldc : as for int8_gemm's B.
+ *   workspace : device memory, 16-byte aligned.
+ */
+bsq_status int8_linear(const void* x, int64_t M, int64_t N, int64_t K, const int8_t* w_codes,
+                       const float* w_scales, const float* bias, void* c, int64_t ldc,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Orthogonalised weight updates (Newton-Schulz products), beside
+ * master_weight_update.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of device workspace orthogonalize and muon_update need (BSQ_EUNSUPPORTED for
+ * sizes they do not take: rows or cols of 2^22 or more, batch above 65,535). */
+bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * For each matrix x[rows, cols] of a stack of `batch`:
+ *   X = x / (||x||_F + eps); for each step's a, b, c: A = X X^T,
+ *   X <- (a I + b A + c A^2) X;  out = BF16(X)
+ * (on the transpose where rows > cols, which is the same).  Between products X, A
+ * and the polynomials are FP16 under powers of two (each rounding at most 2^-11 of
+ * the value), sums FP32, the norm FP64; coefficients must keep singular values below
+ * 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of its own.
+ *   x     : in, [batch, rows, cols] of type.   out : out, BF16 [batch, rows, cols].
+ *   coefs : in, HOST array of 3 * steps floats, 1 <= steps <= 32.   eps > 0.
+ *   workspace : device memory, 256-byte aligned.
+ */
+bsq_status orthogonalize(const void* x, bsq_dtype type, int64_t batch, int64_t rows, int64_t cols,
+                         int steps, const float* coefs, float eps, void* out, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/*
+ * One optimizer step of a stack of weight matrices, in place on w32 and momentum:
+ *   momentum <- mu * momentum + grad;   u = grad + mu * momentum (nesterov) or momentum
+ *   w32 <- (1 - lr * weight_decay) * w32 - lr * scale * orthogonalize(u)
+ *   w_bf16 <- BF16_RNE(w32);  amax <- max|w_bf16| over the stack
+ * (FP32; orthogonalize's result rounded to FP16 here).  amax is the per-tensor amax of
+ * the next weight quantization, as for master_weight_update.
+ *   w32, momentum : in/out, FP32 [batch, rows, cols].  grad : in, BF16.
+ *   w_bf16 : out, BF16.  amax : out, device FP32 or NULL.  No two may overlap.
+ */
+bsq_status muon_update(float* w32, float* momentum, const void* grad, int64_t batch, int64_t rows,
+                       int64_t cols, float lr, float mu, int nesterov, float weight_decay, float scale,
+                       int steps, const float* coefs, float eps, void* w_bf16, float* amax,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code; host-side, thread-safe. */
 const char* bsq_status_string(bsq_status status);
 
