@@ -1,8 +1,9 @@
 // 8-bit integer quantizers and products for gfx950 (contract in include/bsq.h):
-//   codes = RNE(x s_enc), s_enc = 127 / amax of the row (or column)
+//   codes = RNE(x s_enc), s_enc = 127 (1 / amax) of the row (or column)
 //   C = BF16(FP32(A . B^T) (sa sb) + bias)
 #include "bsq_device.hpp"
 #include "bsq_nt.hpp"
+#include "bsq_nt_ring.hpp"
 #include "bsq_wave.hpp"
 
 namespace bsq {
@@ -13,7 +14,7 @@ namespace {
 
 __device__ __forceinline__ float i8_enc(uint32_t amax_bits) {
   const float amax = u2f(amax_bits);
-  return amax == 0.0f ? 1.0f : fminf(127.0f / amax, kFltMax);
+  return amax == 0.0f ? 1.0f : fminf(127.0f * (1.0f / amax), kFltMax);
 }
 // x s rounded to the nearest even integer, in the low byte: adding 1.5 2^23 leaves
 // no bits below the unit.  |x s| <= 127.5 by the choice of s, so nothing saturates.
@@ -278,12 +279,9 @@ __global__ __launch_bounds__(256) void k_i8_qt(const uint16_t* __restrict__ x, i
   }
 }
 
-template <int MI, int NI, int WM, int WN, int WK>
-hipError_t run_direct(const Int8Args& a, hipStream_t s) {
-  const NtArgs g{a.ac, a.bc, a.M, a.N, (uint32_t)a.K, 0, 0, 1, false};
-  const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
-  const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec};
-  return run_nt_direct<kNtI8, MI, NI, WM, WN, WK>(g, e, s);
+template <int NT, int NB>
+hipError_t run_ring(const NtArgs& g, const EpiI8& e, hipStream_t s) {
+  return g.kb % 128 == 0 ? run_nt_ring<kNtI8, NT, NB, false>(g, e, s) : run_nt_ring<kNtI8, NT, NB, true>(g, e, s);
 }
 
 }  // namespace
@@ -315,9 +313,29 @@ hipError_t launch_i8_qt(const void* x, int64_t rows, int64_t cols, uint8_t* code
   return hipGetLastError();
 }
 
-hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s) {
-  if (a.M <= 16) return run_direct<1, 4, 1, 1, 4>(a, s);
-  return run_direct<4, 4, 1, 1, 4>(a, s);
+namespace {
+NtArgs i8_args(const Int8Args& a) { return NtArgs{a.ac, a.bc, a.M, a.N, (uint32_t)a.K, 0, 0, 1, false}; }
+}  // namespace
+
+int i8_kernel(const Int8Args& a) {
+  const NtArgs g = i8_args(a);
+  return nt_choose(g, true, ring_fits(g));
+}
+
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel) {
+  const NtArgs g = i8_args(a);
+  const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+  const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec};
+  switch (kernel == kNtChosen ? i8_kernel(a) : kernel) {
+    case kNtDirect16x64: return run_nt_direct<kNtI8, 1, 4, 1, 1, 4>(g, e, s);
+    case kNtDirect64x64: return run_nt_direct<kNtI8, 4, 4, 1, 1, 4>(g, e, s);
+    case kNtRing128: return run_ring<4, 2>(g, e, s);
+    case kNtRing64: return run_ring<2, 4>(g, e, s);
+    case kNtRing128x5: return run_ring<4, 5>(g, e, s);
+    case kNtRing192: return run_ring<6, 3>(g, e, s);
+    case kNtRing256: return run_ring<8, 2>(g, e, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace bsq

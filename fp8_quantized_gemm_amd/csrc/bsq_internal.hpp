@@ -280,7 +280,22 @@ struct Int8Args {
   void* c;                        // BF16 [M, N]
   int64_t ldc;
 };
-hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s);
+// The kernels of the plain products (8-bit integers, and the FP16 products of the
+// orthogonalisation), by output tile.
+enum NtKernel {
+  kNtChosen = -1,
+  kNtDirect16x64,          // direct loads, K over four waves: any alignment
+  kNtDirect64x64,
+  kNtRing128,              // LDS ring: rows of whole 16-byte chunks
+  kNtRing192,
+  kNtRing256,
+  kNtRing128x5,
+  kNtRing64
+};
+// kernel: one of the above (hipErrorInvalidValue where it does not take these
+// operands), for the tests and measurements of each, or the one that pays.
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel = kNtChosen);
+int i8_kernel(const Int8Args& a);
 
 // ---------------------------------------------------------------- orthogonalisation
 
@@ -303,6 +318,7 @@ struct OrthoArgs {
   float keep, step;               // w <- keep w - step O
   void* w_bf16;
   float* amax;                    // or null; cleared here
+  int kernel = kNtChosen;         // an NtKernel for every product, or the one that pays
 };
 int64_t ortho_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);   // -1: too large
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);

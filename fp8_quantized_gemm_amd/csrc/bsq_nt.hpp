@@ -45,8 +45,8 @@ inline int64_t nt_tiles(const NtArgs& g, int mt, int nt) {
 // remap gives each a contiguous run of the tile order, which sweeps 8 (lower
 // triangle: 4) tile rows at a time so that neighbouring tiles share A and B rows in
 // their L2.
-__device__ __forceinline__ void nt_tile(int pid, int total, int batch, bool sym, int tiles_m, int tiles_n, int& e,
-                                        int& tm, int& tn) {
+__device__ __forceinline__ void nt_tile_of(int pid, int total, int batch, bool sym, int tiles_m, int tiles_n, int& e,
+                                           int& tm, int& tn) {
   const int q = total / 8, r = total % 8, x = pid % 8, i = pid / 8;
   int t = x * q + (x < r ? x : r) + i;
   const int per = total / batch;
@@ -79,6 +79,15 @@ __device__ __forceinline__ void nt_tile(int pid, int total, int batch, bool sym,
     tm = s + k;
     tn = s + t;
   }
+}
+
+// The same in scalar registers (the divisions above are vector operations).
+__device__ __forceinline__ void nt_tile(int pid, int total, int batch, bool sym, int tiles_m, int tiles_n, int& e,
+                                        int& tm, int& tn) {
+  nt_tile_of(pid, total, batch, sym, tiles_m, tiles_n, e, tm, tn);
+  e = __builtin_amdgcn_readfirstlane(e);
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
 }
 
 template <int EL>

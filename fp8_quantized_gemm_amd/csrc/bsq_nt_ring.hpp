@@ -1,0 +1,379 @@
+// The LDS-staged kernel of the plain products (bsq_nt.hpp): C = A . B^T of 8-bit
+// integers or FP16 on square tiles of 256, 192, 128 or 64.
+//
+// A workgroup of four waves (one per SIMD) per tile of 32 NT rows and columns; wave w
+// owns the quarter (w >> 1, w & 1) as NT x NT accumulators of 16 x 16, pinned in
+// AGPRs by MFMAs written as inline assembly (left to itself the compiler moves them
+// between AGPRs and VGPRs).  The 16 x 16 MFMA rather than the 32 x 32 one: the matrix
+// pipe is as busy, but draws less power, so the clock holds higher.
+//
+// Units of 128 bytes of K per row reach LDS by global -> LDS direct loads into a ring
+// of NB buffers (the eight lanes of a row read one whole 128-byte line); a unit is two
+// steps of 64 bytes, NT^2 MFMAs per wave each.  The fragments of a step are read
+// during the step before into the other half of a double-buffered register set.  The
+// second step of unit U first waits for unit U + 1, then a barrier makes it visible
+// and retires unit U's buffer (whose last reads were issued in the step before), and
+// the loads of unit U + NB go into that buffer during the step.  The last NB units are
+// peeled, so that every wait count is a constant and a step is one basic block (the
+// compiler does not see the MFMAs' operand timing).
+//
+// LDS rows are 128 bytes; 16-byte chunk c of row r sits at slot c ^ ((r >> 1) & 7):
+// 16 lanes (16 consecutive rows, one chunk) are served per cycle by 64 banks, and rows
+// of one parity start on the same bank.
+//
+// Smaller tiles read more bytes per operation (256: 64 KB of LDS fill per 2^23
+// multiply-adds of FP16; 192: 1.33, 128: 2 times as much) and exist for shapes whose
+// 256 tiles would leave compute units idle.
+#pragma once
+
+#include "bsq_nt.hpp"
+
+namespace bsq {
+
+template <int NT, int NB>
+constexpr int ring_lds() {
+  const int ring = NB * 2 * 32 * NT * 128, epi = 4 * 16 * NT * (32 * NT + 8);
+  return ring > epi ? ring : epi;
+}
+
+template <int EL>
+__device__ __forceinline__ void ring_mfma(typename NtTypes<EL>::acc& acc, const ntu4& b, const ntu4& a) {
+  if constexpr (EL == kNtI8) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+  else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
+template <int NT>
+struct RingFrag {
+  ntu4 a[NT], b[NT];
+};
+
+// What a lane needs of the tile: byte offsets of the rows it loads, its chunks of
+// even and odd loads, and where it reads fragments.
+template <int NT>
+struct RingLane {
+  const uint8_t* a;
+  const uint8_t* b;
+  uint32_t va[NT], vb[NT];
+  uint32_t ldst;                 // LDS byte of this wave's first load in a buffer
+  uint32_t ra, rb;               // byte of this lane's first A / B fragment row in a buffer
+  uint32_t c0, c1;               // its chunk's byte in the row, steps 0 and 1
+  int lane;
+};
+
+// Load Q of a unit (0 .. NT - 1 the A rows, then the B rows) at byte k of the rows.
+template <int NT, int Q>
+__device__ __forceinline__ void ring_load(const RingLane<NT>& L, uint32_t k, uint32_t buf, uint32_t back_even,
+                                          uint32_t back_odd) {
+  constexpr int op = Q / NT, q = Q % NT;
+  const uint32_t back = (q & 1) ? back_odd : back_even;
+  dma_to_lds<16>((op ? L.b : L.a) + k, (op ? L.vb[q] : L.va[q]) - back,
+                 buf + L.ldst + (uint32_t)(op * 32 * NT * 128 + q * 1024));
+}
+template <int NT, int Q = 0>
+__device__ __forceinline__ void ring_issue(const RingLane<NT>& L, uint32_t k, uint32_t buf, uint32_t back_even,
+                                           uint32_t back_odd) {
+  if constexpr (Q < 2 * NT) {
+    ring_load<NT, Q>(L, k, buf, back_even, back_odd);
+    ring_issue<NT, Q + 1>(L, k, buf, back_even, back_odd);
+  }
+}
+
+// Fragment Q (0 .. NT - 1 A, then B) of step J of the unit in `buf`.
+template <int NT, int J, int Q>
+__device__ __forceinline__ void ring_read(RingFrag<NT>& F, const uint8_t* buf, const RingLane<NT>& L) {
+  constexpr int op = Q / NT, t = Q % NT;
+  const ntu4 v = *reinterpret_cast<const ntu4*>(buf + ((op ? L.rb : L.ra) + (J ? L.c1 : L.c0)) + t * 2048);
+  if constexpr (op) F.b[t] = v;
+  else F.a[t] = v;
+}
+template <int NT, int J, int Q = 0>
+__device__ __forceinline__ void ring_read_all(RingFrag<NT>& F, const uint8_t* buf, const RingLane<NT>& L) {
+  if constexpr (Q < 2 * NT) {
+    ring_read<NT, J, Q>(F, buf, L);
+    ring_read_all<NT, J, Q + 1>(F, buf, L);
+  }
+}
+
+// Read q of the next step comes after MFMA ring_rd(q), from MFMA 1 on; load q of n
+// after MFMA ring_ld(q, n).
+template <int NT>
+constexpr int ring_rd(int q) { return 1 + q * (NT * NT - 4) / (2 * NT - 1); }
+template <int NT>
+constexpr int ring_ld(int q) { return q * (NT * NT - 1) / (2 * NT); }
+
+template <int NT, int NJ, int K, int Q = 0>
+__device__ __forceinline__ void ring_reads_at(RingFrag<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L) {
+  if constexpr (Q < 2 * NT) {
+    if constexpr (ring_rd<NT>(Q) == K) ring_read<NT, NJ, Q>(G, nbuf, L);
+    ring_reads_at<NT, NJ, K, Q + 1>(G, nbuf, L);
+  }
+}
+template <int NT, int K, int Q = 0>
+__device__ __forceinline__ void ring_loads_at(const RingLane<NT>& L, uint32_t k, uint32_t lbuf, uint32_t be, uint32_t bo) {
+  if constexpr (Q < 2 * NT) {
+    if constexpr (ring_ld<NT>(Q) == K) ring_load<NT, Q>(L, k, lbuf, be, bo);
+    ring_loads_at<NT, K, Q + 1>(L, k, lbuf, be, bo);
+  }
+}
+
+// The MFMAs of a step with the next step's reads (READ, its step NJ from nbuf) and a
+// unit's loads (LOAD) between them.
+template <int EL, int NT, bool READ, int NJ, bool LOAD, int K = 0>
+__device__ __forceinline__ void ring_step(typename NtTypes<EL>::acc (&acc)[NT][NT], const RingFrag<NT>& F,
+                                          RingFrag<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L, uint32_t k,
+                                          uint32_t lbuf, uint32_t be, uint32_t bo) {
+  if constexpr (K < NT * NT) {
+    ring_mfma<EL>(acc[K / NT][K % NT], F.b[K % NT], F.a[K / NT]);
+    if constexpr (READ) ring_reads_at<NT, NJ, K>(G, nbuf, L);
+    if constexpr (LOAD) ring_loads_at<NT, K>(L, k, lbuf, be, bo);
+    __builtin_amdgcn_sched_barrier(0);
+    ring_step<EL, NT, READ, NJ, LOAD, K + 1>(acc, F, G, nbuf, L, k, lbuf, be, bo);
+  }
+}
+
+// Chunks of the last unit past the row's end (from chunk `live` on): zero in A.
+template <int NT>
+__device__ __forceinline__ void ring_clip(uint8_t* buf, int live) {
+  for (int r = threadIdx.x; r < 32 * NT; r += 256)
+    for (int c = live; c < 8; ++c)
+      *reinterpret_cast<ntu4*>(buf + r * 128 + ((c ^ ((r >> 1) & 7)) << 4)) = ntu4{0u, 0u, 0u, 0u};
+  lds_barrier();
+}
+
+// Unit with REM units from it to the end (REM > NB: more than NB, loads go on).  slot,
+// nslot: its buffer and the next unit's.
+template <int EL, int NT, int NB, int REM, bool CLIP>
+__device__ __forceinline__ void ring_unit(typename NtTypes<EL>::acc (&acc)[NT][NT], RingFrag<NT>& F0, RingFrag<NT>& F1,
+                                          uint8_t* smem, uint32_t smem_lds, const RingLane<NT>& L, int slot, int nslot,
+                                          uint32_t k_load, uint32_t be, uint32_t bo, int live) {
+  constexpr int UNIT = 2 * 32 * NT * 128, LD = 2 * NT;
+  constexpr bool more = REM > NB, next = REM > 1;
+  constexpr int flying = more ? NB - 1 : REM - 1;          // units in flight behind this one
+  uint8_t* buf = smem + slot * UNIT;
+  uint8_t* nbuf = smem + nslot * UNIT;
+  ring_step<EL, NT, true, 1, false>(acc, F0, F1, buf, L, 0, 0, 0, 0);
+  if constexpr (next) {
+    wait_vmcnt<(flying - 1) * LD>();
+    lds_barrier();
+    if (CLIP && REM == 2) ring_clip<NT>(nbuf, live);
+    asm volatile("s_nop 4" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  ring_step<EL, NT, next, 0, more>(acc, F1, F0, nbuf, L, k_load, smem_lds + (uint32_t)(slot * UNIT), be, bo);
+}
+
+template <int EL, int NT, int NB, int REM, bool CLIP>
+__device__ __forceinline__ void ring_tail(typename NtTypes<EL>::acc (&acc)[NT][NT], RingFrag<NT>& F0, RingFrag<NT>& F1,
+                                          uint8_t* smem, uint32_t smem_lds, const RingLane<NT>& L, int slot, int NU,
+                                          int live) {
+  if constexpr (REM > 0) {
+    int nslot = slot;
+    if (REM <= NU) {
+      nslot = slot + 1 == NB ? 0 : slot + 1;
+      ring_unit<EL, NT, NB, REM, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, nslot, 0, 0, 0, live);
+    }
+    ring_tail<EL, NT, NB, REM - 1, CLIP>(acc, F0, F1, smem, smem_lds, L, nslot, NU, live);
+  }
+}
+
+// CLIP: kb is no multiple of 128 (it is one of 16).
+template <int EL, int NT, int NB, bool CLIP, typename Epi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(ring_lds<NT, NB>() > 80 * 1024 ? 1 : 2, ring_lds<NT, NB>() > 80 * 1024 ? 1 : 2)))
+void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
+  typedef typename NtTypes<EL>::acc Acc;
+  constexpr int MT = 32 * NT, S = 16 * NT, UNIT = 2 * MT * 128, LD = 2 * NT;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const uint32_t smem_lds = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)smem;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 1, wn = w & 1;
+  int e, tm, tn;
+  nt_tile(blockIdx.x, total, g.batch, g.sym, tiles_m, tiles_n, e, tm, tn);
+  const int64_t m0 = (int64_t)tm * MT, n0 = (int64_t)tn * MT;
+  const int last_m = (int)(g.M - m0 < MT ? g.M - m0 - 1 : MT - 1), last_n = (int)(g.N - n0 < MT ? g.N - n0 - 1 : MT - 1);
+  const int NU = (int)((g.kb + 127) / 128);
+  RingLane<NT> L;
+  L.lane = lane;
+  L.a = g.a + e * g.stride_a + m0 * g.kb;
+  L.b = g.b + e * g.stride_b + n0 * g.kb;
+  // load q of this wave: rows w 8 NT + 8 q + (lane >> 3), slot lane & 7
+  const uint32_t ce = (uint32_t)((lane & 7) ^ (((w * 8 * NT + (lane >> 3)) >> 1) & 7)) * 16u;
+  const uint32_t co = (uint32_t)((lane & 7) ^ (((w * 8 * NT + 8 + (lane >> 3)) >> 1) & 7)) * 16u;
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int r = w * 8 * NT + 8 * q + (lane >> 3);
+    const uint32_t c = (q & 1) ? co : ce;
+    L.va[q] = (uint32_t)min(r, last_m) * g.kb + c;
+    L.vb[q] = (uint32_t)min(r, last_n) * g.kb + c;
+  }
+  L.ldst = (uint32_t)(w * 8 * NT * 128);
+  const int r16 = lane & 15, q4 = lane >> 4, sw = (r16 >> 1) & 7;
+  L.ra = (uint32_t)((wm * S + r16) * 128);
+  L.rb = (uint32_t)((MT + wn * S + r16) * 128);
+  L.c0 = (uint32_t)((q4 ^ sw) << 4);
+  L.c1 = (uint32_t)(((4 + q4) ^ sw) << 4);
+  // in the last unit, lanes whose chunk lies past the row's end read its last chunk
+  const int live = CLIP ? (int)(g.kb - (uint32_t)(NU - 1) * 128u) / 16 : 8;
+  const uint32_t top = (uint32_t)live * 16u;
+  const uint32_t be = CLIP && ce >= top ? ce - (top - 16u) : 0u, bo = CLIP && co >= top ? co - (top - 16u) : 0u;
+
+  Acc acc[NT][NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      acc[i][j] = Acc{0, 0, 0, 0};
+      asm volatile("" : "+a"(acc[i][j]));
+    }
+  __builtin_amdgcn_sched_barrier(0);
+
+#pragma unroll
+  for (int u = 0; u < NB; ++u)
+    if (u < NU) {
+      const bool end = CLIP && u == NU - 1;
+      ring_issue<NT>(L, (uint32_t)u * 128u, smem_lds + (uint32_t)(u * UNIT), end ? be : 0u, end ? bo : 0u);
+    }
+  if (NU >= NB) wait_vmcnt<(NB - 1) * LD>();
+  else wait_vmcnt<0>();
+  lds_barrier();
+  if (CLIP && NU == 1) ring_clip<NT>(smem, live);
+  RingFrag<NT> F0, F1;
+  ring_read_all<NT, 0>(F0, smem, L);
+  __builtin_amdgcn_sched_barrier(0);
+
+  int slot = 0;
+  for (int U = 0; U + NB < NU; ++U) {
+    const int nslot = slot + 1 == NB ? 0 : slot + 1;
+    const bool end = CLIP && U + NB == NU - 1;
+    ring_unit<EL, NT, NB, NB + 1, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, nslot, (uint32_t)(U + NB) * 128u,
+                                        end ? be : 0u, end ? bo : 0u, live);
+    slot = nslot;
+  }
+  ring_tail<EL, NT, NB, NB, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, NU, live);
+
+  // every wave is done with the ring (the epilogue reuses the LDS; no load is in
+  // flight), and the last MFMAs' results have reached the accumulators
+  lds_barrier();
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
+
+  // 16-bit values, four columns of a row per accumulator, staged by rows
+  constexpr int RS = S + 4;
+  uint16_t* E = reinterpret_cast<uint16_t*>(smem) + w * S * RS;
+  const int64_t mw = m0 + wm * S, nw = n0 + wn * S;
+  ntu2 val[NT][NT];
+  {
+    typename Epi::Col col[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) col[j] = epi.col(e, nw + j * 16 + 4 * q4);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int64_t m = mw + i * 16 + r16;
+      const typename Epi::Row row = epi.row(e, m);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        val[i][j] = epi.pack4(e, m, nw + j * 16 + 4 * q4, row, col[j], acc[i][j]);
+        *reinterpret_cast<ntu2*>(E + (i * 16 + r16) * RS + j * 16 + 4 * q4) = val[i][j];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int q = lane; q < S * S / 8; q += 64) {
+    const int row = q / (S / 8), c = q % (S / 8) * 8;
+    const ntu2 x = *reinterpret_cast<const ntu2*>(E + row * RS + c), y = *reinterpret_cast<const ntu2*>(E + row * RS + c + 4);
+    epi.store(e, mw + row, nw + c, ntu4{x[0], x[1], y[0], y[1]});
+  }
+  if (Epi::kTrans && !(g.sym && tm == tn)) {
+    // staged again by columns: neighbouring lanes (rows m, m + 1) exchange halves, so
+    // that the even one writes the pair of columns n and n + 1, the odd one n + 2 and
+    // n + 3, as dwords of two rows (read back by 16-bit columns instead, the rows'
+    // stride puts four lanes on a bank: 6 us a tile more)
+    __syncthreads();
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const uint32_t mine = odd ? val[i][j][1] : val[i][j][0], give = odd ? val[i][j][0] : val[i][j][1];
+        const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0xB1, 0xF, 0xF, false);   // lane ^ 1
+        const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;      // rows m (even lane's), m + 1
+        uint16_t* d = E + (j * 16 + 4 * q4 + (odd ? 2 : 0)) * RS + i * 16 + (r16 & ~1);
+        *reinterpret_cast<uint32_t*>(d) = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+        *reinterpret_cast<uint32_t*>(d + RS) = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+      }
+    __syncthreads();
+#pragma unroll 4
+    for (int q = lane; q < S * S / 8; q += 64) {
+      const int c = q / (S / 8), row = q % (S / 8) * 8;
+      const ntu2 x = *reinterpret_cast<const ntu2*>(E + c * RS + row), y = *reinterpret_cast<const ntu2*>(E + c * RS + row + 4);
+      epi.store_t(e, nw + c, mw + row, ntu4{x[0], x[1], y[0], y[1]});
+    }
+  }
+  epi.finish(e);
+}
+
+// ---------------------------------------------------------------- choice of kernel
+
+// What a tile costs, in microseconds measured on an MI355X (8-bit integers; FP16 is
+// 10-20% slower on every kernel): a unit of 128 bytes of K when all compute units are
+// busy and when few are, and a tile besides its units; `per_cu` workgroups share a
+// compute unit at that cost.
+struct NtCost {
+  int kernel, mt, nt, per_cu;
+  float full, few, tile;
+};
+constexpr NtCost kNtCosts[] = {
+    {kNtDirect16x64, 16, 64, 1, 0.29f, 0.22f, 1.9f}, {kNtDirect64x64, 64, 64, 1, 0.52f, 0.50f, 2.0f},
+    {kNtRing64, 64, 64, 2, 0.42f, 0.22f, 2.2f},      {kNtRing128, 128, 128, 2, 0.80f, 0.78f, 2.0f},
+    {kNtRing128x5, 128, 128, 1, 0.47f, 0.42f, 2.7f}, {kNtRing192, 192, 192, 1, 0.82f, 0.61f, 8.0f},
+    {kNtRing256, 256, 256, 1, 1.29f, 0.97f, 13.0f},
+};
+
+// The kernel with the least estimated time: full rounds of workgroups over the compute
+// units, and a last round that is cheaper the emptier it is.  direct, ring: which kinds
+// there are to choose from.
+inline int nt_choose(const NtArgs& g, bool direct, bool ring) {
+  const double cus = device_cus() > 0 ? device_cus() : 256;
+  const double units = (double)((g.kb + 127) / 128);
+  int best = direct ? kNtDirect64x64 : kNtRing64;
+  double least = 1e300;
+  for (const NtCost& c : kNtCosts) {
+    const bool is_direct = c.kernel == kNtDirect16x64 || c.kernel == kNtDirect64x64;
+    if (is_direct ? !direct : !ring) continue;
+    const int64_t tm = (g.M + c.mt - 1) / c.mt, tn = (g.N + c.nt - 1) / c.nt;
+    const double tiles = (double)(g.sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch, slots = cus * c.per_cu;
+    const double rounds = (double)(int64_t)(tiles / slots), last = tiles / slots - rounds;
+    double us = rounds * (units * c.full + c.tile);
+    if (last > 0) us += units * (c.few + (c.full - c.few) * last) + c.tile;
+    if (!is_direct && g.kb % 128 != 0) us += 1.0;             // the last unit clipped in LDS
+    if (us < least) {
+      least = us;
+      best = c.kernel;
+    }
+  }
+  return best;
+}
+
+// kb > 0 and a multiple of 16, rows 16-byte aligned.
+inline bool ring_fits(const NtArgs& g) {
+  return g.kb > 0 && g.kb % 16 == 0 && g.kb < (1u << 24) &&
+         ((reinterpret_cast<uintptr_t>(g.a) | reinterpret_cast<uintptr_t>(g.b)) & 15) == 0;
+}
+
+template <int EL, int NT, int NB, bool CLIP, typename Epi>
+hipError_t run_nt_ring(const NtArgs& g, const Epi& epi, hipStream_t s) {
+  constexpr int MT = 32 * NT, LDS = ring_lds<NT, NB>();
+  static_assert(LDS <= 160 * 1024, "LDS plan");
+  const int64_t total = nt_tiles(g, MT, MT);
+  if (total > 0x7FFFFFFF || !ring_fits(g) || (!CLIP && g.kb % 128 != 0)) return hipErrorInvalidValue;
+  const void* fn = reinterpret_cast<const void*>(&k_nt_ring<EL, NT, NB, CLIP, Epi>);
+  if (set_lds_limit(fn, LDS) != hipSuccess) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_nt_ring<EL, NT, NB, CLIP, Epi>), dim3((unsigned)total), dim3(256), LDS, s, g, (int)total,
+                     (int)((g.M + MT - 1) / MT), (int)((g.N + MT - 1) / MT), epi);
+  return hipGetLastError();
+}
+
+}  // namespace bsq

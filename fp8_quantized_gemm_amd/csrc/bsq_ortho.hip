@@ -2,29 +2,37 @@
 // that takes it, for gfx950 (contract in include/bsq.h):
 //   X = u / (||u||_F + eps);  per step  A = X X^T,  X <- (a I + b A + c A^2) X
 //
-// X, A and the polynomials are held in FP16 between products, under powers of two
-// that keep every entry of a matrix with singular values up to 8 in range and its
-// typical entries normal; sums are FP32 (MFMA).  FP16 rather than BF16: the matrix
-// rate is the same and each rounding is eight times finer (2^-11 of an entry); on
-// gradients of 512 x 1,792 the result is 1.0e-3 (relative, Frobenius) from the 64-bit
-// one, against 1.3e-2 with BF16 between products.
+// The products run on the FP16 MFMA (FP32 sums), and what they leave is held so that the
+// result stays near the 64-bit one, where small roundings near singular value zero are
+// multiplied by a in every step:
+//  * X as an FP16 matrix and the FP16 rest of its rounding (22 bits): the product takes the
+//    first, and the diagonal of the polynomial, nearly all of it at small singular values,
+//    multiplies both in the epilogue.
+//  * the symmetric matrices (A, the polynomials) as their diagonal in FP32 and the rest in
+//    FP16, so that the largest entries are not rounded.
+// On gradients of 512 x 1,792 five steps are 4e-4 (relative, Frobenius) from the 64-bit
+// result; with everything in FP16 1.0e-3, in BF16 1.3e-2; on a matrix of rank 8 over a floor
+// of 1e-2 2e-4, 2e-2 and 2e-1.
 //
 // Everything is computed on the smaller side m of the matrix, padded with zeros to
 // multiples of 64 in both directions (zero rows and columns stay zero), so that the
 // products need no edges.
 #include "bsq_nt.hpp"
+#include "bsq_nt_ring.hpp"
 #include "bsq_wave.hpp"
 
 #include <algorithm>
+#include <cmath>
 
 namespace bsq {
 
 namespace {
 
-// Powers of two of the FP16 forms: X and the Gram matrix (entries at most 1.3
-// squared with the usual coefficients, typically 1 / sqrt(m n)) and the polynomials
-// (entries up to the product of the leading coefficients).
-constexpr float kSX = 1024.0f, kSA = 1024.0f, kSP = 256.0f;
+// Power of two of the FP16 forms: entries of X are at most 1.3 with the usual coefficients
+// and typically 1 / sqrt(m n) at first; off-diagonal entries of the polynomials at most half
+// the product of their leading coefficients.
+constexpr float kS = 1024.0f;
+constexpr float kLo = 2048.0f;           // of the rest of X's rounding, at most 2^-11 of X
 constexpr int kParts = 256;              // most workgroups that sum one matrix's squares
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -91,18 +99,19 @@ __global__ __launch_bounds__(256) void k_ns_moment(NsSource src, int64_t n, doub
   if (threadIdx.x == 0) part[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = sum;
 }
 
-// X0 in FP16 in the matrix's own orientation (a [rows64][cols64]) and transposed
-// (at), 64 x 64 elements a turn, zeros in the padding.
+// X0 in FP16 in the matrix's own orientation (a [rows64][cols64]; lo: the rest of its
+// rounding) and transposed (at), 64 x 64 elements a turn, zeros in the padding.
 template <int IN>
 __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, int64_t cols, int parts,
                                                   const double* __restrict__ part, float eps, uint16_t* __restrict__ a,
-                                                  uint16_t* __restrict__ at, int64_t rows64, int64_t cols64, int turns) {
+                                                  uint16_t* __restrict__ lo, uint16_t* __restrict__ at, int64_t rows64,
+                                                  int64_t cols64, int turns) {
   constexpr int LD = 66;
   __shared__ double lds[4];
   __shared__ uint16_t tile[64 * LD];
   const int t = threadIdx.x;
   const double sum = block_sum(t < parts ? part[(int64_t)blockIdx.y * parts + t] : 0.0, lds);
-  const float inv = (float)((double)kSX / (sqrt(sum) + (double)eps));
+  const float inv = (float)((double)kS / (sqrt(sum) + (double)eps));
   const int64_t base = (int64_t)blockIdx.y * rows * cols, pad = (int64_t)blockIdx.y * rows64 * cols64;
   const int64_t tiles_c = cols64 / 64, tiles = rows64 / 64 * tiles_c;
   for (int k = 0; k < turns; ++k) {
@@ -138,10 +147,15 @@ __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, in
           for (int j = 0; j < 8; ++j) u[j] = raw_at(xr, j);
         }
       }
-      ntu4 v;
+      ntu4 v, l;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = pack_f16x2(u[2 * j] * inv, u[2 * j + 1] * inv);
+      for (int j = 0; j < 4; ++j) {
+        const float x0 = u[2 * j] * inv, x1 = u[2 * j + 1] * inv;
+        v[j] = pack_f16x2(x0, x1);
+        l[j] = pack_f16x2((x0 - f16_lo(v[j])) * kLo, (x1 - f16_hi(v[j])) * kLo);
+      }
       *reinterpret_cast<ntu4*>(a + pad + r * cols64 + col) = v;
+      *reinterpret_cast<ntu4*>(lo + pad + r * cols64 + col) = l;
       uint32_t* d = reinterpret_cast<uint32_t*>(tile + (t >> 2) * LD + (t & 3) * 16 + 8 * h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) d[j] = v[j];
@@ -164,55 +178,144 @@ __global__ void k_ns_zero(float* p) { *p = 0.0f; }
 
 // ---------------------------------------------------------------- epilogues
 
-// FP16(alpha sum + beta add + gamma I), and its transpose: of a symmetric product the
-// tile on the other side of the diagonal, else the matrix in its other orientation.
-struct EpiNs {
+// A symmetric matrix: the diagonal d [m] in FP32, and e [m][m] in FP16 under kS with zeros
+// on the diagonal.
+struct NsSquare {
+  uint16_t* e;
+  float* d;
+};
+
+// A symmetric product of two such matrices (or of X and its transpose: l, r null), the
+// MFMAs having formed the product of their FP16 parts; the tile on the other side of the
+// diagonal is stored too.
+//   entry (i, j)  alpha sum + r_ij (k0 + k1 dl_i) + l_ij (k0 + k1 dr_j)
+//   entry (i, i)  alpha / kS sum + q0 + q1 dl_i + q2 dl_i dr_i, in FP32
+struct EpiNsSquare {
   static constexpr bool kTrans = true;
-  uint16_t* c;
-  uint16_t* ct;
-  const uint16_t* add;           // null: none
-  int64_t ldc, ldt, stride, M, N;
-  float alpha, beta, gamma;
-  struct Row {};
-  struct Col {};
-  __device__ __forceinline__ Row row(int, int64_t) const { return Row{}; }
-  __device__ __forceinline__ Col col(int, int64_t) const { return Col{}; }
-  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row&, const Col&, ntf4 v) const {
+  NsSquare c;
+  const uint16_t* l;
+  const uint16_t* r;
+  const float* dl;
+  const float* dr;
+  int64_t m_;                    // side
+  float alpha, k0, k1, q0, q1, q2;
+  struct Row { float d; };
+  struct Col { float d[4]; };
+  __device__ __forceinline__ Row row(int e, int64_t m) const { return Row{dl ? dl[e * m_ + min(m, m_ - 1)] : 0.0f}; }
+  __device__ __forceinline__ Col col(int e, int64_t n) const {
+    Col k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k.d[i] = dr ? dr[e * m_ + min(n, m_ - 4) + i] : 0.0f;
+    return k;
+  }
+  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) y[i] = alpha * v[i];
-    if (add) {
-      const ntu2 w = *reinterpret_cast<const ntu2*>(add + e * stride + min(m, M - 1) * ldc + min(n, N - 4));
-      y[0] += beta * f16_lo(w[0]);
-      y[1] += beta * f16_hi(w[0]);
-      y[2] += beta * f16_lo(w[1]);
-      y[3] += beta * f16_hi(w[1]);
+    if (r) {
+      const int64_t at = (e * m_ + min(m, m_ - 1)) * m_ + min(n, m_ - 4);
+      const ntu2 x = *reinterpret_cast<const ntu2*>(r + at);
+      const ntu2 w = l == r ? x : *reinterpret_cast<const ntu2*>(l + at);
+      const float kr = k0 + k1 * a.d;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] += m == n + i ? gamma : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        const float xr = i & 1 ? f16_hi(x[i >> 1]) : f16_lo(x[i >> 1]), xl = i & 1 ? f16_hi(w[i >> 1]) : f16_lo(w[i >> 1]);
+        y[i] = y[i] + xr * kr + xl * (k0 + k1 * b.d[i]);
+      }
+    }
+    if (m >= n && m < n + 4 && m < m_) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (m == n + i) {
+          c.d[e * m_ + m] = alpha * (1.0f / kS) * v[i] + (q0 + q1 * a.d + q2 * (a.d * b.d[i]));
+          y[i] = 0.0f;
+        }
     }
     return ntu2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
   }
   __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
-    if (m < M && n < N) *reinterpret_cast<ntu4*>(c + e * stride + m * ldc + n) = v;
+    if (m < m_ && n < m_) *reinterpret_cast<ntu4*>(c.e + (e * m_ + m) * m_ + n) = v;
+  }
+  __device__ __forceinline__ void store_t(int e, int64_t n, int64_t m, const ntu4& v) { store(e, n, m, v); }
+  __device__ __forceinline__ void finish(int) {}
+};
+
+// What the products P X (X in the matrix's own orientation, M x N) add to the MFMAs' sum
+// of P's FP16 part and X's: P's diagonal times X, whole.  In units of X under kS.
+struct NsApply {
+  const uint16_t* hi;
+  const uint16_t* lo;
+  const float* d;
+  int64_t M, N;
+  bool wide;                     // M <= N: the diagonal runs along M
+  struct Row { float d; };
+  struct Col { float d[4]; };
+  __device__ __forceinline__ Row row(int e, int64_t m) const { return Row{wide ? d[e * M + min(m, M - 1)] : 0.0f}; }
+  __device__ __forceinline__ Col col(int e, int64_t n) const {
+    Col k;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k.d[i] = wide ? 0.0f : d[e * N + min(n, N - 4) + i];
+    return k;
+  }
+  __device__ __forceinline__ int64_t at(int e, int64_t m, int64_t n) const {
+    return (e * M + min(m, M - 1)) * N + min(n, N - 4);
+  }
+  __device__ __forceinline__ void sums(int64_t at, const Row& a, const Col& b, ntf4 v, float (&y)[4]) const {
+    const ntu2 h = *reinterpret_cast<const ntu2*>(hi + at), l = *reinterpret_cast<const ntu2*>(lo + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = (i & 1 ? f16_hi(h[i >> 1]) : f16_lo(h[i >> 1])) +
+                      (i & 1 ? f16_hi(l[i >> 1]) : f16_lo(l[i >> 1])) * (1.0f / kLo);
+      y[i] = v[i] * (1.0f / kS) + (wide ? a.d : b.d[i]) * x;
+    }
+  }
+};
+
+// The next X: FP16, the rest of its rounding (in place), and its transpose.
+struct EpiNsNext {
+  static constexpr bool kTrans = true;
+  NsApply x;
+  uint16_t* hi;
+  uint16_t* lo;
+  uint16_t* t;
+  typedef NsApply::Row Row;
+  typedef NsApply::Col Col;
+  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
+  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
+  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+    const int64_t at = x.at(e, m, n);
+    float y[4];
+    x.sums(at, a, b, v, y);
+    const ntu2 h = {pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
+    if (m < x.M && n < x.N)
+      *reinterpret_cast<ntu2*>(lo + at) = ntu2{pack_f16x2((y[0] - f16_lo(h[0])) * kLo, (y[1] - f16_hi(h[0])) * kLo),
+                                               pack_f16x2((y[2] - f16_lo(h[1])) * kLo, (y[3] - f16_hi(h[1])) * kLo)};
+    return h;
+  }
+  __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
+    if (m < x.M && n < x.N) *reinterpret_cast<ntu4*>(hi + (e * x.M + m) * x.N + n) = v;
   }
   __device__ __forceinline__ void store_t(int e, int64_t n, int64_t m, const ntu4& v) {
-    if (m < M && n < N) *reinterpret_cast<ntu4*>(ct + e * stride + n * ldt + m) = v;
+    if (m < x.M && n < x.N) *reinterpret_cast<ntu4*>(t + (e * x.N + n) * x.M + m) = v;
   }
   __device__ __forceinline__ void finish(int) {}
 };
 
-// BF16(alpha sum) of the matrix without its padding.
+// BF16(X) of the matrix without its padding.
 struct EpiNsOut {
   static constexpr bool kTrans = false;
+  NsApply x;
   uint16_t* out;
   int64_t rows, cols;
-  float alpha;
-  struct Row {};
-  struct Col {};
-  __device__ __forceinline__ Row row(int, int64_t) const { return Row{}; }
-  __device__ __forceinline__ Col col(int, int64_t) const { return Col{}; }
-  __device__ __forceinline__ ntu2 pack4(int, int64_t, int64_t, const Row&, const Col&, ntf4 v) const {
-    return ntu2{pack_bf16x2(alpha * v[0], alpha * v[1]), pack_bf16x2(alpha * v[2], alpha * v[3])};
+  typedef NsApply::Row Row;
+  typedef NsApply::Col Col;
+  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
+  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
+  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+    float y[4];
+    x.sums(x.at(e, m, n), a, b, v, y);
+    constexpr float k = 1.0f / kS;
+    return ntu2{pack_bf16x2(k * y[0], k * y[1]), pack_bf16x2(k * y[2], k * y[3])};
   }
   __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
     if (m >= rows || n >= cols) return;
@@ -224,22 +327,25 @@ struct EpiNsOut {
   __device__ __forceinline__ void finish(int) {}
 };
 
-// w <- keep w - step O, its BF16 copy and that copy's largest magnitude.  O passes
-// through LDS in FP16, whose rounding is below the products' own error.
+// w <- keep w - step X, its BF16 copy and that copy's largest magnitude.  X passes
+// through LDS in FP16 (2^-11 of an entry, below the products' own error).
 struct EpiNsUpdate {
   static constexpr bool kTrans = false;
+  NsApply x;
   float* w;
   uint16_t* wb;
   float* amax;                   // null: none
   int64_t rows, cols;
-  float alpha, keep, step;
+  float keep, step;              // step of X under kS
   uint32_t most;
-  struct Row {};
-  struct Col {};
-  __device__ __forceinline__ Row row(int, int64_t) const { return Row{}; }
-  __device__ __forceinline__ Col col(int, int64_t) const { return Col{}; }
-  __device__ __forceinline__ ntu2 pack4(int, int64_t, int64_t, const Row&, const Col&, ntf4 v) const {
-    return ntu2{pack_f16x2(alpha * v[0], alpha * v[1]), pack_f16x2(alpha * v[2], alpha * v[3])};
+  typedef NsApply::Row Row;
+  typedef NsApply::Col Col;
+  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
+  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
+  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+    float y[4];
+    x.sums(x.at(e, m, n), a, b, v, y);
+    return ntu2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
   }
   __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
     if (m >= rows || n >= cols) return;
@@ -270,16 +376,23 @@ struct EpiNsUpdate {
 
 template <typename Epi>
 hipError_t product(const uint16_t* a, const uint16_t* b, int64_t M, int64_t N, int64_t K, int64_t batch, bool sym,
-                   const Epi& epi, hipStream_t s) {
+                   const Epi& epi, int kernel, hipStream_t s) {
   const NtArgs g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), M, N, (uint32_t)(2 * K),
                  2 * M * K, 2 * N * K, (int)batch, sym};
-  return run_nt_direct<kNtF16, 4, 4, 1, 1, 4>(g, epi, s);
+  switch (kernel == kNtChosen ? nt_choose(g, false, true) : kernel) {
+    case kNtRing128: return run_nt_ring<kNtF16, 4, 2, false>(g, epi, s);
+    case kNtRing64: return run_nt_ring<kNtF16, 2, 4, false>(g, epi, s);
+    case kNtRing128x5: return run_nt_ring<kNtF16, 4, 5, false>(g, epi, s);
+    case kNtRing192: return run_nt_ring<kNtF16, 6, 3, false>(g, epi, s);
+    case kNtRing256: return run_nt_ring<kNtF16, 8, 2, false>(g, epi, s);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 struct NsSizes {
   int64_t rows64, cols64, m, n;          // padded; m <= n
   int64_t x, sq;                         // elements of one X and of one m x m matrix
-  int64_t parts_bytes, bytes;
+  int64_t parts_bytes, diag_bytes, bytes;
   int parts;
 };
 bool ns_sizes(int64_t batch, int64_t rows, int64_t cols, NsSizes* z) {
@@ -294,8 +407,27 @@ bool ns_sizes(int64_t batch, int64_t rows, int64_t cols, NsSizes* z) {
   const int64_t n = rows * cols;
   z->parts = (int)std::max<int64_t>(1, std::min<int64_t>(kParts, (n + 16383) / 16384));
   z->parts_bytes = (batch * z->parts * 8 + 255) / 256 * 256;
-  z->bytes = z->parts_bytes + batch * 2 * (3 * z->x + 4 * z->sq);
+  z->diag_bytes = batch * z->m * 4;                        // a multiple of 256
+  z->bytes = z->parts_bytes + 4 * z->diag_bytes + batch * 2 * (4 * z->x + 4 * z->sq);
   return true;
+}
+
+// Steps from step i on that share one Gram matrix, the phase before having been of
+// `before`.  After A = X X^T, the next step's Gram matrix is Q A Q with the polynomial
+// Q = a I + b A + c A^2, and the product P of both polynomials is applied to X once: two
+// steps take 1.5 m^2 n + 2.5 m^3 multiply-adds (symmetric products counted half), one by
+// one 3 m^2 n + m^3.  But Q A Q multiplies A's rounding at singular values near zero by
+// a^2 until A is formed afresh, so a pair is followed by a single step, and is taken
+// where the matrix is far enough from square to have no singular values near zero and
+// the a's are small (at most 12; the usual ones 11.9).  Simulated on gradients, distance
+// from the 64-bit result one by one / in pairs with singles between / 2 and 3: 512 x
+// 1,792 4.1e-4, 2.9e-4, 6.4e-4; 500 x 800 5.4e-4, 5.7e-4, 1.6e-3; 1,024 x 1,024 5.8e-4,
+// 1.4e-3, 4.1e-3; all five at once infinity.
+int phase_steps(const OrthoArgs& o, const NsSizes& z, int i, int before) {
+  return 2 * z.n >= 3 * z.m && before != 2 && i + 2 <= o.steps &&
+                 std::fabs(o.coefs[3 * i] * o.coefs[3 * i + 3]) <= 12.0f
+             ? 2
+             : 1;
 }
 
 }  // namespace
@@ -309,11 +441,17 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
   NsSizes z;
   if (!ns_sizes(o.batch, o.rows, o.cols, &z)) return hipErrorInvalidValue;
   double* part = static_cast<double*>(o.workspace);
-  uint16_t* p = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(o.workspace) + z.parts_bytes);
+  float* diag = reinterpret_cast<float*>(static_cast<uint8_t*>(o.workspace) + z.parts_bytes);
+  uint16_t* p = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(diag) + 4 * z.diag_bytes);
   const int64_t B = o.batch, X = B * z.x, S = B * z.sq;
-  // x [m][n] and its transposes xt, xn [n][m]; the m x m matrices
-  uint16_t *x = p, *xt = p + X, *xn = p + 2 * X, *ga = p + 3 * X, *q = ga + S, *t = q + S, *pp = t + S;
-  const bool wide = z.rows64 == z.m;                       // rows <= cols: x has the matrix's own orientation
+  // x [m][n]; its transpose xt and the next one xn [n][m]; lo in the matrix's own orientation
+  uint16_t *x = p, *xt = p + X, *xn = p + 2 * X, *lo = p + 3 * X;
+  const auto matrix = [&](int i) { return NsSquare{p + 4 * X + i * S, diag + i * B * z.m}; };
+  NsSquare ga = matrix(0), q = matrix(1), t = matrix(2), pp = matrix(3);
+  // x has the matrix's own orientation.  By the true sizes: on the larger side, where the
+  // padded ones are equal, the Gram matrix has singular values zero, along which roundings
+  // grow (7 x 5: 2.6e-3 from the 64-bit result against 8e-4)
+  const bool wide = o.rows <= o.cols;
 
   const NsSource src{o.x, o.momentum, static_cast<const uint16_t*>(o.grad), o.mu, o.nesterov ? 1 : 0};
   const dim3 gm((unsigned)z.parts, (unsigned)B);
@@ -323,8 +461,8 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
   uint16_t *own = wide ? x : xt, *other = wide ? xt : x;
 #define BSQ_NS_IN(IN)                                                                                              \
   hipLaunchKernelGGL(k_ns_moment<IN>, gm, dim3(256), 0, s, src, o.rows * o.cols, part);                            \
-  hipLaunchKernelGGL(k_ns_scale<IN>, gs, dim3(256), 0, s, src, o.rows, o.cols, z.parts, part, o.eps, own, other,   \
-                     z.rows64, z.cols64, turns)
+  hipLaunchKernelGGL(k_ns_scale<IN>, gs, dim3(256), 0, s, src, o.rows, o.cols, z.parts, part, o.eps, own, lo,      \
+                     other, z.rows64, z.cols64, turns)
   if (o.w) {
     BSQ_NS_IN(kNsMoment);
   } else if (o.f32) {
@@ -337,37 +475,43 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
-  const auto square = [&](const uint16_t* a, const uint16_t* b, uint16_t* c, int64_t K, const uint16_t* add, float alpha,
-                          float beta, float gamma) {
-    const EpiNs epi{c, c, add, z.m, z.m, z.sq, z.m, z.m, alpha, beta, gamma};
-    return product(a, b, z.m, z.m, K, B, true, epi, s);
+  // c = the product of symmetric matrices l and r, or (poly) a I + b l + c l^2
+  const auto multiply = [&](const NsSquare& l, const NsSquare& r, const NsSquare& c, const float* poly) {
+    const EpiNsSquare epi = poly ? EpiNsSquare{c, l.e, l.e, l.d, l.d, z.m, poly[2] / kS, 0.5f * poly[1], poly[2],
+                                               poly[0], poly[1], poly[2]}
+                                 : EpiNsSquare{c, l.e, r.e, l.d, r.d, z.m, 1.0f / kS, 0.0f, 1.0f, 0.0f, 0.0f, 1.0f};
+    return product(l.e, r.e, z.m, z.m, z.m, B, true, epi, o.kernel, s);
   };
-  for (int i = 0; i < o.steps; ++i) {
-    const float* c = o.coefs + 3 * i;
-    const bool last = i + 1 == o.steps;
-    e = square(x, x, ga, z.n, nullptr, kSA / (kSX * kSX), 0.0f, 0.0f);
+  for (int i = 0, r = 0; i < o.steps;) {
+    r = phase_steps(o, z, i, r);
+    const EpiNsSquare gram{ga, nullptr, nullptr, nullptr, nullptr, z.m, 1.0f / kS, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    e = product(x, x, z.m, z.m, z.n, B, true, gram, o.kernel, s);
+    if (e == hipSuccess) e = multiply(ga, ga, pp, o.coefs + 3 * i);
+    if (r == 2) {
+      if (e == hipSuccess) e = multiply(pp, ga, t, nullptr);
+      if (e == hipSuccess) e = multiply(t, pp, ga, nullptr);
+      if (e == hipSuccess) e = multiply(ga, ga, q, o.coefs + 3 * i + 3);
+      if (e == hipSuccess) e = multiply(q, pp, t, nullptr);
+      std::swap(pp, t);
+    }
     if (e != hipSuccess) return e;
-    e = square(ga, ga, q, z.m, ga, c[2] * (kSP / (kSA * kSA)), c[1] * (kSP / kSA), c[0] * kSP);
-    if (e != hipSuccess) return e;
-    if (!last) {
-      const EpiNs epi{xn, x, nullptr, z.m, z.n, z.x, z.n, z.m, 1.0f / kSP, 0.0f, 0.0f};
-      e = product(xt, q, z.n, z.m, z.m, B, false, epi, s);
+    i += r;
+    // P X in the matrix's own orientation
+    const uint16_t *l = wide ? pp.e : xt, *rr = wide ? xt : pp.e;
+    const NsApply apply{wide ? x : xt, lo, pp.d, z.rows64, z.cols64, wide};
+    if (i < o.steps) {
+      const EpiNsNext epi{apply, wide ? x : xn, lo, wide ? xn : x};
+      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
       std::swap(xt, xn);
+    } else if (o.w) {
+      const EpiNsUpdate epi{apply, o.w, static_cast<uint16_t*>(o.w_bf16), o.amax, o.rows, o.cols, o.keep, o.step / kS, 0u};
+      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
     } else {
-      const uint16_t *l = wide ? q : xt, *r = wide ? xt : q;
-      const float alpha = 1.0f / (kSP * kSX);
-      if (o.w) {
-        const EpiNsUpdate epi{o.w, static_cast<uint16_t*>(o.w_bf16), o.amax, o.rows, o.cols, alpha, o.keep, o.step, 0u};
-        e = product(l, r, z.rows64, z.cols64, z.m, B, false, epi, s);
-      } else {
-        const EpiNsOut epi{static_cast<uint16_t*>(o.out), o.rows, o.cols, alpha};
-        e = product(l, r, z.rows64, z.cols64, z.m, B, false, epi, s);
-      }
+      const EpiNsOut epi{apply, static_cast<uint16_t*>(o.out), o.rows, o.cols};
+      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
     }
     if (e != hipSuccess) return e;
   }
-  (void)t;
-  (void)pp;
   return hipSuccess;
 }
 

@@ -538,7 +538,7 @@ bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* off
 
 /*
  * Codes of the rows of x[rows, cols] (BF16), one scale per row:
- *   amax = max|x| of the row; s_enc = 127/amax (FP32; 1 if amax == 0; <= FLT_MAX);
+ *   amax = max|x| of the row; s_enc = 127 * (1/amax) (1 if amax == 0; <= FLT_MAX);
  *   scale = 1/s_enc; code = RNE(x * s_enc), in [-127, 127]
  * (FP32 IEEE RNE at every step).  NaN and infinities touch their own row only.
  *   codes  : out, int8 [rows, cols].  scales : out, FP32 [rows].
@@ -597,10 +597,11 @@ bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, in
  * For each matrix x[rows, cols] of a stack of `batch`:
  *   X = x / (||x||_F + eps); for each step's a, b, c: A = X X^T,
  *   X <- (a I + b A + c A^2) X;  out = BF16(X)
- * (on the transpose where rows > cols, which is the same).  Between products X, A
- * and the polynomials are FP16 under powers of two (each rounding at most 2^-11 of
- * the value), sums FP32, the norm FP64; coefficients must keep singular values below
- * 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of its own.
+ * (on the transpose where rows > cols, which is the same).  The products take FP16
+ * matrices under a power of two (each rounding at most 2^-11 of the value) and sum in
+ * FP32; X itself is held to 22 bits, the diagonals of A and the polynomials in FP32,
+ * the norm in FP64: five steps are within about 1e-3 (relative, Frobenius) of the
+ * exact result.  Coefficients must keep singular values below 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of its own.
  *   x     : in, [batch, rows, cols] of type.   out : out, BF16 [batch, rows, cols].
  *   coefs : in, HOST array of 3 * steps floats, 1 <= steps <= 32.   eps > 0.
  *   workspace : device memory, 256-byte aligned.

@@ -1,6 +1,6 @@
 """8-bit integer quantizers and product (definitions in include/bsq.h), in NumPy.
 
-codes = RNE(FP32(x * s_enc)), s_enc = FP32(127 / amax) of the row, scale = 1 / s_enc;
+codes = RNE(FP32(x * s_enc)), s_enc = FP32(127 * FP32(1 / amax)) of the row, scale = 1 / s_enc;
 C = BF16(FP32(FP32(sum) * FP32(sa * sb)) + bias), every step one FP32 rounding."""
 
 import numpy as np
@@ -15,7 +15,7 @@ def quantize(bits):
     x = (bits.astype(np.uint32) << 16).view(np.float32)
     amax = np.abs(x).max(axis=1, initial=0.0).astype(np.float32)
     with np.errstate(divide="ignore", over="ignore"):
-        enc = np.where(amax == 0, np.float32(1), np.minimum(np.float32(127) / amax, FLT_MAX)).astype(np.float32)
+        enc = np.where(amax == 0, np.float32(1), np.minimum(np.float32(127) * (np.float32(1) / amax), FLT_MAX)).astype(np.float32)
     codes = np.rint((x * enc[:, None]).astype(np.float32))
     return codes.astype(np.int8), (np.float32(1) / enc).astype(np.float32)
 

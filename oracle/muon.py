@@ -2,8 +2,9 @@
 include/bsq.h).
 
 orthogonalize: the definition in FP64.  orthogonalize_f16: the same with what is held
-between products rounded to FP16 as the kernels hold it, for the size of error that
-these roundings cause; sums are FP64 here, FP32 in the kernels."""
+between products rounded as the kernels hold it (X as an FP16 matrix and the FP16 rest
+of its rounding, symmetric matrices as an FP32 diagonal and an FP16 rest), for the size
+of error that these roundings cause; sums are FP64 here, FP32 in the kernels."""
 
 import numpy as np
 
@@ -30,45 +31,48 @@ def orthogonalize(x, steps=5, coefs=COEFS, eps=1e-7):
 
 
 def phases(m, n, steps, coefs=COEFS):
-    """Numbers of steps that are taken on one Gram matrix, in turn: one by one on
-    nearly square matrices; else up to three while the product of the leading
-    coefficients is at most 48."""
-    lead = [abs(float(v[0])) for v in _steps(steps, coefs)]
-    out, i = [], 0
-    while i < steps:
-        r, p = 1, lead[i]
-        while 2 * n >= 3 * m and r < 3 and i + r < steps and p * lead[i + r] <= 48:
-            p *= lead[i + r]
-            r += 1
-        out.append(r)
-        i += r
+    """Numbers of steps that are taken on one Gram matrix, in turn: one by one, or, from
+    n = 1.5 m on, pairs with a single step between them, of steps whose leading
+    coefficients' product is at most 12."""
+    lead = [abs(float(np.float32(v[0]))) for v in _steps(steps, coefs)]
+    out = []
+    while sum(out) < steps:
+        i = sum(out)
+        pair = 2 * n >= 3 * m and out[-1:] != [2] and i + 2 <= steps and lead[i] * lead[i + 1] <= 12
+        out.append(2 if pair else 1)
     return out
 
 
 def orthogonalize_f16(x, steps=5, coefs=COEFS, eps=1e-7, plan=None):
-    def half(v, scale):
-        return (v * scale).astype(np.float32).astype(np.float16).astype(np.float64) / scale
+    S, LO = 1024.0, 2048.0
 
-    def mirror(v):
-        return np.tril(v) + np.tril(v, -1).T
-    X, A, P = 1024.0, 1024.0, 256.0
+    def half(v):
+        return v.astype(np.float32).astype(np.float16).astype(np.float64)
+
+    def split(v):
+        """A symmetric matrix as (diagonal, FP16 rest)."""
+        v = np.tril(v) + np.tril(v, -1).T
+        return np.diag(v).astype(np.float32).astype(np.float64), half((v - np.diag(np.diag(v))) * S) / S
+
+    def times(l, r):
+        return l[1] @ r[1] + l[0][:, None] * r[1] + l[1] * r[0][None, :] + np.diag(l[0] * r[0])
     x = np.asarray(x, dtype=np.float64)
     t = _small_side(x)
-    t = half(t / (np.sqrt((t * t).sum()) + eps), X)
+    t = t / (np.sqrt((t * t).sum()) + eps)
     eye, c = np.eye(t.shape[0]), _steps(steps, coefs)
     plan = [1] * steps if plan is None else plan
     i = 0
-    for k, r in enumerate(plan):
-        g, p = half(mirror(t @ t.T), A), None
+    for r in plan:
+        hi = half(t * S) / S
+        whole = hi + half((t - hi) * S * LO) / (S * LO)
+        g, p = split(hi @ hi.T), None
         for j in range(r):
-            q = half(mirror(c[i][0] * eye + c[i][1] * g + c[i][2] * (g @ g)), P)
+            q = split(c[i][0] * eye + c[i][1] * (np.diag(g[0]) + g[1]) + c[i][2] * times(g, g))
             if j + 1 < r:
-                g = half(mirror(half(mirror(q @ g), A) @ q), A)
-            p = q if p is None else half(mirror(q @ p), P)
+                g = split(times(split(times(q, g)), q))
+            p = q if p is None else split(times(q, p))
             i += 1
-        t = p @ t
-        if k + 1 < len(plan):
-            t = half(t, X)
+        t = p[0][:, None] * whole + p[1] @ hi
     return t.T if x.shape[0] > x.shape[1] else t
 
 

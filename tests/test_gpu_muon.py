@@ -1,7 +1,7 @@
 """Orthogonalisation and the weight update against the FP64 definition.
 
-Tolerance of an orthogonalised matrix: between products the kernels hold FP16 values
-(each rounding at most 2^-11).  The oracle repeats those roundings with FP64 sums; its
+Tolerance of an orthogonalised matrix: the products take FP16 values (each rounding at
+most 2^-11) between which parts are held more exactly.  The oracle repeats those roundings with FP64 sums; its
 distance from the definition is the error they cause, on this matrix and with these
 coefficients.  The kernels' sums are FP32, so their roundings fall elsewhere but are of
 the same number and size: twice that distance is allowed, and half a step of the output

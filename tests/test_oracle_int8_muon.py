@@ -39,7 +39,7 @@ def test_quantize_by_fractions():
     vals = (bits.astype(np.uint32) << 16).view(np.float32)
     for r in range(7):
         amax = max(abs(Fraction(float(v))) for v in vals[r])
-        enc = Fraction(1) if amax == 0 else _f32(Fraction(127) / amax)
+        enc = Fraction(1) if amax == 0 else _f32(127 * _f32(1 / amax))
         assert Fraction(float(scales[r])) == _f32(1 / enc)
         assert [_rne(_f32(Fraction(float(v)) * enc)) for v in vals[r]] == [int(c) for c in codes[r]]
         assert amax == 0 or np.abs(codes[r].astype(int)).max() == 127
@@ -100,18 +100,18 @@ def test_orthogonalize_zero_and_steps():
 
 
 def test_f16_form_and_phases():
-    """The form with FP16 between products stays near the definition for every plan, and
-    is exact where nothing rounds."""
+    """The form with FP16 products stays near the definition for every plan, and is exact
+    where nothing rounds."""
     rng = np.random.RandomState(4)
     x = rng.randn(40, 100)
     e = OM.orthogonalize(x)
-    for plan in ([1] * 5, [3, 2], [2, 3]):
+    for plan in ([1] * 5, [2, 1, 2]):
         f = OM.orthogonalize_f16(x, plan=plan)
-        assert 0 < np.linalg.norm(f - e) < 2.0 ** -11 * 20 * np.linalg.norm(e)
+        assert 0 < np.linalg.norm(f - e) < 2.0 ** -11 * 5 * np.linalg.norm(e)
     assert np.allclose(OM.orthogonalize_f16(2.0 * np.eye(4), steps=1, coefs=(1.0, 0.0, 0.0), eps=1e-30), 0.5 * np.eye(4))
-    assert OM.phases(64, 64, 5) == [1] * 5 and OM.phases(64, 128, 5) == [3, 2]
-    assert OM.phases(64, 128, 3, [(8.3, 0, 0), (4.1, 0, 0), (3.9, 0, 0)]) == [2, 1]
-    assert OM.phases(64, 128, 7, (1.5, -0.5, 0)) == [3, 3, 1]
+    assert OM.phases(64, 64, 5) == [1] * 5 and OM.phases(64, 128, 5) == [2, 1, 2]
+    assert OM.phases(64, 128, 3, [(8.3, 0, 0), (4.1, 0, 0), (2.9, 0, 0)]) == [1, 2]
+    assert OM.phases(64, 128, 7, (1.5, -0.5, 0)) == [2, 1, 2, 1, 1]
 
 
 def test_moment():
