@@ -319,18 +319,19 @@ NtArgs i8_args(const Int8Args& a) { return NtArgs{a.ac, a.bc, a.M, a.N, (uint32_
 
 int i8_kernel(const Int8Args& a) {
   const NtArgs g = i8_args(a);
-  return nt_choose(g, true, ring_fits(g));
+  return nt_choose(g, true, ring_fits(g), false, false);
 }
 
 hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel) {
   const NtArgs g = i8_args(a);
   const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
-  const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec};
+  const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec, 0, 0, 0, 0};
   switch (kernel == kNtChosen ? i8_kernel(a) : kernel) {
     case kNtDirect16x64: return run_nt_direct<kNtI8, 1, 4, 1, 1, 4>(g, e, s);
     case kNtDirect64x64: return run_nt_direct<kNtI8, 4, 4, 1, 1, 4>(g, e, s);
     case kNtRing128: return run_ring<4, 2>(g, e, s);
-    case kNtRing64: return run_ring<2, 4>(g, e, s);
+    case kNtRing64: return run_ring<2, 3>(g, e, s);
+    case kNtRing96: return run_ring<3, 6>(g, e, s);
     case kNtRing128x5: return run_ring<4, 5>(g, e, s);
     case kNtRing192: return run_ring<6, 3>(g, e, s);
     case kNtRing256: return run_ring<8, 2>(g, e, s);

@@ -290,7 +290,8 @@ enum NtKernel {
   kNtRing192,
   kNtRing256,
   kNtRing128x5,
-  kNtRing64
+  kNtRing64,
+  kNtRing96
 };
 // kernel: one of the above (hipErrorInvalidValue where it does not take these
 // operands), for the tests and measurements of each, or the one that pays.

@@ -135,8 +135,14 @@ __device__ __forceinline__ ntu4 nt_load_end(const uint8_t* row, int k, int kb) {
 //
 // A finished tile becomes 16-bit values in LDS (Epi::pack4, four columns of one row)
 // and leaves as whole row pieces of eight (Epi::store), and, with Epi::kTrans, as
-// pieces of its transpose (Epi::store_t).  Row and Col hold what pack4 needs of its
-// row and of its four columns; the indexes may lie past the matrix there.
+// pieces of its transpose (Epi::store_t).  Epi::at moves the epilogue's pointers to a
+// wave's part of the tile, whose rows and columns are counted from there; r16 and c4 are
+// the lane's row and first column in a 16 x 16 block.  What pack4 needs of the rows of
+// block row i (Row), of the columns of block column j (Col) and of what it adds at block
+// (i, j) (Add), and store of what it updates (Fetch), is loaded by calls of their own,
+// some places ahead.
+
+struct EpiNothing {};
 
 // 8-bit integer products: BF16(FP32(sum) (sa sb) + bias).  The sum is exact, so the
 // result does not depend on the kernel that formed it.
@@ -146,22 +152,40 @@ struct EpiI8 {
   const float* sb;
   const float* bias;             // null: none
   uint16_t* c;
-  int64_t ldc, M, N;
+  int64_t ldc;
+  int64_t rows, cols;
   bool vec;                      // c 16-byte aligned and ldc % 8 == 0
+  int M, N, r16, c4;             // rows and columns left from the wave's first, negative past the matrix
   struct Row { float s; };
   struct Col { float s[4], b[4]; };
-  __device__ __forceinline__ Row row(int, int64_t m) const { return Row{sa[m < M ? m : M - 1]}; }
-  __device__ __forceinline__ Col col(int, int64_t n) const {
+  typedef EpiNothing Add;
+  typedef EpiNothing Fetch;
+  __device__ __forceinline__ void at(int, int64_t m0, int64_t n0, int r, int c4_) {
+    sa += m0;
+    sb += n0;
+    if (bias) bias += n0;
+    c += m0 * ldc + n0;
+    M = (int)max((int64_t)-1024, min(rows - m0, (int64_t)1024));
+    N = (int)max((int64_t)-1024, min(cols - n0, (int64_t)1024));
+    r16 = r;
+    c4 = c4_;
+  }
+  __device__ __forceinline__ Row row_at(int m) const { return Row{sa[min(m, M - 1)]}; }
+  __device__ __forceinline__ Col col_at(int n) const {
     Col k;
+    const float* b = bias ? bias : sb;                     // loaded either way: no branch around each load
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t j = n + i < N ? n + i : N - 1;
+      const int j = min(n + i, N - 1);
       k.s[i] = sb[j];
-      k.b[i] = bias ? bias[j] : 0.0f;
+      k.b[i] = b[j];
     }
     return k;
   }
-  __device__ __forceinline__ ntu2 pack4(int, int64_t, int64_t, const Row& r, const Col& k, nti4 v) const {
+  __device__ __forceinline__ Row row(int i) const { return row_at(i * 16 + r16); }
+  __device__ __forceinline__ Col col(int j) const { return col_at(j * 16 + c4); }
+  __device__ __forceinline__ void add(Add&, int, int) const {}
+  __device__ __forceinline__ ntu2 pack4(int, int, const Row& r, const Col& k, const Add&, nti4 v) const {
     float y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -170,7 +194,8 @@ struct EpiI8 {
     }
     return ntu2{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
   }
-  __device__ __forceinline__ void store(int, int64_t m, int64_t n, const ntu4& v) {
+  __device__ __forceinline__ void fetch(Fetch&, int, int) const {}
+  __device__ __forceinline__ void store(int m, int n, const ntu4& v, const Fetch&) {
     if (m >= M || n >= N) return;
     uint16_t* dst = c + m * ldc + n;
     if (vec && n + 8 <= N) {
@@ -181,8 +206,8 @@ struct EpiI8 {
         if (n + i < N) dst[i] = (uint16_t)(v[i >> 1] >> (16 * (i & 1)));
     }
   }
-  __device__ __forceinline__ void store_t(int, int64_t, int64_t, const ntu4&) {}
-  __device__ __forceinline__ void finish(int) {}
+  __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
+  __device__ __forceinline__ void finish() {}
 };
 
 // ---------------------------------------------------------------- direct kernel
@@ -194,7 +219,7 @@ struct EpiI8 {
 template <int MI, int NI, int WM, int WN, int WK>
 constexpr int nt_direct_lds() {
   constexpr int MT = WM * MI * 16, NT = WN * NI * 16;
-  return (WK > 1 ? WK * MT * (NT + 4) * 4 : 0) + MT * (NT + 4) * 2;
+  return WK * MT * (NT + 4) * 4 + MT * (NT + 4) * 2;
 }
 template <int EL, int MI, int NI, int WM, int WN, int WK, typename Epi>
 __global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
@@ -270,57 +295,32 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, int t
     multiply(fa[0], fb[0]);
   }
 
-  // 16-bit tile, rows of NT + 4
+  // the waves' parts added, 16-bit tile in rows of NT + 4
+  static_assert(!Epi::kTrans, "the direct kernel stores no transpose and adds nothing");
   constexpr int RS = NT + 4, PS = NT + 4;
-  uint16_t* E = reinterpret_cast<uint16_t*>(smem + (WK > 1 ? WK * MT * PS * 4 : 0));
-  if constexpr (WK == 1) {
+  uint16_t* E = reinterpret_cast<uint16_t*>(smem + WK * MT * PS * 4);
+  epi.at(e, m0, n0, 0, 0);
+  Acc* part = reinterpret_cast<Acc*>(smem);                // [WK][MT][PS / 4]
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int row = (wm * MI + i) * 16 + r16;
-      const typename Epi::Row er = epi.row(e, m0 + row);
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) {
-        const int col = (wn * NI + j) * 16 + 4 * q4;
-        *reinterpret_cast<ntu2*>(E + row * RS + col) =
-            epi.pack4(e, m0 + row, n0 + col, er, epi.col(e, n0 + col), acc[i][j]);
-      }
-    }
-  } else {
-    Acc* part = reinterpret_cast<Acc*>(smem);              // [WK][MT][PS / 4]
+    for (int j = 0; j < NI; ++j)
+      part[((wk * MT + (wm * MI + i) * 16 + r16) * PS + (wn * NI + j) * 16) / 4 + q4] = acc[i][j];
+  __syncthreads();
+  for (int q = threadIdx.x; q < MT * NT / 4; q += T) {
+    const int row = q / (NT / 4), col = q % (NT / 4) * 4;
+    Acc v = part[(row * PS + col) / 4];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j)
-        part[((wk * MT + (wm * MI + i) * 16 + r16) * PS + (wn * NI + j) * 16) / 4 + q4] = acc[i][j];
-    __syncthreads();
-    for (int q = threadIdx.x; q < MT * NT / 4; q += T) {
-      const int row = q / (NT / 4), col = q % (NT / 4) * 4;
-      Acc v = part[(row * PS + col) / 4];
-#pragma unroll
-      for (int s = 1; s < WK; ++s) v += part[((s * MT + row) * PS + col) / 4];
-      *reinterpret_cast<ntu2*>(E + row * RS + col) =
-          epi.pack4(e, m0 + row, n0 + col, epi.row(e, m0 + row), epi.col(e, n0 + col), v);
-    }
+    for (int s = 1; s < WK; ++s) v += part[((s * MT + row) * PS + col) / 4];
+    *reinterpret_cast<ntu2*>(E + row * RS + col) = epi.pack4(0, 0, epi.row_at(row), epi.col_at(col), EpiNothing{}, v);
   }
   __syncthreads();
   for (int q = threadIdx.x; q < MT * NT / 8; q += T) {
     const int row = q / (NT / 8), col = q % (NT / 8) * 8;
-    if (row > last_m || col > last_n) continue;
     const ntu2 x = *reinterpret_cast<const ntu2*>(E + row * RS + col), y = *reinterpret_cast<const ntu2*>(E + row * RS + col + 4);
-    epi.store(e, m0 + row, n0 + col, ntu4{x[0], x[1], y[0], y[1]});
+    epi.store(row, col, ntu4{x[0], x[1], y[0], y[1]}, EpiNothing{});
   }
-  if (Epi::kTrans && !(g.sym && tm == tn)) {
-    for (int q = threadIdx.x; q < MT * NT / 8; q += T) {
-      const int col = q / (MT / 8), row = q % (MT / 8) * 8;
-      if (row > last_m || col > last_n) continue;
-      ntu4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = (uint32_t)E[(row + 2 * i) * RS + col] | ((uint32_t)E[(row + 2 * i + 1) * RS + col] << 16);
-      epi.store_t(e, n0 + col, m0 + row, v);
-    }
-  }
-  epi.finish(e);
+  epi.finish();
 }
 
 template <int EL, int MI, int NI, int WM, int WN, int WK, typename Epi>

@@ -97,7 +97,7 @@ __device__ __forceinline__ void ring_read_all(RingFrag<NT>& F, const uint8_t* bu
 // Read q of the next step comes after MFMA ring_rd(q), from MFMA 1 on; load q of n
 // after MFMA ring_ld(q, n).
 template <int NT>
-constexpr int ring_rd(int q) { return 1 + q * (NT * NT - 4) / (2 * NT - 1); }
+constexpr int ring_rd(int q) { return 1 + q * (NT * NT * 3 / 4 - 4) / (2 * NT - 1); }
 template <int NT>
 constexpr int ring_ld(int q) { return q * (NT * NT - 1) / (2 * NT); }
 
@@ -176,9 +176,98 @@ __device__ __forceinline__ void ring_tail(typename NtTypes<EL>::acc (&acc)[NT][N
   }
 }
 
+// ---- small tiles: a step is a whole unit.  Its fragments (both halves) are read during
+// the unit before, so that the reads' latency, longer than the few MFMAs of half a unit,
+// is covered; unit U's buffer is free from the barrier at its start on.  Their MFMAs are
+// the compiler's: few accumulators need no pinning, and across the branches of a short
+// product it copies them, which assembly MFMAs would have to be guarded against.
+
+template <int NT>
+struct RingUnit {
+  RingFrag<NT> h[2];
+};
+
+template <int NT, int Q>
+__device__ __forceinline__ void ring_read2(RingUnit<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L) {
+  ring_read<NT, Q / (2 * NT), Q % (2 * NT)>(G.h[Q / (2 * NT)], nbuf, L);
+}
+template <int NT, int Q = 0>
+__device__ __forceinline__ void ring_read2_all(RingUnit<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L) {
+  if constexpr (Q < 4 * NT) {
+    ring_read2<NT, Q>(G, nbuf, L);
+    ring_read2_all<NT, Q + 1>(G, nbuf, L);
+  }
+}
+template <int NT>
+constexpr int ring_rd2(int q) { return q * NT / 4; }
+template <int NT, int K, int Q = 0>
+__device__ __forceinline__ void ring_reads2_at(RingUnit<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L) {
+  if constexpr (Q < 4 * NT) {
+    if constexpr (ring_rd2<NT>(Q) == K) ring_read2<NT, Q>(G, nbuf, L);
+    ring_reads2_at<NT, K, Q + 1>(G, nbuf, L);
+  }
+}
+template <int NT, int K, int Q = 0>
+__device__ __forceinline__ void ring_loads2_at(const RingLane<NT>& L, uint32_t k, uint32_t lbuf, uint32_t be, uint32_t bo) {
+  if constexpr (Q < 2 * NT) {
+    if constexpr (NT * NT + Q * (NT * NT - 1) / (2 * NT) == K) ring_load<NT, Q>(L, k, lbuf, be, bo);
+    ring_loads2_at<NT, K, Q + 1>(L, k, lbuf, be, bo);
+  }
+}
+template <int EL, int NT, bool READ, bool LOAD, int K = 0>
+__device__ __forceinline__ void ring_step2(typename NtTypes<EL>::acc (&acc)[NT][NT], const RingUnit<NT>& F,
+                                           RingUnit<NT>& G, const uint8_t* nbuf, const RingLane<NT>& L, uint32_t k,
+                                           uint32_t lbuf, uint32_t be, uint32_t bo) {
+  if constexpr (K < 2 * NT * NT) {
+    constexpr int h = K / (NT * NT), i = K % (NT * NT) / NT, j = K % NT;
+    acc[i][j] = nt_mfma<EL>(F.h[h].b[j], F.h[h].a[i], acc[i][j]);
+    if constexpr (LOAD) ring_loads2_at<NT, K>(L, k, lbuf, be, bo);
+    if constexpr (READ) ring_reads2_at<NT, K>(G, nbuf, L);
+    __builtin_amdgcn_sched_barrier(0);
+    ring_step2<EL, NT, READ, LOAD, K + 1>(acc, F, G, nbuf, L, k, lbuf, be, bo);
+  }
+}
+template <int EL, int NT, int NB, int REM, bool CLIP>
+__device__ __forceinline__ void ring_unit2(typename NtTypes<EL>::acc (&acc)[NT][NT], const RingUnit<NT>& F,
+                                           RingUnit<NT>& G, uint8_t* smem, uint32_t smem_lds, const RingLane<NT>& L,
+                                           int& slot, uint32_t k_load, uint32_t be, uint32_t bo, int live) {
+  constexpr int UNIT = 2 * 32 * NT * 128, LD = 2 * NT;
+  constexpr bool more = REM > NB, next = REM > 1;
+  constexpr int flying = more ? NB - 1 : REM - 1;
+  const int nslot = slot + 1 == NB ? 0 : slot + 1;
+  if constexpr (next) {
+    wait_vmcnt<(flying - 1) * LD>();
+    lds_barrier();
+    if (CLIP && REM == 2) ring_clip<NT>(smem + nslot * UNIT, live);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  ring_step2<EL, NT, next, more>(acc, F, G, smem + nslot * UNIT, L, k_load, smem_lds + (uint32_t)(slot * UNIT), be, bo);
+  slot = nslot;
+}
+template <int EL, int NT, int NB, int REM, bool CLIP>
+__device__ __forceinline__ void ring_tail2(typename NtTypes<EL>::acc (&acc)[NT][NT], RingUnit<NT>& F, RingUnit<NT>& G,
+                                           uint8_t* smem, uint32_t smem_lds, const RingLane<NT>& L, int slot, int live) {
+  if constexpr (REM > 0) {
+    ring_unit2<EL, NT, NB, REM, CLIP>(acc, F, G, smem, smem_lds, L, slot, 0, 0, 0, live);
+    ring_tail2<EL, NT, NB, REM - 1, CLIP>(acc, G, F, smem, smem_lds, L, slot, live);
+  }
+}
+// The tail of a product of fewer units than the ring has buffers.
+template <int EL, int NT, int NB, int REM, bool CLIP>
+__device__ __forceinline__ void ring_short2(typename NtTypes<EL>::acc (&acc)[NT][NT], RingUnit<NT>& F, RingUnit<NT>& G,
+                                            uint8_t* smem, uint32_t smem_lds, const RingLane<NT>& L, int NU, int live) {
+  if constexpr (REM > 0) {
+    if (NU == REM) ring_tail2<EL, NT, NB, REM, CLIP>(acc, F, G, smem, smem_lds, L, 0, live);
+    else ring_short2<EL, NT, NB, REM - 1, CLIP>(acc, F, G, smem, smem_lds, L, NU, live);
+  }
+}
+
+// Whether a step is a whole unit.
+constexpr bool ring_whole(int nt, int nb) { return nt <= 3 || (nt == 4 && nb > 2); }
+
 // CLIP: kb is no multiple of 128 (it is one of 16).
 template <int EL, int NT, int NB, bool CLIP, typename Epi>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(ring_lds<NT, NB>() > 80 * 1024 ? 1 : 2, ring_lds<NT, NB>() > 80 * 1024 ? 1 : 2)))
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(160 * 1024 / ring_lds<NT, NB>(), 160 * 1024 / ring_lds<NT, NB>())))
 void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
   typedef typename NtTypes<EL>::acc Acc;
   constexpr int MT = 32 * NT, S = 16 * NT, UNIT = 2 * MT * 128, LD = 2 * NT;
@@ -221,7 +310,7 @@ void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       acc[i][j] = Acc{0, 0, 0, 0};
-      asm volatile("" : "+a"(acc[i][j]));
+      if constexpr (!ring_whole(NT, NB)) asm volatile("" : "+a"(acc[i][j]));
     }
   __builtin_amdgcn_sched_barrier(0);
 
@@ -235,56 +324,123 @@ void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
   else wait_vmcnt<0>();
   lds_barrier();
   if (CLIP && NU == 1) ring_clip<NT>(smem, live);
-  RingFrag<NT> F0, F1;
-  ring_read_all<NT, 0>(F0, smem, L);
-  __builtin_amdgcn_sched_barrier(0);
-
+  // what the first rows of accumulators add is loaded before the last units, so that the
+  // epilogue does not begin with a wait for memory
+  typename Epi::Row row[NT];
+  typename Epi::Add add[3][NT];
+  const auto ahead = [&]() {
+    epi.at(e, m0 + wm * S, n0 + wn * S, r16, 4 * q4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) epi.add(add[i][j], i, j);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) row[i] = epi.row(i);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   int slot = 0;
-  for (int U = 0; U + NB < NU; ++U) {
-    const int nslot = slot + 1 == NB ? 0 : slot + 1;
-    const bool end = CLIP && U + NB == NU - 1;
-    ring_unit<EL, NT, NB, NB + 1, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, nslot, (uint32_t)(U + NB) * 128u,
-                                        end ? be : 0u, end ? bo : 0u, live);
-    slot = nslot;
+  if constexpr (ring_whole(NT, NB)) {
+    RingUnit<NT> F0, F1;
+    ring_read2_all<NT>(F0, smem, L);
+    __builtin_amdgcn_sched_barrier(0);
+    const auto unit = [&](int U, RingUnit<NT>& F, RingUnit<NT>& G) {
+      const bool end = CLIP && U + NB == NU - 1;
+      ring_unit2<EL, NT, NB, NB + 1, CLIP>(acc, F, G, smem, smem_lds, L, slot, (uint32_t)(U + NB) * 128u, end ? be : 0u,
+                                           end ? bo : 0u, live);
+    };
+    int U = 0;
+    for (; U + NB + 1 < NU; U += 2) {
+      unit(U, F0, F1);
+      unit(U + 1, F1, F0);
+    }
+    const bool odd = U + NB < NU;
+    if (odd) unit(U, F0, F1);
+    ahead();
+    if (odd) {
+      ring_tail2<EL, NT, NB, NB, CLIP>(acc, F1, F0, smem, smem_lds, L, slot, live);
+    } else if (NU >= NB) {
+      ring_tail2<EL, NT, NB, NB, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, live);
+    } else {
+      ring_short2<EL, NT, NB, NB - 1, CLIP>(acc, F0, F1, smem, smem_lds, L, NU, live);
+    }
+  } else {
+    RingFrag<NT> F0, F1;
+    ring_read_all<NT, 0>(F0, smem, L);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int U = 0; U + NB < NU; ++U) {
+      const int nslot = slot + 1 == NB ? 0 : slot + 1;
+      const bool end = CLIP && U + NB == NU - 1;
+      ring_unit<EL, NT, NB, NB + 1, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, nslot, (uint32_t)(U + NB) * 128u,
+                                          end ? be : 0u, end ? bo : 0u, live);
+      slot = nslot;
+    }
+    ahead();
+    ring_tail<EL, NT, NB, NB, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, NU, live);
   }
-  ring_tail<EL, NT, NB, NB, CLIP>(acc, F0, F1, smem, smem_lds, L, slot, NU, live);
 
   // every wave is done with the ring (the epilogue reuses the LDS; no load is in
   // flight), and the last MFMAs' results have reached the accumulators
   lds_barrier();
-  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
+  if constexpr (!ring_whole(NT, NB)) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
-  __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < NT; ++j) asm volatile("" : "+a"(acc[i][j]));
+    __builtin_amdgcn_sched_barrier(0);
+  }
 
-  // 16-bit values, four columns of a row per accumulator, staged by rows
+  // 16-bit values, four columns of a row per accumulator, staged by rows; what is added
+  // to a row of accumulators is loaded two rows ahead (one wave per SIMD: a load that its
+  // use waits for waits alone)
   constexpr int RS = S + 4;
   uint16_t* E = reinterpret_cast<uint16_t*>(smem) + w * S * RS;
-  const int64_t mw = m0 + wm * S, nw = n0 + wn * S;
   ntu2 val[NT][NT];
   {
     typename Epi::Col col[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) col[j] = epi.col(e, nw + j * 16 + 4 * q4);
+    for (int j = 0; j < NT; ++j) col[j] = epi.col(j);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int64_t m = mw + i * 16 + r16;
-      const typename Epi::Row row = epi.row(e, m);
+      if (i + 2 < NT) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) epi.add(add[(i + 2) % 3][j], i + 2, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        val[i][j] = epi.pack4(e, m, nw + j * 16 + 4 * q4, row, col[j], acc[i][j]);
+        val[i][j] = epi.pack4(i, j, row[i], col[j], add[i % 3][j], acc[i][j]);
         *reinterpret_cast<ntu2*>(E + (i * 16 + r16) * RS + j * 16 + 4 * q4) = val[i][j];
       }
     }
   }
+  // a wave stores its own part: whole row pieces, as many rows at a time as its lanes cover
+  constexpr int PP = S / 8, RPI = 64 / PP, IT = (S + RPI - 1) / RPI, G = IT < 8 ? IT : 8;
+  const int pr = lane / PP, pc = lane % PP * 8;
+  const auto piece = [&](int row) {
+    const ntu2 x = *reinterpret_cast<const ntu2*>(E + row * RS + pc), y = *reinterpret_cast<const ntu2*>(E + row * RS + pc + 4);
+    return ntu4{x[0], x[1], y[0], y[1]};
+  };
+  const auto row_of = [&](int it) { return it * RPI + pr; };
+  const auto mine = [&](int it) { return pr < RPI && it < IT && row_of(it) < S; };
+  typename Epi::Fetch f[2][G];
+#pragma unroll
+  for (int u = 0; u < G; ++u)
+    if (mine(u)) epi.fetch(f[0][u], row_of(u), pc);
   __syncthreads();
-#pragma unroll 4
-  for (int q = lane; q < S * S / 8; q += 64) {
-    const int row = q / (S / 8), c = q % (S / 8) * 8;
-    const ntu2 x = *reinterpret_cast<const ntu2*>(E + row * RS + c), y = *reinterpret_cast<const ntu2*>(E + row * RS + c + 4);
-    epi.store(e, mw + row, nw + c, ntu4{x[0], x[1], y[0], y[1]});
+  // (loops, not unrolled further: the compiler would hold the addresses of all of them)
+#pragma unroll 1
+  for (int it = 0; it < IT; it += 2 * G) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+        if (mine(it + (h + 1) * G + u)) epi.fetch(f[1 - h][u], row_of(it + (h + 1) * G + u), pc);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+        if (mine(it + h * G + u)) epi.store(row_of(it + h * G + u), pc, piece(row_of(it + h * G + u)), f[h][u]);
+    }
   }
   if (Epi::kTrans && !(g.sym && tm == tn)) {
     // staged again by columns: neighbouring lanes (rows m, m + 1) exchange halves, so
@@ -297,58 +453,59 @@ void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
     for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint32_t mine = odd ? val[i][j][1] : val[i][j][0], give = odd ? val[i][j][0] : val[i][j][1];
+        const uint32_t own = odd ? val[i][j][1] : val[i][j][0], give = odd ? val[i][j][0] : val[i][j][1];
         const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0xB1, 0xF, 0xF, false);   // lane ^ 1
-        const uint32_t lo = odd ? got : mine, hi = odd ? mine : got;      // rows m (even lane's), m + 1
+        const uint32_t lo = odd ? got : own, hi = odd ? own : got;        // rows m (even lane's), m + 1
         uint16_t* d = E + (j * 16 + 4 * q4 + (odd ? 2 : 0)) * RS + i * 16 + (r16 & ~1);
         *reinterpret_cast<uint32_t*>(d) = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
         *reinterpret_cast<uint32_t*>(d + RS) = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
       }
     __syncthreads();
-#pragma unroll 4
-    for (int q = lane; q < S * S / 8; q += 64) {
-      const int c = q / (S / 8), row = q % (S / 8) * 8;
-      const ntu2 x = *reinterpret_cast<const ntu2*>(E + c * RS + row), y = *reinterpret_cast<const ntu2*>(E + c * RS + row + 4);
-      epi.store_t(e, nw + c, mw + row, ntu4{x[0], x[1], y[0], y[1]});
+#pragma unroll 1
+    for (int it = 0; it < IT; it += G) {
+#pragma unroll
+      for (int u = 0; u < G; ++u)
+        if (mine(it + u)) epi.store_t(row_of(it + u), pc, piece(row_of(it + u)));
     }
   }
-  epi.finish(e);
+  epi.finish();
 }
 
 // ---------------------------------------------------------------- choice of kernel
 
-// What a tile costs, in microseconds measured on an MI355X (8-bit integers; FP16 is
-// 10-20% slower on every kernel): a unit of 128 bytes of K when all compute units are
-// busy and when few are, and a tile besides its units; `per_cu` workgroups share a
-// compute unit at that cost.
+// What a tile costs, in microseconds measured on an MI355X with 8-bit integers (a unit of
+// FP16 takes 1.15 times as long): a unit of 128 bytes of K when all compute units are busy
+// and when few are, a tile besides its units, and what an epilogue that reads takes on
+// top; `per_cu` workgroups share a compute unit at that cost.
 struct NtCost {
-  int kernel, mt, nt, per_cu;
-  float full, few, tile;
+  int kernel, side_m, side_n, per_cu;
+  float full, few, tile, reads;
 };
 constexpr NtCost kNtCosts[] = {
-    {kNtDirect16x64, 16, 64, 1, 0.29f, 0.22f, 1.9f}, {kNtDirect64x64, 64, 64, 1, 0.52f, 0.50f, 2.0f},
-    {kNtRing64, 64, 64, 2, 0.42f, 0.22f, 2.2f},      {kNtRing128, 128, 128, 2, 0.80f, 0.78f, 2.0f},
-    {kNtRing128x5, 128, 128, 1, 0.47f, 0.42f, 2.7f}, {kNtRing192, 192, 192, 1, 0.82f, 0.61f, 8.0f},
-    {kNtRing256, 256, 256, 1, 1.29f, 0.97f, 13.0f},
+    {kNtDirect16x64, 16, 64, 1, 0.29f, 0.22f, 1.9f, 0.0f}, {kNtDirect64x64, 64, 64, 1, 0.52f, 0.50f, 2.0f, 0.0f},
+    {kNtRing64, 64, 64, 3, 0.58f, 0.18f, 2.0f, 0.8f},      {kNtRing96, 96, 96, 1, 0.34f, 0.29f, 2.0f, 1.5f},
+    {kNtRing128, 128, 128, 2, 0.84f, 0.42f, 2.0f, 2.0f},   {kNtRing128x5, 128, 128, 1, 0.50f, 0.41f, 2.4f, 2.5f},
+    {kNtRing192, 192, 192, 1, 0.83f, 0.62f, 6.0f, 5.0f},   {kNtRing256, 256, 256, 1, 1.33f, 0.98f, 9.0f, 10.0f},
 };
 
 // The kernel with the least estimated time: full rounds of workgroups over the compute
 // units, and a last round that is cheaper the emptier it is.  direct, ring: which kinds
-// there are to choose from.
-inline int nt_choose(const NtArgs& g, bool direct, bool ring) {
+// there are to choose from; f16, reads: the element type, and whether the epilogue reads.
+inline int nt_choose(const NtArgs& g, bool direct, bool ring, bool f16, bool reads) {
   const double cus = device_cus() > 0 ? device_cus() : 256;
-  const double units = (double)((g.kb + 127) / 128);
+  const double units = (double)((g.kb + 127) / 128) * (f16 ? 1.15 : 1.0);
   int best = direct ? kNtDirect64x64 : kNtRing64;
   double least = 1e300;
   for (const NtCost& c : kNtCosts) {
     const bool is_direct = c.kernel == kNtDirect16x64 || c.kernel == kNtDirect64x64;
     if (is_direct ? !direct : !ring) continue;
-    const int64_t tm = (g.M + c.mt - 1) / c.mt, tn = (g.N + c.nt - 1) / c.nt;
+    const int64_t tm = (g.M + c.side_m - 1) / c.side_m, tn = (g.N + c.side_n - 1) / c.side_n;
     const double tiles = (double)(g.sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch, slots = cus * c.per_cu;
     const double rounds = (double)(int64_t)(tiles / slots), last = tiles / slots - rounds;
-    double us = rounds * (units * c.full + c.tile);
-    if (last > 0) us += units * (c.few + (c.full - c.few) * last) + c.tile;
-    if (!is_direct && g.kb % 128 != 0) us += 1.0;             // the last unit clipped in LDS
+    const double tile = c.tile + (reads ? c.reads : 0.0f);
+    double us = rounds * (units * c.full + tile);
+    if (last > 0) us += units * (c.few + (c.full - c.few) * last) + tile;
+    if (!is_direct && g.kb % 128 != 0) us += 1.0;          // the last unit clipped in LDS
     if (us < least) {
       least = us;
       best = c.kernel;

@@ -185,173 +185,298 @@ struct NsSquare {
   float* d;
 };
 
-// A symmetric product of two such matrices (or of X and its transpose: l, r null), the
-// MFMAs having formed the product of their FP16 parts; the tile on the other side of the
+// A wave's part of a padded matrix of rows x cols, both multiples of 16, so that a 16 x 16
+// block lies inside or outside as a whole.  Blocks outside are computed on the last one's
+// inputs and not stored; a part that lies outside altogether is computed on the first's.
+struct NsPart {
+  int M, N;                      // rows and columns from the part's first
+  bool dead;
+  int64_t m0, n0;
+  uint32_t lane;                 // the lane's element in a block
+  __device__ __forceinline__ void at(int rows, int cols, int64_t m, int64_t n, int r16, int c4) {
+    dead = m >= rows || n >= cols;
+    m0 = dead ? 0 : m;
+    n0 = dead ? 0 : n;
+    M = rows - (int)m0;
+    N = cols - (int)n0;
+    lane = (uint32_t)(r16 * cols + c4);
+  }
+  // the block's first element, from the part's, in a matrix with rows of cols
+  __device__ __forceinline__ int block(int i, int j, int cols) const { return min(16 * i, M - 16) * cols + min(16 * j, N - 16); }
+  __device__ __forceinline__ bool inside(int i, int j) const { return !dead && 16 * i < M && 16 * j < N; }
+};
+// Four 16-bit elements of the lane: a uniform address plus the lane's offset, so that a
+// block costs scalar operations only.
+__device__ __forceinline__ ntu2 ns_load(const uint16_t* p, int block, uint32_t lane) {
+  const uint16_t* q = p + block;
+  return *reinterpret_cast<const ntu2*>(reinterpret_cast<const uint8_t*>(q) + 2u * lane);
+}
+
+// A symmetric product of two such matrices, the MFMAs having formed the product of their
+// FP16 parts: of two different ones (kNsProduct), or a matrix's polynomial (kNsPoly, l is
+// r), or of X and its transpose (kNsGram, neither); the tile on the other side of the
 // diagonal is stored too.
 //   entry (i, j)  alpha sum + r_ij (k0 + k1 dl_i) + l_ij (k0 + k1 dr_j)
 //   entry (i, i)  alpha / kS sum + q0 + q1 dl_i + q2 dl_i dr_i, in FP32
+enum NsMode { kNsGram = 0, kNsPoly = 1, kNsProduct = 2 };
+template <int MODE>
 struct EpiNsSquare {
-  static constexpr bool kTrans = true;
+  static constexpr bool kTrans = true, kReads = MODE != kNsGram;
   NsSquare c;
   const uint16_t* l;
   const uint16_t* r;
   const float* dl;
   const float* dr;
-  int64_t m_;                    // side
+  int side;                      // at most 2^22; offsets inside a tile's rows fit 32 bits
   float alpha, k0, k1, q0, q1, q2;
-  struct Row { float d; };
-  struct Col { float d[4]; };
-  __device__ __forceinline__ Row row(int e, int64_t m) const { return Row{dl ? dl[e * m_ + min(m, m_ - 1)] : 0.0f}; }
-  __device__ __forceinline__ Col col(int e, int64_t n) const {
-    Col k;
+  uint16_t* t;                   // the tile on the other side of the diagonal
+  NsPart p;
+  int diag, r16, c4;             // block (i, j) holds the diagonal where 16 i + diag is 16 j
+  struct Row { float k; };
+  struct Col { ntf4 k; };
+  struct Add { ntu2 l, r; };
+  typedef EpiNothing Fetch;
+  __device__ __forceinline__ void at(int e, int64_t m0, int64_t n0, int r16_, int c4_) {
+    p.at(side, side, m0, n0, r16_, c4_);
+    const int64_t base = (int64_t)e * side, o = (base + p.m0) * side + p.n0;
+    t = c.e + (base + p.n0) * side + p.m0;
+    c.e += o;
+    c.d += base + p.m0;
+    if constexpr (MODE != kNsGram) {
+      l += o;
+      r += o;
+      dl += base + p.m0;
+      dr += base + p.n0;
+    }
+    diag = (int)(p.m0 - p.n0);
+    r16 = r16_;
+    c4 = c4_;
+  }
+  __device__ __forceinline__ Row row(int i) const {
+    if constexpr (MODE == kNsGram) return Row{0.0f};
+    else return Row{__builtin_fmaf(k1, dl[min(16 * i, p.M - 16) + r16], k0)};
+  }
+  __device__ __forceinline__ Col col(int j) const {
+    Col k{ntf4{0.0f, 0.0f, 0.0f, 0.0f}};
+    if constexpr (MODE != kNsGram) {
+      const ntf4 d = *reinterpret_cast<const ntf4*>(dr + min(16 * j, p.N - 16) + c4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) k.d[i] = dr ? dr[e * m_ + min(n, m_ - 4) + i] : 0.0f;
+      for (int i = 0; i < 4; ++i) k.k[i] = __builtin_fmaf(k1, d[i], k0);
+    }
     return k;
   }
-  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+  __device__ __forceinline__ void add(Add& x, int i, int j) const {
+    if constexpr (MODE != kNsGram) x.r = ns_load(r, p.block(i, j, side), p.lane);
+    if constexpr (MODE == kNsProduct) x.l = ns_load(l, p.block(i, j, side), p.lane);
+  }
+  __device__ __forceinline__ ntu2 pack4(int i, int j, const Row& a, const Col& b, const Add& x, ntf4 v) const {
     float y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = alpha * v[i];
-    if (r) {
-      const int64_t at = (e * m_ + min(m, m_ - 1)) * m_ + min(n, m_ - 4);
-      const ntu2 x = *reinterpret_cast<const ntu2*>(r + at);
-      const ntu2 w = l == r ? x : *reinterpret_cast<const ntu2*>(l + at);
-      const float kr = k0 + k1 * a.d;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float xr = i & 1 ? f16_hi(x[i >> 1]) : f16_lo(x[i >> 1]), xl = i & 1 ? f16_hi(w[i >> 1]) : f16_lo(w[i >> 1]);
-        y[i] = y[i] + xr * kr + xl * (k0 + k1 * b.d[i]);
+    for (int k = 0; k < 4; ++k) {
+      y[k] = alpha * v[k];
+      if constexpr (MODE != kNsGram) {
+        const float xr = k & 1 ? f16_hi(x.r[k >> 1]) : f16_lo(x.r[k >> 1]);
+        if constexpr (MODE == kNsPoly) {
+          y[k] = __builtin_fmaf(xr, a.k + b.k[k], y[k]);
+        } else {
+          const float xl = k & 1 ? f16_hi(x.l[k >> 1]) : f16_lo(x.l[k >> 1]);
+          y[k] = __builtin_fmaf(xl, b.k[k], __builtin_fmaf(xr, a.k, y[k]));
+        }
       }
     }
-    if (m >= n && m < n + 4 && m < m_) {
+    if (16 * i + diag == 16 * j && p.inside(i, j)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (m == n + i) {
-          c.d[e * m_ + m] = alpha * (1.0f / kS) * v[i] + (q0 + q1 * a.d + q2 * (a.d * b.d[i]));
-          y[i] = 0.0f;
+      for (int k = 0; k < 4; ++k)
+        if (r16 == c4 + k) {
+          float d = alpha * (1.0f / kS) * v[k];
+          if constexpr (MODE != kNsGram) {
+            const float u = dl[16 * i + r16], w = dr[16 * j + r16];
+            d += q0 + q1 * u + q2 * (u * w);
+          }
+          c.d[16 * i + r16] = d;
+          y[k] = 0.0f;
         }
     }
     return ntu2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
   }
-  __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
-    if (m < m_ && n < m_) *reinterpret_cast<ntu4*>(c.e + (e * m_ + m) * m_ + n) = v;
+  __device__ __forceinline__ void fetch(Fetch&, int, int) const {}
+  __device__ __forceinline__ void store(int m, int n, const ntu4& v, const Fetch&) {
+    if (!p.dead && m < p.M && n < p.N) *reinterpret_cast<ntu4*>(c.e + (uint32_t)(m * side + n)) = v;
   }
-  __device__ __forceinline__ void store_t(int e, int64_t n, int64_t m, const ntu4& v) { store(e, n, m, v); }
-  __device__ __forceinline__ void finish(int) {}
+  __device__ __forceinline__ void store_t(int n, int m, const ntu4& v) {
+    if (!p.dead && m < p.M && n < p.N) *reinterpret_cast<ntu4*>(t + (uint32_t)(n * side + m)) = v;
+  }
+  __device__ __forceinline__ void finish() {}
 };
 
-// What the products P X (X in the matrix's own orientation, M x N) add to the MFMAs' sum
-// of P's FP16 part and X's: P's diagonal times X, whole.  In units of X under kS.
+// What the products P X (X in the matrix's own orientation, rows x cols) add to the MFMAs'
+// sum of P's FP16 part and X's: P's diagonal times X, whole.  In units of X under kS.
+// WIDE: rows <= cols, the diagonal runs along the rows.
+template <bool WIDE>
 struct NsApply {
   const uint16_t* hi;
   const uint16_t* lo;
   const float* d;
-  int64_t M, N;
-  bool wide;                     // M <= N: the diagonal runs along M
+  int rows, cols;
+  NsPart p;
+  int r16, c4;
   struct Row { float d; };
-  struct Col { float d[4]; };
-  __device__ __forceinline__ Row row(int e, int64_t m) const { return Row{wide ? d[e * M + min(m, M - 1)] : 0.0f}; }
-  __device__ __forceinline__ Col col(int e, int64_t n) const {
-    Col k;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) k.d[i] = wide ? 0.0f : d[e * N + min(n, N - 4) + i];
-    return k;
+  struct Col { ntf4 d; };
+  struct Add { ntu2 hi, lo; };
+  __device__ __forceinline__ int64_t at(int e, int64_t m0, int64_t n0, int r16_, int c4_) {
+    p.at(rows, cols, m0, n0, r16_, c4_);
+    const int64_t o = ((int64_t)e * rows + p.m0) * cols + p.n0;
+    hi += o;
+    lo += o;
+    d += WIDE ? (int64_t)e * rows + p.m0 : (int64_t)e * cols + p.n0;
+    r16 = r16_;
+    c4 = c4_;
+    return o;
   }
-  __device__ __forceinline__ int64_t at(int e, int64_t m, int64_t n) const {
-    return (e * M + min(m, M - 1)) * N + min(n, N - 4);
+  __device__ __forceinline__ Row row(int i) const { return Row{WIDE ? d[min(16 * i, p.M - 16) + r16] : 0.0f}; }
+  __device__ __forceinline__ Col col(int j) const {
+    if constexpr (WIDE) return Col{ntf4{0.0f, 0.0f, 0.0f, 0.0f}};
+    else return Col{*reinterpret_cast<const ntf4*>(d + min(16 * j, p.N - 16) + c4)};
   }
-  __device__ __forceinline__ void sums(int64_t at, const Row& a, const Col& b, ntf4 v, float (&y)[4]) const {
-    const ntu2 h = *reinterpret_cast<const ntu2*>(hi + at), l = *reinterpret_cast<const ntu2*>(lo + at);
+  __device__ __forceinline__ void add(Add& x, int i, int j) const {
+    const int b = p.block(i, j, cols);
+    x.hi = ns_load(hi, b, p.lane);
+    x.lo = ns_load(lo, b, p.lane);
+  }
+  __device__ __forceinline__ void sums(const Row& a, const Col& b, const Add& o, ntf4 v, float (&y)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = (i & 1 ? f16_hi(h[i >> 1]) : f16_lo(h[i >> 1])) +
-                      (i & 1 ? f16_hi(l[i >> 1]) : f16_lo(l[i >> 1])) * (1.0f / kLo);
-      y[i] = v[i] * (1.0f / kS) + (wide ? a.d : b.d[i]) * x;
+      const float h = i & 1 ? f16_hi(o.hi[i >> 1]) : f16_lo(o.hi[i >> 1]);
+      const float l = i & 1 ? f16_hi(o.lo[i >> 1]) : f16_lo(o.lo[i >> 1]);
+      const float x = __builtin_fmaf(l, 1.0f / kLo, h);
+      y[i] = __builtin_fmaf(v[i], 1.0f / kS, (WIDE ? a.d : b.d[i]) * x);
     }
   }
 };
 
 // The next X: FP16, the rest of its rounding (in place), and its transpose.
+template <bool WIDE>
 struct EpiNsNext {
-  static constexpr bool kTrans = true;
-  NsApply x;
+  static constexpr bool kTrans = true, kReads = true;
+  NsApply<WIDE> x;
   uint16_t* hi;
   uint16_t* lo;
   uint16_t* t;
-  typedef NsApply::Row Row;
-  typedef NsApply::Col Col;
-  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
-  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
-  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
-    const int64_t at = x.at(e, m, n);
+  typedef typename NsApply<WIDE>::Row Row;
+  typedef typename NsApply<WIDE>::Col Col;
+  typedef typename NsApply<WIDE>::Add Add;
+  typedef EpiNothing Fetch;
+  __device__ __forceinline__ void at(int e, int64_t m0, int64_t n0, int r16, int c4) {
+    const int64_t o = x.at(e, m0, n0, r16, c4);
+    hi += o;
+    lo += o;
+    t += ((int64_t)e * x.cols + x.p.n0) * x.rows + x.p.m0;
+  }
+  __device__ __forceinline__ Row row(int i) const { return x.row(i); }
+  __device__ __forceinline__ Col col(int j) const { return x.col(j); }
+  __device__ __forceinline__ void add(Add& o, int i, int j) const { x.add(o, i, j); }
+  __device__ __forceinline__ ntu2 pack4(int i, int j, const Row& a, const Col& b, const Add& o, ntf4 v) const {
     float y[4];
-    x.sums(at, a, b, v, y);
+    x.sums(a, b, o, v, y);
     const ntu2 h = {pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
-    if (m < x.M && n < x.N)
-      *reinterpret_cast<ntu2*>(lo + at) = ntu2{pack_f16x2((y[0] - f16_lo(h[0])) * kLo, (y[1] - f16_hi(h[0])) * kLo),
-                                               pack_f16x2((y[2] - f16_lo(h[1])) * kLo, (y[3] - f16_hi(h[1])) * kLo)};
+    if (x.p.inside(i, j)) {
+      float l[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)                          // (y - h) kLo, exact
+        l[k] = __builtin_fmaf(k & 1 ? f16_hi(h[k >> 1]) : f16_lo(h[k >> 1]), -kLo, y[k] * kLo);
+      uint16_t* q = lo + x.p.block(i, j, x.cols);
+      *reinterpret_cast<ntu2*>(reinterpret_cast<uint8_t*>(q) + 2u * x.p.lane) =
+          ntu2{pack_f16x2(l[0], l[1]), pack_f16x2(l[2], l[3])};
+    }
     return h;
   }
-  __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
-    if (m < x.M && n < x.N) *reinterpret_cast<ntu4*>(hi + (e * x.M + m) * x.N + n) = v;
+  __device__ __forceinline__ void fetch(Fetch&, int, int) const {}
+  __device__ __forceinline__ void store(int m, int n, const ntu4& v, const Fetch&) {
+    if (!x.p.dead && m < x.p.M && n < x.p.N) *reinterpret_cast<ntu4*>(hi + (uint32_t)(m * x.cols + n)) = v;
   }
-  __device__ __forceinline__ void store_t(int e, int64_t n, int64_t m, const ntu4& v) {
-    if (m < x.M && n < x.N) *reinterpret_cast<ntu4*>(t + (e * x.N + n) * x.M + m) = v;
+  __device__ __forceinline__ void store_t(int n, int m, const ntu4& v) {
+    if (!x.p.dead && m < x.p.M && n < x.p.N) *reinterpret_cast<ntu4*>(t + (uint32_t)(n * x.rows + m)) = v;
   }
-  __device__ __forceinline__ void finish(int) {}
+  __device__ __forceinline__ void finish() {}
 };
 
 // BF16(X) of the matrix without its padding.
+template <bool WIDE>
 struct EpiNsOut {
-  static constexpr bool kTrans = false;
-  NsApply x;
+  static constexpr bool kTrans = false, kReads = true;
+  NsApply<WIDE> x;
   uint16_t* out;
-  int64_t rows, cols;
-  typedef NsApply::Row Row;
-  typedef NsApply::Col Col;
-  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
-  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
-  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+  int rows, cols;
+  int M, N;
+  typedef typename NsApply<WIDE>::Row Row;
+  typedef typename NsApply<WIDE>::Col Col;
+  typedef typename NsApply<WIDE>::Add Add;
+  typedef EpiNothing Fetch;
+  __device__ __forceinline__ void at(int e, int64_t m0, int64_t n0, int r16, int c4) {
+    x.at(e, m0, n0, r16, c4);
+    out += ((int64_t)e * rows + m0) * cols + n0;
+    M = rows - (int)m0;
+    N = cols - (int)n0;
+  }
+  __device__ __forceinline__ Row row(int i) const { return x.row(i); }
+  __device__ __forceinline__ Col col(int j) const { return x.col(j); }
+  __device__ __forceinline__ void add(Add& o, int i, int j) const { x.add(o, i, j); }
+  __device__ __forceinline__ ntu2 pack4(int, int, const Row& a, const Col& b, const Add& o, ntf4 v) const {
     float y[4];
-    x.sums(x.at(e, m, n), a, b, v, y);
+    x.sums(a, b, o, v, y);
     constexpr float k = 1.0f / kS;
     return ntu2{pack_bf16x2(k * y[0], k * y[1]), pack_bf16x2(k * y[2], k * y[3])};
   }
-  __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
-    if (m >= rows || n >= cols) return;
+  __device__ __forceinline__ void fetch(Fetch&, int, int) const {}
+  __device__ __forceinline__ void store(int m, int n, const ntu4& v, const Fetch&) {
+    if (m >= M || n >= N) return;
     Raw<uint16_t> r;
     r.v[0] = v;
-    store_raw<false>(out + (e * rows + m) * cols, (int)n, (int)cols, r);
+    store_raw<false>(out + (m * cols + n), 0, N - n, r);
   }
-  __device__ __forceinline__ void store_t(int, int64_t, int64_t, const ntu4&) {}
-  __device__ __forceinline__ void finish(int) {}
+  __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
+  __device__ __forceinline__ void finish() {}
 };
 
 // w <- keep w - step X, its BF16 copy and that copy's largest magnitude.  X passes
 // through LDS in FP16 (2^-11 of an entry, below the products' own error).
+template <bool WIDE>
 struct EpiNsUpdate {
-  static constexpr bool kTrans = false;
-  NsApply x;
+  static constexpr bool kTrans = false, kReads = true;
+  NsApply<WIDE> x;
   float* w;
   uint16_t* wb;
   float* amax;                   // null: none
-  int64_t rows, cols;
+  int rows, cols;
   float keep, step;              // step of X under kS
   uint32_t most;
-  typedef NsApply::Row Row;
-  typedef NsApply::Col Col;
-  __device__ __forceinline__ Row row(int e, int64_t m) const { return x.row(e, m); }
-  __device__ __forceinline__ Col col(int e, int64_t n) const { return x.col(e, n); }
-  __device__ __forceinline__ ntu2 pack4(int e, int64_t m, int64_t n, const Row& a, const Col& b, ntf4 v) const {
+  int M, N;
+  typedef typename NsApply<WIDE>::Row Row;
+  typedef typename NsApply<WIDE>::Col Col;
+  typedef typename NsApply<WIDE>::Add Add;
+  typedef Raw<float> Fetch;
+  __device__ __forceinline__ void at(int e, int64_t m0, int64_t n0, int r16, int c4) {
+    x.at(e, m0, n0, r16, c4);
+    const int64_t o = ((int64_t)e * rows + m0) * cols + n0;
+    w += o;
+    wb += o;
+    M = rows - (int)m0;
+    N = cols - (int)n0;
+  }
+  __device__ __forceinline__ Row row(int i) const { return x.row(i); }
+  __device__ __forceinline__ Col col(int j) const { return x.col(j); }
+  __device__ __forceinline__ void add(Add& o, int i, int j) const { x.add(o, i, j); }
+  __device__ __forceinline__ ntu2 pack4(int, int, const Row& a, const Col& b, const Add& o, ntf4 v) const {
     float y[4];
-    x.sums(x.at(e, m, n), a, b, v, y);
+    x.sums(a, b, o, v, y);
     return ntu2{pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
   }
-  __device__ __forceinline__ void store(int e, int64_t m, int64_t n, const ntu4& v) {
-    if (m >= rows || n >= cols) return;
-    const int64_t at = (e * rows + m) * cols + n;
-    const int len = (int)min((int64_t)8, cols - n);
-    Raw<float> r = load_raw<false>(w + at, 0, len);
+  __device__ __forceinline__ void fetch(Fetch& r, int m, int n) const {
+    if (m < M && n < N) r = load_raw<false>(w + (m * cols + n), 0, min(8, N - n));
+  }
+  __device__ __forceinline__ void store(int m, int n, const ntu4& v, Fetch& r) {
+    if (m >= M || n >= N) return;
+    const int at = m * cols + n, len = min(8, N - n);
     float y[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = keep * raw_at(r, i) - step * (i & 1 ? f16_hi(v[i >> 1]) : f16_lo(v[i >> 1]));
@@ -366,8 +491,8 @@ struct EpiNsUpdate {
     store_raw<false>(w + at, 0, len, r);
     store_raw<false>(wb + at, 0, len, b);
   }
-  __device__ __forceinline__ void store_t(int, int64_t, int64_t, const ntu4&) {}
-  __device__ __forceinline__ void finish(int) {
+  __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
+  __device__ __forceinline__ void finish() {
     if (!amax) return;
     const uint32_t m = wave_max_dpp(most);
     if ((threadIdx.x & 63) == 0) atomicMax(reinterpret_cast<uint32_t*>(amax), m);
@@ -379,9 +504,10 @@ hipError_t product(const uint16_t* a, const uint16_t* b, int64_t M, int64_t N, i
                    const Epi& epi, int kernel, hipStream_t s) {
   const NtArgs g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), M, N, (uint32_t)(2 * K),
                  2 * M * K, 2 * N * K, (int)batch, sym};
-  switch (kernel == kNtChosen ? nt_choose(g, false, true) : kernel) {
+  switch (kernel == kNtChosen ? nt_choose(g, false, true, true, Epi::kReads) : kernel) {
     case kNtRing128: return run_nt_ring<kNtF16, 4, 2, false>(g, epi, s);
-    case kNtRing64: return run_nt_ring<kNtF16, 2, 4, false>(g, epi, s);
+    case kNtRing64: return run_nt_ring<kNtF16, 2, 3, false>(g, epi, s);
+    case kNtRing96: return run_nt_ring<kNtF16, 3, 6, false>(g, epi, s);
     case kNtRing128x5: return run_nt_ring<kNtF16, 4, 5, false>(g, epi, s);
     case kNtRing192: return run_nt_ring<kNtF16, 6, 3, false>(g, epi, s);
     case kNtRing256: return run_nt_ring<kNtF16, 8, 2, false>(g, epi, s);
@@ -410,6 +536,27 @@ bool ns_sizes(int64_t batch, int64_t rows, int64_t cols, NsSizes* z) {
   z->diag_bytes = batch * z->m * 4;                        // a multiple of 256
   z->bytes = z->parts_bytes + 4 * z->diag_bytes + batch * 2 * (4 * z->x + 4 * z->sq);
   return true;
+}
+
+// P X in the matrix's own orientation, X being x [m][n] and its transpose xt: the next X
+// (x, its transpose xn, the rest lo), or the result.
+struct NsBuffers {
+  uint16_t* x;
+  uint16_t* xt;
+  uint16_t* xn;
+  uint16_t* lo;
+  NsSquare p;
+};
+template <bool WIDE>
+hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool more, hipStream_t s) {
+  const uint16_t *l = WIDE ? b.p.e : b.xt, *r = WIDE ? b.xt : b.p.e;
+  const NsApply<WIDE> a{WIDE ? b.x : b.xt, b.lo, b.p.d, (int)z.rows64, (int)z.cols64};
+  const auto run = [&](const auto& epi) { return product(l, r, z.rows64, z.cols64, z.m, o.batch, false, epi, o.kernel, s); };
+  if (more) return run(EpiNsNext<WIDE>{a, WIDE ? b.x : b.xn, b.lo, WIDE ? b.xn : b.x});
+  if (o.w)
+    return run(EpiNsUpdate<WIDE>{a, o.w, static_cast<uint16_t*>(o.w_bf16), o.amax, (int)o.rows, (int)o.cols, o.keep,
+                                 o.step / kS, 0u, 0, 0});
+  return run(EpiNsOut<WIDE>{a, static_cast<uint16_t*>(o.out), (int)o.rows, (int)o.cols, 0, 0});
 }
 
 // Steps from step i on that share one Gram matrix, the phase before having been of
@@ -475,42 +622,35 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
-  // c = the product of symmetric matrices l and r, or (poly) a I + b l + c l^2
-  const auto multiply = [&](const NsSquare& l, const NsSquare& r, const NsSquare& c, const float* poly) {
-    const EpiNsSquare epi = poly ? EpiNsSquare{c, l.e, l.e, l.d, l.d, z.m, poly[2] / kS, 0.5f * poly[1], poly[2],
-                                               poly[0], poly[1], poly[2]}
-                                 : EpiNsSquare{c, l.e, r.e, l.d, r.d, z.m, 1.0f / kS, 0.0f, 1.0f, 0.0f, 0.0f, 1.0f};
+  // c = the product of symmetric matrices l and r, or a I + b l + c l^2
+  const auto multiply = [&](const NsSquare& l, const NsSquare& r, const NsSquare& c) {
+    EpiNsSquare<kNsProduct> epi{c, l.e, r.e, l.d, r.d, (int)z.m};
+    epi.alpha = 1.0f / kS, epi.k1 = 1.0f, epi.q2 = 1.0f;
     return product(l.e, r.e, z.m, z.m, z.m, B, true, epi, o.kernel, s);
+  };
+  const auto polynomial = [&](const NsSquare& l, const NsSquare& c, const float* k) {
+    EpiNsSquare<kNsPoly> epi{c, l.e, l.e, l.d, l.d, (int)z.m};
+    epi.alpha = k[2] / kS, epi.k0 = 0.5f * k[1], epi.k1 = k[2], epi.q0 = k[0], epi.q1 = k[1], epi.q2 = k[2];
+    return product(l.e, l.e, z.m, z.m, z.m, B, true, epi, o.kernel, s);
   };
   for (int i = 0, r = 0; i < o.steps;) {
     r = phase_steps(o, z, i, r);
-    const EpiNsSquare gram{ga, nullptr, nullptr, nullptr, nullptr, z.m, 1.0f / kS, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    EpiNsSquare<kNsGram> gram{ga, nullptr, nullptr, nullptr, nullptr, (int)z.m};
+    gram.alpha = 1.0f / kS;
     e = product(x, x, z.m, z.m, z.n, B, true, gram, o.kernel, s);
-    if (e == hipSuccess) e = multiply(ga, ga, pp, o.coefs + 3 * i);
+    if (e == hipSuccess) e = polynomial(ga, pp, o.coefs + 3 * i);
     if (r == 2) {
-      if (e == hipSuccess) e = multiply(pp, ga, t, nullptr);
-      if (e == hipSuccess) e = multiply(t, pp, ga, nullptr);
-      if (e == hipSuccess) e = multiply(ga, ga, q, o.coefs + 3 * i + 3);
-      if (e == hipSuccess) e = multiply(q, pp, t, nullptr);
+      if (e == hipSuccess) e = multiply(pp, ga, t);
+      if (e == hipSuccess) e = multiply(t, pp, ga);
+      if (e == hipSuccess) e = polynomial(ga, q, o.coefs + 3 * i + 3);
+      if (e == hipSuccess) e = multiply(q, pp, t);
       std::swap(pp, t);
     }
-    if (e != hipSuccess) return e;
     i += r;
-    // P X in the matrix's own orientation
-    const uint16_t *l = wide ? pp.e : xt, *rr = wide ? xt : pp.e;
-    const NsApply apply{wide ? x : xt, lo, pp.d, z.rows64, z.cols64, wide};
-    if (i < o.steps) {
-      const EpiNsNext epi{apply, wide ? x : xn, lo, wide ? xn : x};
-      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
-      std::swap(xt, xn);
-    } else if (o.w) {
-      const EpiNsUpdate epi{apply, o.w, static_cast<uint16_t*>(o.w_bf16), o.amax, o.rows, o.cols, o.keep, o.step / kS, 0u};
-      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
-    } else {
-      const EpiNsOut epi{apply, static_cast<uint16_t*>(o.out), o.rows, o.cols};
-      e = product(l, rr, z.rows64, z.cols64, z.m, B, false, epi, o.kernel, s);
-    }
+    const NsBuffers b{x, xt, xn, lo, pp};
+    if (e == hipSuccess) e = wide ? apply<true>(o, z, b, i < o.steps, s) : apply<false>(o, z, b, i < o.steps, s);
     if (e != hipSuccess) return e;
+    std::swap(xt, xn);
   }
   return hipSuccess;
 }

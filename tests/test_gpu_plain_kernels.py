@@ -19,8 +19,8 @@ from test_gpu_muon import _allowed, _grad
 pytestmark = gpu + [pytest.mark.skipif(not os.path.exists(os.path.join(bsq._PKG, "libbsq_ceiling.so")),
                                        reason="libbsq_ceiling.so not built")]
 
-DIRECT16, DIRECT64, RING128, RING192, RING256, RING128X5, RING64 = range(7)
-RINGS = (RING64, RING128, RING128X5, RING192, RING256)
+DIRECT16, DIRECT64, RING128, RING192, RING256, RING128X5, RING64, RING96 = range(8)
+RINGS = (RING64, RING96, RING128, RING128X5, RING192, RING256)
 
 
 @pytest.fixture(scope="module")
