@@ -787,8 +787,9 @@ bsq_status int8_linear(const void* x, int64_t M, int64_t N, int64_t K, const int
   uint8_t* codes = static_cast<uint8_t*>(workspace);
   float* scales = reinterpret_cast<float*>(codes + (M * K + 15) / 16 * 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (bsq::launch_i8_rows(x, M, K, codes, scales, s) != hipSuccess) return BSQ_EHIP;
   const bsq::Int8Args a{M, N, K, codes, scales, reinterpret_cast<const uint8_t*>(w_codes), w_scales, bias, c, ldc};
+  if (bsq::i8_few_rows(a)) return hip_status(bsq::launch_i8_linear_few(x, a, s));
+  if (bsq::launch_i8_rows(x, M, K, codes, scales, s) != hipSuccess) return BSQ_EHIP;
   return hip_status(bsq::launch_i8_gemm(a, s));
 }
 

@@ -279,16 +279,169 @@ __global__ __launch_bounds__(256) void k_i8_qt(const uint16_t* __restrict__ x, i
   }
 }
 
-template <int NT, int NB>
-hipError_t run_ring(const NtArgs& g, const EpiI8& e, hipStream_t s) {
-  return g.kb % 128 == 0 ? run_nt_ring<kNtI8, NT, NB, false>(g, e, s) : run_nt_ring<kNtI8, NT, NB, true>(g, e, s);
+// ---------------------------------------------------------------- few tokens
+//
+// int8_linear of at most 64 rows in one launch: a workgroup of eight waves per 16
+// columns quantizes all rows into LDS itself, with the weights of its first steps in
+// flight meanwhile, then each wave takes an eighth of K, and the parts are added in LDS.
+// The rows are quantized by every workgroup again, out of the L2: in at most 128 pieces of
+// 512 columns, above which a launch of its own costs less.  Bound by the weights' bytes,
+// or by the launch.
+// LDS rows are whole 128-byte groups; chunk c of row r sits at slot c ^ (r & 7) of its group.
+constexpr int kFewWaves = 8, kFewPieces = 128, kFewRows = 64, kFewAhead = 4;
+template <int MI>
+constexpr int few_part() { return kFewWaves * 16 * MI * (16 + 4) * 4; }
+
+// PT: pieces of x per wave, at most.
+template <int MI, int PT>
+__global__ __launch_bounds__(kFewWaves * 64, PT <= 2 ? 4 : 2) void k_i8_linear(const uint16_t* __restrict__ x, int M, int K,
+                                                              const uint8_t* __restrict__ w, int64_t N,
+                                                              const float* __restrict__ sw,
+                                                              const float* __restrict__ bias, uint16_t* __restrict__ c,
+                                                              int64_t ldc) {
+  constexpr int WK = kFewWaves, NT = 16, MT = 16 * MI, PS = NT + 4, D = kFewAhead;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ uint32_t most[kFewRows];
+  const int lane = threadIdx.x & 63, r16 = lane & 15, q4 = lane >> 4;
+  const int wk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = (int64_t)blockIdx.x * NT;
+  const int ks = (K + 127) & ~127;
+  const int full = K / 128, steps = ks / 128;
+  const int s0 = steps * wk / WK, s1 = steps * (wk + 1) / WK, f1 = min(s1, full);
+  // x: pieces wk, wk + 8, ... of the rows' pieces in turn
+  const int pr = (K + 511) / 512, pieces = M * pr, rcp = 65536 / pr + 1;   // t / pr = t rcp >> 16 for t < 128
+  Raw<uint16_t> v[PT];
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int t = wk + WK * i, row = t * rcp >> 16;
+    if (t < pieces) v[i] = load_raw<true>(x + (int64_t)row * K, (t - row * pr) * 512 + lane * 8, K);
+  }
+  // weights: this lane's row (past the matrix: its last row again)
+  const uint8_t* b = w + n0 * K;
+  const int last_n = (int)min((int64_t)NT - 1, N - n0 - 1);
+  const uint32_t ob = (uint32_t)min(r16, last_n) * (uint32_t)K;
+  ntu4 fb[D][2];
+  const auto load = [&](ntu4 (&f)[2], int s) {
+    const uint32_t k = ob + (uint32_t)s * 128u + (uint32_t)q4 * 16u;
+    f[0] = *reinterpret_cast<const ntu4*>(b + k);
+    f[1] = *reinterpret_cast<const ntu4*>(b + k + 64);
+  };
+#pragma unroll
+  for (int u = 0; u < D; ++u)
+    if (s0 + u < f1) load(fb[u], s0 + u);
+
+  if (threadIdx.x < kFewRows) most[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int t = wk + WK * i;
+    if (t < pieces) {
+      const uint32_t m = wave_max_dpp(max_abs(v[i]));
+      if (lane == 0) atomicMax(&most[t * rcp >> 16], m);   // a maximum: any order
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    const int t = wk + WK * i, row = t * rcp >> 16, col = (t - row * pr) * 512 + lane * 8;
+    if (t < pieces && col < ks) {
+      const float s = i8_enc(most[row]);
+      uint32_t e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = i8_code(raw_at(v[i], j), s);
+      const int ch = col >> 4;
+      const bool in = col < K;                             // the group's rest is zero
+      *reinterpret_cast<ntu2*>(smem + row * ks + (((ch & ~7) | ((ch ^ row) & 7)) << 4) + (col & 8)) =
+          ntu2{in ? i8_pack4(e[0], e[1], e[2], e[3]) : 0u, in ? i8_pack4(e[4], e[5], e[6], e[7]) : 0u};
+    }
+  }
+  __syncthreads();
+
+  nti4 acc[MI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) acc[i] = nti4{0, 0, 0, 0};
+  const auto multiply = [&](const ntu4 (&f)[2], int s) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int row = min(16 * i + r16, M - 1);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const ntu4 a = *reinterpret_cast<const ntu4*>(smem + row * ks + s * 128 + (((4 * h + q4) ^ (row & 7)) << 4));
+        acc[i] = nt_mfma<kNtI8>(f[h], a, acc[i]);
+      }
+    }
+  };
+  for (int s = s0; s < f1; s += D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      if (s + u < f1) {
+        multiply(fb[u], s + u);
+        if (s + u + D < f1) load(fb[u], s + u + D);
+      }
+    }
+  }
+  if (s1 > full && s0 < s1) {                              // the partial group at the row's end
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fb[0][h] = nt_load_end<false>(b + ob, full * 128 + q4 * 16 + 64 * h, K);
+    multiply(fb[0], full);
+  }
+  __syncthreads();                                         // every wave has read the codes
+  nti4* part = reinterpret_cast<nti4*>(smem);              // [WK][MT][PS / 4]
+#pragma unroll
+  for (int i = 0; i < MI; ++i) part[(wk * MT + 16 * i + r16) * PS / 4 + q4] = acc[i];
+  __syncthreads();
+  for (int q = threadIdx.x; q < M * (NT / 4); q += WK * 64) {
+    const int row = q / (NT / 4), col = q % (NT / 4) * 4;
+    nti4 v = part[(row * PS + col) / 4];
+#pragma unroll
+    for (int u = 1; u < WK; ++u) v += part[((u * MT + row) * PS + col) / 4];
+    uint16_t* dst = c + row * ldc + n0 + col;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i <= last_n) {
+        float y = (float)v[i] * (1.0f / i8_enc(most[row]) * sw[n0 + col + i]);
+        if (bias) y = y + bias[n0 + col + i];
+        dst[i] = bf16_rne(y);
+      }
+  }
 }
 
+template <int MI, int PT>
+hipError_t run_few(const void* x, const Int8Args& a, hipStream_t s) {
+  const int codes = (int)(a.M * ((a.K + 127) / 128 * 128)), lds = codes > few_part<MI>() ? codes : few_part<MI>();
+  const void* fn = reinterpret_cast<const void*>(&k_i8_linear<MI, PT>);
+  constexpr int codes_most = PT * kFewWaves * 512, most = codes_most > few_part<MI>() ? codes_most : few_part<MI>();
+  if (lds > most || set_lds_limit(fn, most) != hipSuccess) return hipErrorInvalidConfiguration;
+  const int64_t blocks = (a.N + 15) / 16;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_i8_linear<MI, PT>), dim3((unsigned)blocks), dim3(kFewWaves * 64), lds, s,
+                     static_cast<const uint16_t*>(x), (int)a.M, (int)a.K, a.bc, a.N, a.bs, a.bias,
+                     static_cast<uint16_t*>(a.c), a.ldc);
+  return hipGetLastError();
+}
 }  // namespace
 
 hipError_t launch_i8_rows(const void* x, int64_t rows, int64_t cols, uint8_t* codes, float* scales, hipStream_t s) {
   const bool al = cols % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
   return al ? run_rows_any<true>(x, rows, cols, codes, scales, s) : run_rows_any<false>(x, rows, cols, codes, scales, s);
+}
+
+bool i8_few_rows(const Int8Args& a) {
+  if (a.M > kFewRows || a.K <= 0 || a.K % 16 != 0 || a.K > 8192) return false;
+  // few pieces of x cost little beside the weights; more of them pay only where every
+  // workgroup runs at once, and there by the launch that the host saves (us on the GPU by this
+  // launch / by two: 1 x 28,672 x 4,096 25.9 / 29.8, 1 x 4,096 x 4,096 7.1 / 13.2, 3 x 1,000 x
+  // 512 4.3 / 7.9; 48 x 2,048 x 2,048 9.3 / 9.3, 37 x 2,048 x 1,408 10.2 / 8.1 but 10.4 / 13.1
+  // a call from Python; 8 x 28,672 x 4,096 45.7 / 30.0)
+  const int64_t pieces = a.M * ((a.K + 511) / 512);
+  return pieces <= 2 * kFewWaves || (pieces <= kFewPieces && (a.N + 15) / 16 <= 256);
+}
+
+hipError_t launch_i8_linear_few(const void* x, const Int8Args& a, hipStream_t s) {
+  if (a.M * ((a.K + 511) / 512) <= 2 * kFewWaves) return run_few<1, 2>(x, a, s);   // 16 rows at most
+  constexpr int PT = kFewPieces / kFewWaves;
+  if (a.M <= 16) return run_few<1, PT>(x, a, s);
+  return a.M <= 32 ? run_few<2, PT>(x, a, s) : run_few<4, PT>(x, a, s);
 }
 
 hipError_t launch_i8_qt(const void* x, int64_t rows, int64_t cols, uint8_t* codes_row, float* scales_row,
@@ -319,24 +472,18 @@ NtArgs i8_args(const Int8Args& a) { return NtArgs{a.ac, a.bc, a.M, a.N, (uint32_
 
 int i8_kernel(const Int8Args& a) {
   const NtArgs g = i8_args(a);
-  return nt_choose(g, true, ring_fits(g), false, false);
+  return nt_choose(g, true, ring_fits(g), false, 0.0f).kernel;
 }
 
-hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel) {
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel, int rest, int count) {
   const NtArgs g = i8_args(a);
   const bool vec = a.ldc % 8 == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
   const EpiI8 e{a.as, a.bs, a.bias, static_cast<uint16_t*>(a.c), a.ldc, a.M, a.N, vec, 0, 0, 0, 0};
-  switch (kernel == kNtChosen ? i8_kernel(a) : kernel) {
-    case kNtDirect16x64: return run_nt_direct<kNtI8, 1, 4, 1, 1, 4>(g, e, s);
-    case kNtDirect64x64: return run_nt_direct<kNtI8, 4, 4, 1, 1, 4>(g, e, s);
-    case kNtRing128: return run_ring<4, 2>(g, e, s);
-    case kNtRing64: return run_ring<2, 3>(g, e, s);
-    case kNtRing96: return run_ring<3, 6>(g, e, s);
-    case kNtRing128x5: return run_ring<4, 5>(g, e, s);
-    case kNtRing192: return run_ring<6, 3>(g, e, s);
-    case kNtRing256: return run_ring<8, 2>(g, e, s);
-    default: return hipErrorInvalidValue;
-  }
+  NtChoice c{kernel, rest == kNtChosen ? -1 : count, rest, nt_side(kernel) / nt_side(rest)};
+  if (kernel == kNtChosen) c = nt_choose(g, true, ring_fits(g), false, 0.0f);
+  if (c.kernel == kNtDirect16x64) return run_nt_direct<kNtI8, 1, 4, 1, 1, 4>(g, e, s);
+  if (c.kernel == kNtDirect64x64) return run_nt_direct<kNtI8, 4, 4, 1, 1, 4>(g, e, s);
+  return g.kb % 128 == 0 ? run_nt_choice<kNtI8, false>(g, c, e, s) : run_nt_choice<kNtI8, true>(g, c, e, s);
 }
 
 }  // namespace bsq

@@ -294,9 +294,13 @@ enum NtKernel {
   kNtRing96
 };
 // kernel: one of the above (hipErrorInvalidValue where it does not take these
-// operands), for the tests and measurements of each, or the one that pays.
-hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel = kNtChosen);
+// operands), for the tests and measurements of each, or the one that pays.  rest: the tiles
+// from number `count` on (at most all) cut for this smaller ring kernel.
+hipError_t launch_i8_gemm(const Int8Args& a, hipStream_t s, int kernel = kNtChosen, int rest = kNtChosen, int count = 0);
 int i8_kernel(const Int8Args& a);
+// x [M, K] (BF16) quantized by rows times a.bc, in one launch: few rows (a.ac, a.as unused).
+bool i8_few_rows(const Int8Args& a);
+hipError_t launch_i8_linear_few(const void* x, const Int8Args& a, hipStream_t s);
 
 // ---------------------------------------------------------------- orthogonalisation
 
@@ -320,6 +324,7 @@ struct OrthoArgs {
   void* w_bf16;
   float* amax;                    // or null; cleared here
   int kernel = kNtChosen;         // an NtKernel for every product, or the one that pays
+  int rest = kNtChosen;           // the second half of its tiles cut for this smaller one
 };
 int64_t ortho_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);   // -1: too large
 hipError_t launch_ortho(const OrthoArgs& a, hipStream_t s);

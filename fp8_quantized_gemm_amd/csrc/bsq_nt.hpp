@@ -36,24 +36,29 @@ struct NtArgs {
   bool sym;                      // C is symmetric: only the tiles on and below the diagonal
 };
 
+// The tiles that a launch computes: `count` of the tiles_m x tiles_n grid of a matrix
+// (below the diagonal if symmetric) of each of a stack, from number `first` on in the order
+// of nt_tile, each cut into split x split tiles of the launch's own size.
+struct NtGrid {
+  int first, count, per, tiles_m, tiles_n, split;
+};
+
 inline int64_t nt_tiles(const NtArgs& g, int mt, int nt) {
   const int64_t tm = (g.M + mt - 1) / mt, tn = (g.N + nt - 1) / nt;
   return (g.sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch;
 }
+inline NtGrid nt_grid(const NtArgs& g, int mt, int nt) {
+  const int64_t tm = (g.M + mt - 1) / mt, tn = (g.N + nt - 1) / nt, per = g.sym ? tm * (tm + 1) / 2 : tm * tn;
+  return NtGrid{0, (int)(per * g.batch), (int)per, (int)tm, (int)tn, 1};
+}
 
-// Matrix and tile of block `pid`.  Blocks are dealt round-robin to the 8 XCDs; the
-// remap gives each a contiguous run of the tile order, which sweeps 8 (lower
-// triangle: 4) tile rows at a time so that neighbouring tiles share A and B rows in
-// their L2.
-__device__ __forceinline__ void nt_tile_of(int pid, int total, int batch, bool sym, int tiles_m, int tiles_n, int& e,
-                                           int& tm, int& tn) {
-  const int q = total / 8, r = total % 8, x = pid % 8, i = pid / 8;
-  int t = x * q + (x < r ? x : r) + i;
-  const int per = total / batch;
-  e = t / per;
-  t -= e * per;
+// Matrix e and tile (tm, tn) number t: the order sweeps 8 (lower triangle: 4) tile rows at
+// a time so that neighbouring tiles share A and B rows.
+__device__ __forceinline__ void nt_tile_of(int t, const NtGrid& d, bool sym, int& e, int& tm, int& tn) {
+  e = t / d.per;
+  t -= e * d.per;
   if (!sym) {
-    const int group = 8 * tiles_n, first = t / group * 8, gm = min(tiles_m - first, 8);
+    const int group = 8 * d.tiles_n, first = t / group * 8, gm = min(d.tiles_m - first, 8);
     t %= group;
     tm = first + t % gm;
     tn = t / gm;
@@ -61,11 +66,11 @@ __device__ __forceinline__ void nt_tile_of(int pid, int total, int batch, bool s
   }
   // rows s .. s + h - 1: the h x s tiles left of the diagonal block in columns of
   // four, then the block's triangle
-  int s = 0, h = min(4, tiles_m);
+  int s = 0, h = min(4, d.tiles_m);
   while (t >= h * s + h * (h + 1) / 2) {
     t -= h * s + h * (h + 1) / 2;
     s += 4;
-    h = min(4, tiles_m - s);
+    h = min(4, d.tiles_m - s);
   }
   if (t < h * s) {
     tn = t / (4 * h) * 4;
@@ -80,14 +85,20 @@ __device__ __forceinline__ void nt_tile_of(int pid, int total, int batch, bool s
     tn = s + t;
   }
 }
-
-// The same in scalar registers (the divisions above are vector operations).
-__device__ __forceinline__ void nt_tile(int pid, int total, int batch, bool sym, int tiles_m, int tiles_n, int& e,
-                                        int& tm, int& tn) {
-  nt_tile_of(pid, total, batch, sym, tiles_m, tiles_n, e, tm, tn);
+// The tile of block `pid`, in scalar registers (the divisions are vector operations).
+// Blocks are dealt round-robin to the 8 XCDs; each gets a contiguous run of the order, so
+// that its tiles share rows in its L2.
+__device__ __forceinline__ void nt_tile(int pid, const NtGrid& d, bool sym, int& e, int& tm, int& tn) {
+  const int total = d.count * d.split * d.split, q = total / 8, r = total % 8, x = pid % 8;
+  int t = x * q + (x < r ? x : r) + pid / 8, sub = 0;
+  if (d.split > 1) {
+    sub = t % (d.split * d.split);
+    t /= d.split * d.split;
+  }
+  nt_tile_of(d.first + t, d, sym, e, tm, tn);
   e = __builtin_amdgcn_readfirstlane(e);
-  tm = __builtin_amdgcn_readfirstlane(tm);
-  tn = __builtin_amdgcn_readfirstlane(tn);
+  tm = __builtin_amdgcn_readfirstlane(tm * d.split + sub / d.split);
+  tn = __builtin_amdgcn_readfirstlane(tn * d.split + sub % d.split);
 }
 
 template <int EL>
@@ -207,7 +218,7 @@ struct EpiI8 {
     }
   }
   __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish(uint8_t*) {}
 };
 
 // ---------------------------------------------------------------- direct kernel
@@ -222,7 +233,7 @@ constexpr int nt_direct_lds() {
   return WK * MT * (NT + 4) * 4 + MT * (NT + 4) * 2;
 }
 template <int EL, int MI, int NI, int WM, int WN, int WK, typename Epi>
-__global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
+__global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, NtGrid d, Epi epi) {
   typedef typename NtTypes<EL>::acc Acc;
   constexpr int MT = WM * MI * 16, NT = WN * NI * 16, T = WM * WN * WK * 64;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -230,7 +241,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, int t
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wk = w / (WM * WN), wm = w % (WM * WN) / WN, wn = w % WN;
   int e, tm, tn;
-  nt_tile(blockIdx.x, total, g.batch, g.sym, tiles_m, tiles_n, e, tm, tn);
+  nt_tile(blockIdx.x, d, g.sym, e, tm, tn);
   const int64_t m0 = (int64_t)tm * MT, n0 = (int64_t)tn * NT;
   const uint8_t* a = g.a + e * g.stride_a + m0 * g.kb;
   const uint8_t* b = g.b + e * g.stride_b + n0 * g.kb;
@@ -320,7 +331,7 @@ __global__ __launch_bounds__(WM * WN * WK * 64) void k_nt_direct(NtArgs g, int t
     const ntu2 x = *reinterpret_cast<const ntu2*>(E + row * RS + col), y = *reinterpret_cast<const ntu2*>(E + row * RS + col + 4);
     epi.store(row, col, ntu4{x[0], x[1], y[0], y[1]}, EpiNothing{});
   }
-  epi.finish();
+  epi.finish(smem);
 }
 
 template <int EL, int MI, int NI, int WM, int WN, int WK, typename Epi>
@@ -333,7 +344,7 @@ hipError_t run_nt_direct(const NtArgs& g, const Epi& epi, hipStream_t s) {
   const void* fn = reinterpret_cast<const void*>(&k_nt_direct<EL, MI, NI, WM, WN, WK, Epi>);
   if (LDS > 64 * 1024 && set_lds_limit(fn, LDS) != hipSuccess) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_nt_direct<EL, MI, NI, WM, WN, WK, Epi>), dim3((unsigned)total), dim3(WM * WN * WK * 64), LDS, s, g,
-                     (int)total, (int)((g.M + MT - 1) / MT), (int)((g.N + NT - 1) / NT), epi);
+                     nt_grid(g, MT, NT), epi);
   return hipGetLastError();
 }
 

@@ -268,15 +268,17 @@ constexpr bool ring_whole(int nt, int nb) { return nt <= 3 || (nt == 4 && nb > 2
 // CLIP: kb is no multiple of 128 (it is one of 16).
 template <int EL, int NT, int NB, bool CLIP, typename Epi>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(160 * 1024 / ring_lds<NT, NB>(), 160 * 1024 / ring_lds<NT, NB>())))
-void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
+void k_nt_ring(NtArgs g, NtGrid d, Epi epi) {
   typedef typename NtTypes<EL>::acc Acc;
   constexpr int MT = 32 * NT, S = 16 * NT, UNIT = 2 * MT * 128, LD = 2 * NT;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const uint32_t smem_lds = (uint32_t)(size_t)(__attribute__((address_space(3))) uint8_t*)smem;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 1, wn = w & 1;
   int e, tm, tn;
-  nt_tile(blockIdx.x, total, g.batch, g.sym, tiles_m, tiles_n, e, tm, tn);
+  nt_tile(blockIdx.x, d, g.sym, e, tm, tn);
   const int64_t m0 = (int64_t)tm * MT, n0 = (int64_t)tn * MT;
+  // parts of a cut tile above the diagonal, or past the matrix
+  if (d.split > 1 && ((g.sym && tn > tm) || m0 >= g.M || n0 >= g.N)) return;
   const int last_m = (int)(g.M - m0 < MT ? g.M - m0 - 1 : MT - 1), last_n = (int)(g.N - n0 < MT ? g.N - n0 - 1 : MT - 1);
   const int NU = (int)((g.kb + 127) / 128);
   RingLane<NT> L;
@@ -468,47 +470,75 @@ void k_nt_ring(NtArgs g, int total, int tiles_m, int tiles_n, Epi epi) {
         if (mine(it + u)) epi.store_t(row_of(it + u), pc, piece(row_of(it + u)));
     }
   }
-  epi.finish();
+  epi.finish(smem);
 }
 
 // ---------------------------------------------------------------- choice of kernel
 
 // What a tile costs, in microseconds measured on an MI355X with 8-bit integers (a unit of
-// FP16 takes 1.15 times as long): a unit of 128 bytes of K when all compute units are busy
-// and when few are, a tile besides its units, and what an epilogue that reads takes on
-// top; `per_cu` workgroups share a compute unit at that cost.
+// FP16 takes 1.2 times as long): a unit of 128 bytes of K when all compute units are busy
+// and when few are, a tile besides its units, and what the epilogue of a polynomial of the
+// orthogonalisation takes on top (Epi::kWork: how many times that another one takes).
+// `per_cu` workgroups share a compute unit at that cost.  Fitted to 210 kernel times of 22
+// sizes, 8% root mean square; the choice is at most 3% behind the best kernel on each but one (7%).
 struct NtCost {
   int kernel, side_m, side_n, per_cu;
-  float full, few, tile, reads;
+  float full, few, tile, work;
 };
 constexpr NtCost kNtCosts[] = {
     {kNtDirect16x64, 16, 64, 1, 0.29f, 0.22f, 1.9f, 0.0f}, {kNtDirect64x64, 64, 64, 1, 0.52f, 0.50f, 2.0f, 0.0f},
-    {kNtRing64, 64, 64, 3, 0.58f, 0.18f, 2.0f, 0.8f},      {kNtRing96, 96, 96, 1, 0.34f, 0.29f, 2.0f, 1.5f},
-    {kNtRing128, 128, 128, 2, 0.84f, 0.42f, 2.0f, 2.0f},   {kNtRing128x5, 128, 128, 1, 0.50f, 0.41f, 2.4f, 2.5f},
-    {kNtRing192, 192, 192, 1, 0.83f, 0.62f, 6.0f, 5.0f},   {kNtRing256, 256, 256, 1, 1.33f, 0.98f, 9.0f, 10.0f},
+    {kNtRing64, 64, 64, 3, 0.49f, 0.14f, 1.8f, 1.7f},      {kNtRing96, 96, 96, 1, 0.30f, 0.235f, 2.9f, 2.1f},
+    {kNtRing128, 128, 128, 2, 0.88f, 0.27f, 3.8f, 5.3f},   {kNtRing128x5, 128, 128, 1, 0.45f, 0.295f, 3.8f, 3.6f},
+    {kNtRing192, 192, 192, 1, 0.83f, 0.575f, 5.9f, 6.6f},  {kNtRing256, 256, 256, 1, 1.30f, 0.77f, 9.6f, 12.7f},
 };
 
-// The kernel with the least estimated time: full rounds of workgroups over the compute
-// units, and a last round that is cheaper the emptier it is.  direct, ring: which kinds
-// there are to choose from; f16, reads: the element type, and whether the epilogue reads.
-inline int nt_choose(const NtArgs& g, bool direct, bool ring, bool f16, bool reads) {
-  const double cus = device_cus() > 0 ? device_cus() : 256;
-  const double units = (double)((g.kb + 127) / 128) * (f16 ? 1.15 : 1.0);
-  int best = direct ? kNtDirect64x64 : kNtRing64;
+// Which kernel computes a product: all of it (count of tiles -1), or the first `count`
+// tiles, and the rest on `rest`, its tiles cut split x split times.
+struct NtChoice {
+  int kernel, count, rest, split;
+};
+
+inline double nt_cost(const NtCost& c, double tiles, double units, float work, int cus) {
+  const double slots = (double)cus * c.per_cu;
+  const double rounds = (double)(int64_t)(tiles / slots), last = tiles / slots - rounds;
+  const double tile = c.tile + work * c.work;
+  return rounds * (units * c.full + tile) + (last > 0 ? units * (c.few + (c.full - c.few) * last) + tile : 0.0);
+}
+
+// The choice with the least estimated time: full rounds of workgroups over the compute
+// units, and a last round that is cheaper the emptier it is, or is left to smaller tiles
+// in a launch of its own (4,096 x 14,336 x 8,192 in 3.5 rounds of 256: 355.8 -> 344.3 us;
+// 3,000 x 7,000 x 4,096: 89.6 us on the best single kernel, 83.3 on two).
+// direct, ring: which kinds there are to choose from; f16, work: the element type, and
+// the epilogue's.
+inline NtChoice nt_choose(const NtArgs& g, bool direct, bool ring, bool f16, float work) {
+  constexpr double kLaunch = 4.0;
+  const int found = device_cus(), cus = found > 0 ? found : 256;
+  const double units = (double)((g.kb + 127) / 128) * (f16 ? 1.2 : 1.0);
+  const double clip = g.kb % 128 != 0 ? 1.0 : 0.0;         // the last unit clipped in LDS
+  NtChoice best{direct ? kNtDirect64x64 : kNtRing64, -1, 0, 1};
   double least = 1e300;
   for (const NtCost& c : kNtCosts) {
     const bool is_direct = c.kernel == kNtDirect16x64 || c.kernel == kNtDirect64x64;
     if (is_direct ? !direct : !ring) continue;
-    const int64_t tm = (g.M + c.side_m - 1) / c.side_m, tn = (g.N + c.side_n - 1) / c.side_n;
-    const double tiles = (double)(g.sym ? tm * (tm + 1) / 2 : tm * tn) * g.batch, slots = cus * c.per_cu;
-    const double rounds = (double)(int64_t)(tiles / slots), last = tiles / slots - rounds;
-    const double tile = c.tile + (reads ? c.reads : 0.0f);
-    double us = rounds * (units * c.full + tile);
-    if (last > 0) us += units * (c.few + (c.full - c.few) * last) + tile;
-    if (!is_direct && g.kb % 128 != 0) us += 1.0;          // the last unit clipped in LDS
+    const int64_t tiles = nt_tiles(g, c.side_m, c.side_n);
+    const double us = nt_cost(c, (double)tiles, units, work, cus) + (is_direct ? 0.0 : clip);
     if (us < least) {
       least = us;
-      best = c.kernel;
+      best = NtChoice{c.kernel, -1, 0, 1};
+    }
+    const int64_t slots = (int64_t)cus * c.per_cu, whole = tiles / slots * slots;
+    if (is_direct || whole == 0 || whole == tiles) continue;
+    for (const NtCost& r : kNtCosts) {
+      const bool small = r.kernel == kNtRing64 || r.kernel == kNtRing96 || r.kernel == kNtRing128 || r.kernel == kNtRing128x5;
+      const int k = c.side_m / r.side_m;
+      if (!small || k < 2 || k * r.side_m != c.side_m) continue;
+      const double both = nt_cost(c, (double)whole, units, work, cus) + nt_cost(r, (double)((tiles - whole) * k * k), units, work, cus) +
+                          kLaunch + 2 * clip;
+      if (both < least) {
+        least = both;
+        best = NtChoice{c.kernel, (int)whole, r.kernel, k};
+      }
     }
   }
   return best;
@@ -521,16 +551,49 @@ inline bool ring_fits(const NtArgs& g) {
 }
 
 template <int EL, int NT, int NB, bool CLIP, typename Epi>
-hipError_t run_nt_ring(const NtArgs& g, const Epi& epi, hipStream_t s) {
-  constexpr int MT = 32 * NT, LDS = ring_lds<NT, NB>();
+hipError_t run_nt_ring(const NtArgs& g, const NtGrid& d, const Epi& epi, hipStream_t s) {
+  constexpr int LDS = ring_lds<NT, NB>();
   static_assert(LDS <= 160 * 1024, "LDS plan");
-  const int64_t total = nt_tiles(g, MT, MT);
-  if (total > 0x7FFFFFFF || !ring_fits(g) || (!CLIP && g.kb % 128 != 0)) return hipErrorInvalidValue;
+  if (!ring_fits(g) || (!CLIP && g.kb % 128 != 0) || (int64_t)d.count * d.split * d.split > 0x7FFFFFFF) return hipErrorInvalidValue;
   const void* fn = reinterpret_cast<const void*>(&k_nt_ring<EL, NT, NB, CLIP, Epi>);
   if (set_lds_limit(fn, LDS) != hipSuccess) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_nt_ring<EL, NT, NB, CLIP, Epi>), dim3((unsigned)total), dim3(256), LDS, s, g, (int)total,
-                     (int)((g.M + MT - 1) / MT), (int)((g.N + MT - 1) / MT), epi);
+  hipLaunchKernelGGL((k_nt_ring<EL, NT, NB, CLIP, Epi>), dim3((unsigned)(d.count * d.split * d.split)), dim3(256), LDS, s, g, d,
+                     epi);
   return hipGetLastError();
+}
+
+template <int EL, bool CLIP, typename Epi>
+hipError_t run_nt_ring_on(const NtArgs& g, int kernel, const NtGrid& d, const Epi& epi, hipStream_t s) {
+  switch (kernel) {
+    case kNtRing64: return run_nt_ring<EL, 2, 3, CLIP>(g, d, epi, s);
+    case kNtRing96: return run_nt_ring<EL, 3, 6, CLIP>(g, d, epi, s);
+    case kNtRing128: return run_nt_ring<EL, 4, 2, CLIP>(g, d, epi, s);
+    case kNtRing128x5: return run_nt_ring<EL, 4, 5, CLIP>(g, d, epi, s);
+    case kNtRing192: return run_nt_ring<EL, 6, 3, CLIP>(g, d, epi, s);
+    case kNtRing256: return run_nt_ring<EL, 8, 2, CLIP>(g, d, epi, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+inline int nt_side(int kernel) {
+  for (const NtCost& c : kNtCosts)
+    if (c.kernel == kernel) return c.side_n;
+  return 64;
+}
+
+// The product on the ring kernels of a choice.
+template <int EL, bool CLIP, typename Epi>
+hipError_t run_nt_choice(const NtArgs& g, const NtChoice& c, const Epi& epi, hipStream_t s) {
+  const int side = nt_side(c.kernel);
+  if (nt_tiles(g, side, side) > 0x7FFFFFFF) return hipErrorInvalidValue;
+  NtGrid d = nt_grid(g, side, side);
+  const int all = d.count;
+  if (c.count >= 0) d.count = c.count;
+  const hipError_t e = d.count > 0 ? run_nt_ring_on<EL, CLIP>(g, c.kernel, d, epi, s) : hipSuccess;
+  if (e != hipSuccess || d.count == all) return e;
+  d.first = d.count;
+  d.count = all - d.count;
+  d.split = c.split;
+  return run_nt_ring_on<EL, CLIP>(g, c.rest, d, epi, s);
 }
 
 }  // namespace bsq

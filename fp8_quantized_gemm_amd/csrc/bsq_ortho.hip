@@ -221,7 +221,8 @@ __device__ __forceinline__ ntu2 ns_load(const uint16_t* p, int block, uint32_t l
 enum NsMode { kNsGram = 0, kNsPoly = 1, kNsProduct = 2 };
 template <int MODE>
 struct EpiNsSquare {
-  static constexpr bool kTrans = true, kReads = MODE != kNsGram;
+  static constexpr bool kTrans = true;
+  static constexpr float kWork = MODE == kNsGram ? 0.0f : MODE == kNsPoly ? 1.0f : 1.4f;
   NsSquare c;
   const uint16_t* l;
   const uint16_t* r;
@@ -306,7 +307,7 @@ struct EpiNsSquare {
   __device__ __forceinline__ void store_t(int n, int m, const ntu4& v) {
     if (!p.dead && m < p.M && n < p.N) *reinterpret_cast<ntu4*>(t + (uint32_t)(n * side + m)) = v;
   }
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish(uint8_t*) {}
 };
 
 // What the products P X (X in the matrix's own orientation, rows x cols) add to the MFMAs'
@@ -357,7 +358,8 @@ struct NsApply {
 // The next X: FP16, the rest of its rounding (in place), and its transpose.
 template <bool WIDE>
 struct EpiNsNext {
-  static constexpr bool kTrans = true, kReads = true;
+  static constexpr bool kTrans = true;
+  static constexpr float kWork = 1.7f;
   NsApply<WIDE> x;
   uint16_t* hi;
   uint16_t* lo;
@@ -397,13 +399,14 @@ struct EpiNsNext {
   __device__ __forceinline__ void store_t(int n, int m, const ntu4& v) {
     if (!x.p.dead && m < x.p.M && n < x.p.N) *reinterpret_cast<ntu4*>(t + (uint32_t)(n * x.rows + m)) = v;
   }
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish(uint8_t*) {}
 };
 
 // BF16(X) of the matrix without its padding.
 template <bool WIDE>
 struct EpiNsOut {
-  static constexpr bool kTrans = false, kReads = true;
+  static constexpr bool kTrans = false;
+  static constexpr float kWork = 0.8f;
   NsApply<WIDE> x;
   uint16_t* out;
   int rows, cols;
@@ -435,14 +438,15 @@ struct EpiNsOut {
     store_raw<false>(out + (m * cols + n), 0, N - n, r);
   }
   __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
-  __device__ __forceinline__ void finish() {}
+  __device__ __forceinline__ void finish(uint8_t*) {}
 };
 
 // w <- keep w - step X, its BF16 copy and that copy's largest magnitude.  X passes
 // through LDS in FP16 (2^-11 of an entry, below the products' own error).
 template <bool WIDE>
 struct EpiNsUpdate {
-  static constexpr bool kTrans = false, kReads = true;
+  static constexpr bool kTrans = false;
+  static constexpr float kWork = 1.2f;
   NsApply<WIDE> x;
   float* w;
   uint16_t* wb;
@@ -492,27 +496,31 @@ struct EpiNsUpdate {
     store_raw<false>(wb + at, 0, len, b);
   }
   __device__ __forceinline__ void store_t(int, int, const ntu4&) {}
-  __device__ __forceinline__ void finish() {
+  // one atomic a workgroup, and none where the maximum is there already: all go to one
+  // address (8 x 520 x 1,000: 4,608 of them took 40 us)
+  __device__ __forceinline__ void finish(uint8_t* lds) {
     if (!amax) return;
+    uint32_t* all = reinterpret_cast<uint32_t*>(lds);
     const uint32_t m = wave_max_dpp(most);
-    if ((threadIdx.x & 63) == 0) atomicMax(reinterpret_cast<uint32_t*>(amax), m);
+    __syncthreads();                                       // the tile's pieces are read
+    if ((threadIdx.x & 63) == 0) all[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    const uint32_t b = max(max(all[0], all[1]), max(all[2], all[3]));
+    uint32_t* a = reinterpret_cast<uint32_t*>(amax);
+    if (b > __hip_atomic_load(a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) atomicMax(a, b);
   }
 };
 
 template <typename Epi>
-hipError_t product(const uint16_t* a, const uint16_t* b, int64_t M, int64_t N, int64_t K, int64_t batch, bool sym,
-                   const Epi& epi, int kernel, hipStream_t s) {
+hipError_t product(const OrthoArgs& o, const uint16_t* a, const uint16_t* b, int64_t M, int64_t N, int64_t K, bool sym,
+                   const Epi& epi, hipStream_t s) {
   const NtArgs g{reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), M, N, (uint32_t)(2 * K),
-                 2 * M * K, 2 * N * K, (int)batch, sym};
-  switch (kernel == kNtChosen ? nt_choose(g, false, true, true, Epi::kReads) : kernel) {
-    case kNtRing128: return run_nt_ring<kNtF16, 4, 2, false>(g, epi, s);
-    case kNtRing64: return run_nt_ring<kNtF16, 2, 3, false>(g, epi, s);
-    case kNtRing96: return run_nt_ring<kNtF16, 3, 6, false>(g, epi, s);
-    case kNtRing128x5: return run_nt_ring<kNtF16, 4, 5, false>(g, epi, s);
-    case kNtRing192: return run_nt_ring<kNtF16, 6, 3, false>(g, epi, s);
-    case kNtRing256: return run_nt_ring<kNtF16, 8, 2, false>(g, epi, s);
-    default: return hipErrorInvalidValue;
-  }
+                 2 * M * K, 2 * N * K, (int)o.batch, sym};
+  if (o.kernel == kNtChosen) return run_nt_choice<kNtF16, false>(g, nt_choose(g, false, true, true, Epi::kWork), epi, s);
+  const int side = nt_side(o.kernel), half = (int)(nt_tiles(g, side, side) / 2);
+  const bool cut = o.rest != kNtChosen && half > 0;
+  return run_nt_choice<kNtF16, false>(g, NtChoice{o.kernel, cut ? half : -1, o.rest, side / nt_side(o.rest)}, epi, s);
 }
 
 struct NsSizes {
@@ -551,7 +559,7 @@ template <bool WIDE>
 hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool more, hipStream_t s) {
   const uint16_t *l = WIDE ? b.p.e : b.xt, *r = WIDE ? b.xt : b.p.e;
   const NsApply<WIDE> a{WIDE ? b.x : b.xt, b.lo, b.p.d, (int)z.rows64, (int)z.cols64};
-  const auto run = [&](const auto& epi) { return product(l, r, z.rows64, z.cols64, z.m, o.batch, false, epi, o.kernel, s); };
+  const auto run = [&](const auto& epi) { return product(o, l, r, z.rows64, z.cols64, z.m, false, epi, s); };
   if (more) return run(EpiNsNext<WIDE>{a, WIDE ? b.x : b.xn, b.lo, WIDE ? b.xn : b.x});
   if (o.w)
     return run(EpiNsUpdate<WIDE>{a, o.w, static_cast<uint16_t*>(o.w_bf16), o.amax, (int)o.rows, (int)o.cols, o.keep,
@@ -626,18 +634,18 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
   const auto multiply = [&](const NsSquare& l, const NsSquare& r, const NsSquare& c) {
     EpiNsSquare<kNsProduct> epi{c, l.e, r.e, l.d, r.d, (int)z.m};
     epi.alpha = 1.0f / kS, epi.k1 = 1.0f, epi.q2 = 1.0f;
-    return product(l.e, r.e, z.m, z.m, z.m, B, true, epi, o.kernel, s);
+    return product(o, l.e, r.e, z.m, z.m, z.m, true, epi, s);
   };
   const auto polynomial = [&](const NsSquare& l, const NsSquare& c, const float* k) {
     EpiNsSquare<kNsPoly> epi{c, l.e, l.e, l.d, l.d, (int)z.m};
     epi.alpha = k[2] / kS, epi.k0 = 0.5f * k[1], epi.k1 = k[2], epi.q0 = k[0], epi.q1 = k[1], epi.q2 = k[2];
-    return product(l.e, l.e, z.m, z.m, z.m, B, true, epi, o.kernel, s);
+    return product(o, l.e, l.e, z.m, z.m, z.m, true, epi, s);
   };
   for (int i = 0, r = 0; i < o.steps;) {
     r = phase_steps(o, z, i, r);
     EpiNsSquare<kNsGram> gram{ga, nullptr, nullptr, nullptr, nullptr, (int)z.m};
     gram.alpha = 1.0f / kS;
-    e = product(x, x, z.m, z.m, z.n, B, true, gram, o.kernel, s);
+    e = product(o, x, x, z.m, z.m, z.n, true, gram, s);
     if (e == hipSuccess) e = polynomial(ga, pp, o.coefs + 3 * i);
     if (r == 2) {
       if (e == hipSuccess) e = multiply(pp, ga, t);

@@ -153,8 +153,14 @@ def test_zero_sizes():
     assert bsq.int8_linear(torch.ones(2, 16, device="cuda").bfloat16(), w[:0], sw[:0]).shape == (2, 0)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 300, 1000), (2, 64, 24), (8, 1000, 2048), (16, 2048, 1408),
-                                   (37, 2048, 1408), (64, 257, 513), (200, 512, 4096), (700, 1024, 1536)])
+# few rows (one launch): each number of waves per row, of row tiles and of column tiles,
+# K below, at and off whole groups, the most codes; then the two launches
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (1, 12300, 8192), (1, 5, 16), (2, 64, 32), (2, 6200, 2064), (3, 100, 144),
+                                   (4, 20, 8192), (5, 33, 496), (8, 1000, 2048), (8, 70, 8192), (15, 12288, 528),
+                                   (16, 2048, 1408), (16, 77, 4096), (17, 300, 112), (31, 6150, 640), (32, 50, 2048),
+                                   (33, 90, 256), (37, 2048, 1408), (48, 6144, 1264), (64, 129, 1024), (63, 1, 128),
+                                   (65, 129, 1024), (64, 257, 1040), (1, 300, 1000), (2, 64, 24), (64, 257, 513), (9, 30, 8208),
+                                   (200, 512, 4096), (700, 1024, 1536)])
 @pytest.mark.parametrize("bias", [False, True])
 def test_linear(M, N, K, bias):
     announce("int8_linear", M, N, K, bias)
