@@ -22,7 +22,9 @@ own, usually kept in higher precision).
             dxp = dY_gu . W_gu[e];  dW_gu[e] = dY_gu^T . xp
             dh = combine of dxp without weights
   close     block_norm backward: dx, do and the norm's and gate's gradients
-  update    W <- W - lr * dW on the FP32 masters (stacked over the experts)
+  update    W <- W - lr * dW on the FP32 masters (stacked over the experts), or with
+              optimizer "muon" the orthogonalised update of an FP32 momentum, each
+              expert's gate, up and down projection a matrix of its own
 
 y is the next block_norm's o.  Groups are padded to 32 rows of zeros and the
 buffers to a multiple of 512 rows, so the column-quantized operands' 16-row blocks
@@ -33,8 +35,9 @@ import torch
 
 from . import (_check, _ptr, _stream, block_norm, block_norm_backward, bs_gemm_grouped,
                bs_gemm_grouped_wgrad, lib, master_weight_update, moe_combine, moe_combine_backward,
-               moe_gather, moe_route, moe_route_backward, quantize_transpose, quantize_transpose_amax,
-               swiglu, swiglu_backward)
+               moe_gather, moe_route, moe_route_backward, muon_update, quantize_transpose,
+               quantize_transpose_amax, swiglu, swiglu_backward)
+from .mlp import muon_options
 
 ALIGN = 32
 
@@ -43,10 +46,11 @@ class MoELayer:
     """w_gu: FP32 masters [E, 2F, hidden] (gate rows first); w_down: [E, hidden, F]; both
     copied.  norm: dict of block_norm's w_pre, w_post, gate, alpha, eps (w_pre
     required).  scoring, normalize, scale, bias, score_bias: moe_route's.  hidden %
-    16 == 0, F % 16 == 0."""
+    16 == 0, F % 16 == 0.  optimizer: "sgd", or "muon" with muon a dict of muon_update's
+    options (its defaults otherwise) and lr its lr."""
 
     def __init__(self, w_gu, w_down, k, norm, scoring="softmax", normalize=True, scale=1.0, bias=None,
-                 rht=True, rht_signs=0, sr_seed=0, lr=1e-4, score_bias=None):
+                 rht=True, rht_signs=0, sr_seed=0, lr=1e-4, score_bias=None, optimizer="sgd", muon=None):
         if not (w_gu.is_cuda and w_down.is_cuda and w_gu.device == w_down.device):
             raise ValueError("the master weights must be CUDA tensors on one device")
         E, F2, Hd = w_gu.shape
@@ -55,6 +59,9 @@ class MoELayer:
             raise ValueError("w_gu must be [E, 2F, hidden] and w_down [E, hidden, F], F and hidden multiples of 16")
         if norm.get("w_pre") is None:
             raise ValueError("norm needs w_pre: the block's input is normalised")
+        if optimizer not in ("sgd", "muon") or (muon is not None and optimizer != "muon"):
+            raise ValueError("optimizer must be 'sgd', or 'muon' (which alone takes muon)")
+        self.optimizer, self.muon = optimizer, muon_options(muon)
         self.dev, self.E, self.F, self.Hd, self.k = w_gu.device, E, F, Hd, int(k)
         self.norm, self.bias, self.score_bias = dict(norm), bias, score_bias
         self.routing = dict(scoring=scoring, normalize=normalize, scale=scale)
@@ -70,6 +77,15 @@ class MoELayer:
             # the BF16 working copies and their amaxes: an update with a zero gradient
             self.grad[n] = torch.zeros(w.shape, dtype=torch.bfloat16, device=self.dev)
             self._update(n, 0.0)
+        if optimizer == "muon":
+            self.momentum = {n: torch.zeros_like(w) for n, w in self.w32.items()}
+
+    def _update_muon(self, n):
+        w = self.w32[n]
+        shape = (2 * self.E, self.F, self.Hd) if n == "W_gu" else w.shape    # gate and up rows apart
+        v = lambda t: t.view(shape)
+        u = muon_update(v(w), v(self.momentum[n]), v(self.grad[n]), self.lr, w_bf16=v(self.wbf[n]), **self.muon)
+        self.wamax[n] = u["amax"]
 
     def _update(self, n, lr):
         u = master_weight_update(self.w32[n], self.grad[n], lr, w_bf16=self.wbf[n])
@@ -145,5 +161,8 @@ class MoELayer:
 
     def update(self):
         for n in self.w32:
-            self._update(n, self.lr)
+            if self.optimizer == "muon":
+                self._update_muon(n)
+            else:
+                self._update(n, self.lr)
         self.it += 1
