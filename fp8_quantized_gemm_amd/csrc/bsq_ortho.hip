@@ -573,13 +573,14 @@ hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool 
 // steps take 1.5 m^2 n + 2.5 m^3 multiply-adds (symmetric products counted half), one by
 // one 3 m^2 n + m^3.  But Q A Q multiplies A's rounding at singular values near zero by
 // a^2 until A is formed afresh, so a pair is followed by a single step, and is taken
-// where the matrix is far enough from square to have no singular values near zero and
-// the a's are small (at most 12; the usual ones 11.9).  Simulated on gradients, distance
-// from the 64-bit result one by one / in pairs with singles between / 2 and 3: 512 x
-// 1,792 4.1e-4, 2.9e-4, 6.4e-4; 500 x 800 5.4e-4, 5.7e-4, 1.6e-3; 1,024 x 1,024 5.8e-4,
-// 1.4e-3, 4.1e-3; all five at once infinity.
+// where the matrix is far enough from square to have few singular values near zero and
+// the a's are small (at most 12; the usual ones 11.9).  Simulated distance from the 64-bit
+// result one by one / in pairs with singles between: gradients of 512 x 1,792 4.1e-4,
+// 2.9e-4 (2 and 3 steps at once: 6.4e-4), 600 x 800 5.2e-4, 7.2e-4, 1,024 x 1,024 5.8e-4,
+// 1.4e-3 (4.1e-3); singular values spread over e^5 at 600 x 800 6.9e-4, 2.2e-3; all five at
+// once infinity.  16 x 1,408 x 2,048: 1,981 us one by one, 1,788 in pairs.
 int phase_steps(const OrthoArgs& o, const NsSizes& z, int i, int before) {
-  return 2 * z.n >= 3 * z.m && before != 2 && i + 2 <= o.steps &&
+  return 3 * z.n >= 4 * z.m && before != 2 && i + 2 <= o.steps &&
                  std::fabs(o.coefs[3 * i] * o.coefs[3 * i + 3]) <= 12.0f
              ? 2
              : 1;

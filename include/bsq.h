@@ -600,8 +600,10 @@ bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, in
  * (on the transpose where rows > cols, which is the same).  The products take FP16
  * matrices under a power of two (each rounding at most 2^-11 of the value) and sum in
  * FP32; X itself is held to 22 bits, the diagonals of A and the polynomials in FP32,
- * the norm in FP64: five steps are within about 1e-3 (relative, Frobenius) of the
- * exact result.  Coefficients must keep singular values below 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of its own.
+ * the norm in FP64: five steps are about 5e-4 (relative, Frobenius) from the exact
+ * result on gradients, 2e-3 where singular values are spread over two decades. 
+ * Coefficients must keep singular values below 8.  A zero matrix gives zeros; a matrix
+ * with NaN or infinities gives NaN of its own.
  *   x     : in, [batch, rows, cols] of type.   out : out, BF16 [batch, rows, cols].
  *   coefs : in, HOST array of 3 * steps floats, 1 <= steps <= 32.   eps > 0.
  *   workspace : device memory, 256-byte aligned.

@@ -32,13 +32,13 @@ def orthogonalize(x, steps=5, coefs=COEFS, eps=1e-7):
 
 def phases(m, n, steps, coefs=COEFS):
     """Numbers of steps that are taken on one Gram matrix, in turn: one by one, or, from
-    n = 1.5 m on, pairs with a single step between them, of steps whose leading
+    n = 4/3 m on, pairs with a single step between them, of steps whose leading
     coefficients' product is at most 12."""
     lead = [abs(float(np.float32(v[0]))) for v in _steps(steps, coefs)]
     out = []
     while sum(out) < steps:
         i = sum(out)
-        pair = 2 * n >= 3 * m and out[-1:] != [2] and i + 2 <= steps and lead[i] * lead[i + 1] <= 12
+        pair = 3 * n >= 4 * m and out[-1:] != [2] and i + 2 <= steps and lead[i] * lead[i + 1] <= 12
         out.append(2 if pair else 1)
     return out
 
