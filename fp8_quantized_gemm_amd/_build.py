@@ -24,7 +24,7 @@ CEILING_LIB = os.path.join(PKG, "libbsq_ceiling.so")
 
 SOURCES = ["bsq_api.cpp", "bsq_quantize.hip", "bsq_gemm.hip", "bsq_gemm_nvfp4.hip",
            "bsq_gemm_nvfp4_rx.hip", "bsq_gemm_mx_rx.hip", "bsq_norm.hip", "bsq_moe.hip",
-           "bsq_gemm_grouped.hip", "bsq_int8.hip", "bsq_ortho.hip"]
+           "bsq_gemm_grouped.hip", "bsq_int8.hip", "bsq_ortho.hip", "bsq_ortho_one.hip"]
 CEILING_SOURCES = ["route_a_ceiling.hip", "grouped_kernels.cpp", "plain_kernels.cpp"]
 
 ARCH = "gfx950"

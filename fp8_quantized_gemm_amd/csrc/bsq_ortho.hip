@@ -19,6 +19,7 @@
 // products need no edges.
 #include "bsq_nt.hpp"
 #include "bsq_nt_ring.hpp"
+#include "bsq_ortho.hpp"
 #include "bsq_wave.hpp"
 
 #include <algorithm>
@@ -26,30 +27,12 @@
 
 namespace bsq {
 
+__global__ void k_ns_zero(float* p) { *p = 0.0f; }
+
 namespace {
 
-// Power of two of the FP16 forms: entries of X are at most 1.3 with the usual coefficients
-// and typically 1 / sqrt(m n) at first; off-diagonal entries of the polynomials at most half
-// the product of their leading coefficients.
-constexpr float kS = 1024.0f;
 constexpr float kLo = 2048.0f;           // of the rest of X's rounding, at most 2^-11 of X
 constexpr int kParts = 256;              // most workgroups that sum one matrix's squares
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, halfx2{(_Float16)lo, (_Float16)hi});
-}
-__device__ __forceinline__ float f16_lo(uint32_t w) { return (float)__builtin_bit_cast(halfx2, w).x; }
-__device__ __forceinline__ float f16_hi(uint32_t w) { return (float)__builtin_bit_cast(halfx2, w).y; }
-
-// What is orthogonalised: a tensor (BF16, FP32) or the moment of an update.
-enum NsInput { kNsBf16 = 0, kNsF32 = 1, kNsMoment = 2 };
-struct NsSource {
-  const void* x;
-  float* momentum;
-  const uint16_t* grad;
-  float mu;
-  int nesterov;
-};
 
 __device__ __forceinline__ double block_sum(double v, double* lds) {
 #pragma unroll
@@ -173,8 +156,6 @@ __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, in
     __syncthreads();
   }
 }
-
-__global__ void k_ns_zero(float* p) { *p = 0.0f; }
 
 // ---------------------------------------------------------------- epilogues
 
@@ -578,9 +559,11 @@ hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool 
 // result one by one / in pairs with singles between: gradients of 512 x 1,792 4.1e-4,
 // 2.9e-4 (2 and 3 steps at once: 6.4e-4), 600 x 800 5.2e-4, 7.2e-4, 1,024 x 1,024 5.8e-4,
 // 1.4e-3 (4.1e-3); singular values spread over e^5 at 600 x 800 6.9e-4, 2.2e-3; all five at
-// once infinity.  16 x 1,408 x 2,048: 1,981 us one by one, 1,788 in pairs.
+// once infinity.  16 x 1,408 x 2,048: 1,981 us one by one, 1,788 in pairs;
+// but a pair is 7 launches, two steps 6, which is what a small matrix costs (192 x 256: 79 us
+// one by one, 93 in pairs).
 int phase_steps(const OrthoArgs& o, const NsSizes& z, int i, int before) {
-  return 3 * z.n >= 4 * z.m && before != 2 && i + 2 <= o.steps &&
+  return z.m > 256 && 3 * z.n >= 4 * z.m && before != 2 && i + 2 <= o.steps &&
                  std::fabs(o.coefs[3 * i] * o.coefs[3 * i + 3]) <= 12.0f
              ? 2
              : 1;
@@ -594,6 +577,7 @@ int64_t ortho_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
+  if (o.kernel == kNtChosen && ortho_in_one(o.rows, o.cols)) return launch_ortho_one(o, s);
   NsSizes z;
   if (!ns_sizes(o.batch, o.rows, o.cols, &z)) return hipErrorInvalidValue;
   double* part = static_cast<double*>(o.workspace);

@@ -32,15 +32,27 @@ def orthogonalize(x, steps=5, coefs=COEFS, eps=1e-7):
 
 def phases(m, n, steps, coefs=COEFS):
     """Numbers of steps that are taken on one Gram matrix, in turn: one by one, or, from
-    n = 4/3 m on, pairs with a single step between them, of steps whose leading
+    n = 4/3 m on and m above 256, pairs with a single step between them, of steps whose leading
     coefficients' product is at most 12."""
     lead = [abs(float(np.float32(v[0]))) for v in _steps(steps, coefs)]
     out = []
     while sum(out) < steps:
         i = sum(out)
-        pair = 3 * n >= 4 * m and out[-1:] != [2] and i + 2 <= steps and lead[i] * lead[i + 1] <= 12
+        pair = m > 256 and 3 * n >= 4 * m and out[-1:] != [2] and i + 2 <= steps and lead[i] * lead[i + 1] <= 12
         out.append(2 if pair else 1)
     return out
+
+
+def plan(rows, cols, steps=5, coefs=COEFS):
+    """The phases that orthogonalize takes: single steps where one workgroup holds the
+    matrix, else those of the sizes padded to 64."""
+    m, n = sorted((rows, cols))
+    up = lambda v, k: (v + k - 1) // k * k
+    a, b = up(m, 32), up(n, 32)
+    lds = a * (a + 8) * 2 + a * 4 + 2 * max(a * (b + 8), b * (a + 8))
+    if m <= 160 and n <= (1024 if m <= 32 else 768 if m <= 64 else 512 if m <= 96 else 256) and lds + 64 <= 160 * 1024:
+        return [1] * steps
+    return phases(up(m, 64), up(n, 64), steps, coefs)
 
 
 def orthogonalize_f16(x, steps=5, coefs=COEFS, eps=1e-7, plan=None):

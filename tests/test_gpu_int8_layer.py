@@ -62,10 +62,9 @@ def _check_muon(before, after, grad, lr, o, what):
     R, C = w.shape[-2:]
     step = float(f(f(lr) * f(0.2 * max(R, C) ** 0.5)))
     keep = float(f(1) - f(lr) * f(o["weight_decay"]))
-    pad = sorted((v + 63) // 64 * 64 for v in (R, C))
     for wi, ui, yi in zip(w.astype(np.float64), u.astype(np.float64), wn.astype(np.float64)):
         e, n = OM.orthogonalize(ui), np.linalg.norm
-        q = OM.orthogonalize_f16(ui, plan=OM.phases(*pad, 5))
+        q = OM.orthogonalize_f16(ui, plan=OM.plan(R, C))
         tol = step * (2 * n(q - e) + 2.0 ** -11 * n(e)) + 2.0 ** -23 * (n(wi) + step * n(e))
         assert n(yi - (keep * wi - step * e)) <= tol, (what, n(yi - (keep * wi - step * e)), tol)
 

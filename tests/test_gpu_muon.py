@@ -29,13 +29,8 @@ def _grad(shape, seed, dtype=torch.float32, size=1e-3):
     return ((x + torch.randn(shape, generator=g)) * size).to(dtype)
 
 
-def _plan(shape, steps, coefs):
-    r, c = ((v + 63) // 64 * 64 for v in shape[-2:])
-    return OM.phases(min(r, c), max(r, c), steps, coefs)
-
-
-def _allowed(x, e, steps, coefs, eps, half_step):
-    f = OM.orthogonalize_f16(x, steps, coefs, eps, plan=_plan(x.shape, steps, coefs))
+def _allowed(x, e, steps, coefs, eps, half_step, plan=None):
+    f = OM.orthogonalize_f16(x, steps, coefs, eps, plan=plan or OM.plan(*x.shape, steps, coefs))
     n = np.linalg.norm(e)
     return 2 * np.linalg.norm(f - e) + half_step * n + 1e-30
 
@@ -56,7 +51,11 @@ def _check(x, steps=5, coefs=OM.COEFS, eps=1e-7):
 
 @pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (2, 3), (16, 16), (63, 64), (64, 65), (65, 64), (64, 128), (128, 64),
                                    (100, 37), (37, 100), (200, 136), (129, 385), (256, 256), (257, 300), (520, 1000), (700, 200),
-                                   (3, 1000), (1000, 5), (512, 640)])
+                                   (3, 1000), (1000, 5), (512, 640),
+                                   # at and past the edges of what one workgroup holds
+                                   (160, 160), (161, 161), (192, 200), (160, 256), (256, 161), (257, 150), (96, 512), (97, 512), (513, 90),
+                                   (32, 1024), (1024, 33), (17, 1024), (1025, 16), (81, 449), (64, 768), (769, 64),
+                                   (128, 250), (250, 129)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_orthogonalize(shape, dtype):
     _check(_grad(shape, 1, dtype))
@@ -70,7 +69,7 @@ def test_stacks(shape):
         assert torch.equal(got[i], bsq.orthogonalize(x[i].cuda()))
 
 
-@pytest.mark.parametrize("shape", [(96, 96), (64, 256), (256, 64)])
+@pytest.mark.parametrize("shape", [(96, 96), (64, 256), (256, 64), (300, 500), (448, 310)])
 @pytest.mark.parametrize("steps,coefs", [
     (1, OM.COEFS), (2, OM.COEFS), (3, OM.COEFS), (8, OM.COEFS), (12, (1.5, -0.5, 0.0)), (6, (2.0, -1.5, 0.5)),
     (4, ((8.2, -23.0, 16.7), (4.1, -2.9, 0.53), (3.9, -2.8, 0.53), (1.9, -1.3, 0.4)))])

@@ -109,9 +109,10 @@ def test_f16_form_and_phases():
         f = OM.orthogonalize_f16(x, plan=plan)
         assert 0 < np.linalg.norm(f - e) < 2.0 ** -11 * 5 * np.linalg.norm(e)
     assert np.allclose(OM.orthogonalize_f16(2.0 * np.eye(4), steps=1, coefs=(1.0, 0.0, 0.0), eps=1e-30), 0.5 * np.eye(4))
-    assert OM.phases(64, 64, 5) == [1] * 5 and OM.phases(64, 128, 5) == [2, 1, 2]
-    assert OM.phases(64, 128, 3, [(8.3, 0, 0), (4.1, 0, 0), (2.9, 0, 0)]) == [1, 2]
-    assert OM.phases(64, 128, 7, (1.5, -0.5, 0)) == [2, 1, 2, 1, 1]
+    assert OM.phases(320, 320, 5) == OM.phases(256, 512, 5) == [1] * 5 and OM.phases(320, 640, 5) == [2, 1, 2]
+    assert OM.phases(320, 640, 3, [(8.3, 0, 0), (4.1, 0, 0), (2.9, 0, 0)]) == [1, 2]
+    assert OM.phases(320, 640, 7, (1.5, -0.5, 0)) == [2, 1, 2, 1, 1]
+    assert OM.plan(64, 128) == OM.plan(512, 96) == OM.plan(512, 97) == [1] * 5 and OM.plan(520, 1000) == [2, 1, 2]
 
 
 def test_moment():
