@@ -770,13 +770,22 @@ def bs_gemm_grouped_wgrad(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_
 
 # ---------------------------------------------------------------- 8-bit integers
 
+def _call(fn, dev, *args):
+    """The entry point on dev's current stream, with dev current: the library asks for
+    the current device's compute units and sets its kernels' LDS there."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+    with torch.cuda.device(dev):
+        return _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+
+
 def int8_quantize(x):
     """Codes of the rows of x [R, C] (bfloat16) -> (codes int8 [R, C], scales float32 [R])."""
     x = _check_input(x)
     R, C = x.shape
     codes = torch.empty(R, C, dtype=torch.int8, device=x.device)
     scales = torch.empty(R, dtype=torch.float32, device=x.device)
-    _check("int8_quantize", lib().int8_quantize(_ptr(x), R, C, _ptr(codes), _ptr(scales), _stream(x.device)))
+    _call("int8_quantize", x.device, _ptr(x), R, C, _ptr(codes), _ptr(scales))
     return codes, scales
 
 
@@ -794,9 +803,8 @@ def int8_quantize_transpose(x, row=True, col=True):
     out = dict(row_codes=i8(row, R, C), row_scales=f32(row, R), col_codes=i8(col, C, R), col_scales=f32(col, C))
     need = _size("int8_quantize_transpose_workspace", R, C)
     ws = _u8(need, dev)
-    _check("int8_quantize_transpose",
-           lib().int8_quantize_transpose(_ptr(x), R, C, _ptr(out["row_codes"]), _ptr(out["row_scales"]),
-                                         _ptr(out["col_codes"]), _ptr(out["col_scales"]), _ptr(ws), need, _stream(dev)))
+    _call("int8_quantize_transpose", dev, _ptr(x), R, C, _ptr(out["row_codes"]), _ptr(out["row_scales"]),
+          _ptr(out["col_codes"]), _ptr(out["col_scales"]), _ptr(ws), need)
     return out
 
 
@@ -830,8 +838,8 @@ def int8_gemm(a_codes, a_scales, b_codes, b_scales, bias=None, out=None):
     dev = a_codes.device
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
-    _check("int8_gemm", lib().int8_gemm(M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales),
-                                        _ptr(bias), _ptr(out), max(out.stride(0), N), _stream(dev)))
+    _call("int8_gemm", dev, M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), _ptr(bias), _ptr(out),
+          max(out.stride(0), N))
     return out
 
 
@@ -850,8 +858,8 @@ def int8_linear(x, w_codes, w_scales, bias=None, out=None):
         out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     need = _size("int8_linear_workspace", M, K)
     ws = _u8(need, dev)
-    _check("int8_linear", lib().int8_linear(_ptr(x), M, N, K, _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(out),
-                                            max(out.stride(0), N), _ptr(ws), need, _stream(dev)))
+    _call("int8_linear", dev, _ptr(x), M, N, K, _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(out),
+          max(out.stride(0), N), _ptr(ws), need)
     return out
 
 
@@ -905,8 +913,8 @@ def orthogonalize(x, steps=5, coefs=NEWTON_SCHULZ, eps=1e-7, out=None):
     _check_device(x, out)
     need = _size("orthogonalize_workspace", B, R, C)
     ws = _u8(need, dev)
-    _check("orthogonalize", lib().orthogonalize(_ptr(x), int(x.dtype == torch.float32), B, R, C, int(steps), host,
-                                                float(eps), _ptr(out), _ptr(ws), need, _stream(dev)))
+    _call("orthogonalize", dev, _ptr(x), int(x.dtype == torch.float32), B, R, C, int(steps), host, float(eps),
+          _ptr(out), _ptr(ws), need)
     return out
 
 
@@ -934,7 +942,6 @@ def muon_update(w32, momentum, grad, lr, mu=0.95, nesterov=True, weight_decay=0.
         scale = 0.2 * max(R, C) ** 0.5
     need = _size("orthogonalize_workspace", B, R, C)
     ws = _u8(need, dev)
-    _check("muon_update", lib().muon_update(_ptr(w32), _ptr(momentum), _ptr(g), B, R, C, float(lr), float(mu),
-                                            1 if nesterov else 0, float(weight_decay), float(scale), int(steps), host,
-                                            float(eps), _ptr(wb), _ptr(a), _ptr(ws), need, _stream(dev)))
+    _call("muon_update", dev, _ptr(w32), _ptr(momentum), _ptr(g), B, R, C, float(lr), float(mu), 1 if nesterov else 0,
+          float(weight_decay), float(scale), int(steps), host, float(eps), _ptr(wb), _ptr(a), _ptr(ws), need)
     return dict(w_bf16=wb, amax=a)
