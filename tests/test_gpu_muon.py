@@ -226,3 +226,55 @@ def test_streams_and_graph():
         e = bsq.muon_update(we, me, g, 1e-2)
         assert torch.equal(w, we) and torch.equal(m, me)
         assert torch.equal(u["w_bf16"], e["w_bf16"]) and torch.equal(u["amax"], e["amax"])
+
+
+@pytest.mark.parametrize("shape", [(120, 200), (3, 64, 90), (330, 500)])
+def test_two_at_once_and_captured(shape):
+    """Both forms (one workgroup, many launches): updates of two weights on two streams at
+    the same time, and replays of a captured one, against the same calls one by one."""
+    announce("muon_update, two at once", shape)
+    cases = [[t.cuda() for t in _update_case(shape, 80 + i)] for i in range(2)]
+    want = [[t.clone() for t in c] for c in cases]
+    for w, m, g in want:
+        for _ in range(3):
+            bsq.muon_update(w, m, g, 1e-2)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(3):
+        for s, (w, m, g) in zip(streams, cases):
+            with torch.cuda.stream(s):
+                outs.append(bsq.muon_update(w, m, g, 1e-2))
+    torch.cuda.synchronize()
+    for (w, m, _), (we, me, _) in zip(cases, want):
+        assert torch.equal(w, we) and torch.equal(m, me)
+    for u, (w, _, _) in zip(outs[-2:], cases):
+        assert torch.equal(u["w_bf16"], w.bfloat16()) and float(u["amax"]) == float(u["w_bf16"].float().abs().max())
+    (w, m, g), (we, me, _) = cases[0], want[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        u = bsq.muon_update(w, m, g, 1e-2)
+    for i in range(4):
+        g.copy_(_grad(shape, 90 + i, torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        e = bsq.muon_update(we, me, g, 1e-2)
+        assert torch.equal(w, we) and torch.equal(m, me)
+        assert torch.equal(u["w_bf16"], e["w_bf16"]) and torch.equal(u["amax"], e["amax"])
+
+
+def test_one_workgroup_form_in_place_and_unaligned():
+    """Updates at addresses that only their type aligns, and a result over its input."""
+    w, m, g = _update_case((75, 130), 95)
+    want = _check_update(w, m, g)
+    odd = lambda t: torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
+    wo, mo, wb = odd(w), odd(m), odd(g)
+    u = bsq.muon_update(wo, mo, odd(g), 1e-2, weight_decay=0.1, w_bf16=wb)
+    assert torch.equal(wo, want[0]) and torch.equal(mo, want[1]) and torch.equal(u["w_bf16"], wo.bfloat16())
+    x = _grad((75, 130), 96, torch.bfloat16).cuda()
+    y = bsq.orthogonalize(x)
+    try:
+        bsq.orthogonalize(x, out=x)
+    except bsq.BsqError:
+        return                                               # refused: the input stays
+    assert torch.equal(x, y)
