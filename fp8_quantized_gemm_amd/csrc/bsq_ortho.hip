@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, in
   __shared__ uint16_t tile[64 * LD];
   const int t = threadIdx.x;
   const double sum = block_sum(t < parts ? part[(int64_t)blockIdx.y * parts + t] : 0.0, lds);
-  const float inv = (float)((double)kS / (sqrt(sum) + (double)eps));
+  const NsNorm norm = ns_norm(sum, eps);
   const int64_t base = (int64_t)blockIdx.y * rows * cols, pad = (int64_t)blockIdx.y * rows64 * cols64;
   const int64_t tiles_c = cols64 / 64, tiles = rows64 / 64 * tiles_c;
   for (int k = 0; k < turns; ++k) {
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, in
       ntu4 v, l;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float x0 = u[2 * j] * inv, x1 = u[2 * j + 1] * inv;
+        const float x0 = ns_scaled(u[2 * j], norm), x1 = ns_scaled(u[2 * j + 1], norm);
         v[j] = pack_f16x2(x0, x1);
         l[j] = pack_f16x2((x0 - f16_lo(v[j])) * kLo, (x1 - f16_hi(v[j])) * kLo);
       }

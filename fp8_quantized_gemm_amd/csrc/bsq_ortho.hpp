@@ -27,6 +27,20 @@ struct NsSource {
   int nesterov;
 };
 
+// What X0 is multiplied by, kS / (||u|| + eps), as frac 2^exp: for a norm and eps below
+// kS / FLT_MAX the number itself is no FP32 (a zero matrix under it would become 0 times
+// infinity), while each product stays below kS.  sum: of the squares.
+struct NsNorm {
+  float frac;
+  int exp;
+};
+__device__ __forceinline__ NsNorm ns_norm(double sum, float eps) {
+  NsNorm n;
+  n.frac = (float)frexp((double)kS / (sqrt(sum) + (double)eps), &n.exp);
+  return n;
+}
+__device__ __forceinline__ float ns_scaled(float x, const NsNorm& n) { return __builtin_ldexpf(x, n.exp) * n.frac; }
+
 __global__ void k_ns_zero(float* p);
 
 // Matrices that one workgroup holds (see bsq_ortho_one.hip).

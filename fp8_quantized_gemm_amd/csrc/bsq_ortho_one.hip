@@ -220,7 +220,7 @@ __global__ __launch_bounds__(kOneWaves * 64) void k_ns_one(NsOne o) {
   sum = 0.0;
 #pragma unroll
   for (int i = 0; i < kOneWaves; ++i) sum += parts[i];
-  const float inv = (float)((double)kS / (sqrt(sum) + (double)o.eps));
+  const NsNorm norm = ns_norm(sum, o.eps);
 #pragma unroll
   for (int j = 0; j < CB; ++j)
 #pragma unroll
@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kOneWaves * 64) void k_ns_one(NsOne o) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[j][i][h][k] *= inv;
+        for (int k = 0; k < 4; ++k) x[j][i][h][k] = ns_scaled(x[j][i][h][k], norm);
 
   // this wave's blocks on and below the diagonal
   int bi[PB], bj[PB];
