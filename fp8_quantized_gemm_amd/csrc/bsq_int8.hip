@@ -12,9 +12,11 @@ namespace {
 
 // ---------------------------------------------------------------- encode
 
+// (A comparison, not fminf: a NaN stays one, and the scale is the only place that can carry
+// it to the product.  Under an infinity s_enc is 0, the codes too, and the scale infinite.)
 __device__ __forceinline__ float i8_enc(uint32_t amax_bits) {
-  const float amax = u2f(amax_bits);
-  return amax == 0.0f ? 1.0f : fminf(127.0f * (1.0f / amax), kFltMax);
+  const float amax = u2f(amax_bits), s = 127.0f * (1.0f / amax);
+  return amax == 0.0f ? 1.0f : s > kFltMax ? kFltMax : s;
 }
 // x s rounded to the nearest even integer, in the low byte: adding 1.5 2^23 leaves
 // no bits below the unit.  |x s| <= 127.5 by the choice of s, so nothing saturates.
