@@ -881,8 +881,21 @@ def _coefs(steps, coefs):
 
 
 def _coef_key(coefs):
-    c = tuple(coefs)
-    return tuple(tuple(v) for v in c) if c and isinstance(c[0], (tuple, list)) else c
+    """coefs as a triple, or triples, of floats: what _coefs remembers goes by values (a
+    tensor's elements, or an array's rows, would be remembered by what they are, and a
+    tensor changed in place taken for what it was).  None where they are no numbers."""
+    def floats(row):
+        row = tuple(row)
+        if any(getattr(v, "ndim", 0) for v in row):
+            raise ValueError("rows of rows")
+        return tuple(float(v) for v in row)
+
+    try:
+        c = tuple(coefs)
+        nested = c and (isinstance(c[0], (tuple, list)) or getattr(c[0], "ndim", 0))
+        return tuple(floats(row) for row in c) if nested else floats(c)
+    except (TypeError, ValueError):
+        return None
 
 
 def _check_stack(x, what, dtypes, shape=None):
