@@ -768,6 +768,18 @@ def bs_gemm_grouped_wgrad(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_
     return out
 
 
+def _on_device(method):
+    """A layer's method with the layer's device (self.dev) current: its calls ask for the
+    current device's compute units and set their kernels' LDS there."""
+    @functools.wraps(method)
+    def run(self, *args, **kwargs):
+        if self.dev.index is None or self.dev.index == torch.cuda.current_device():
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(self.dev):
+            return method(self, *args, **kwargs)
+    return run
+
+
 # ---------------------------------------------------------------- 8-bit integers
 
 def _call(fn, dev, *args):

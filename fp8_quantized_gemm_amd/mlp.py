@@ -38,7 +38,7 @@ import ctypes
 
 import torch
 
-from . import NEWTON_SCHULZ, _coef_key, _coefs, _size, bx_pays, lib as _lib, status_string
+from . import NEWTON_SCHULZ, _coef_key, _coefs, _on_device, _size, bx_pays, lib as _lib, status_string
 
 NV, RNE, SR = 0, 0, 1
 
@@ -171,6 +171,7 @@ class MLPLayer:
             NV, M, N, K, _p(qa[ao + "c"]), _p(qa[ao + "s"]), _p(qa[ao + "a"]), _p(qb[bo + "c"]),
             _p(qb[bo + "s"]), _p(qb[bo + "a"]), _p(c), N, self._stream()))
 
+    @_on_device
     def _update(self, name, lr):
         w = self.w32[name]
         self._ok("master_weight_update " + name, self.lib.master_weight_update(
@@ -199,6 +200,7 @@ class MLPLayer:
             self._stream()))
 
     # -- the step --------------------------------------------------------------------
+    @_on_device
     def forward(self, x):
         T, Hd, F = self.T, self.Hd, self.F
         if not (x.shape == (T, Hd) and x.dtype == torch.bfloat16 and x.is_contiguous()
@@ -222,6 +224,7 @@ class MLPLayer:
         self._gemm("FPROP_down", "H", "r", "W_down", "r", self.act["Y_down"], T, Hd, F)
         return self.act["Y_down"]
 
+    @_on_device
     def backward(self, dy_down):
         T, Hd, F = self.T, self.Hd, self.F
         if not (dy_down.shape == (T, Hd) and dy_down.dtype == torch.bfloat16 and dy_down.is_contiguous()
@@ -266,6 +269,7 @@ class MLPLayer:
         self._gemm8("WGRAD_gu", "dY_gu", "c", "X", "c", self.grad["W_gu"], 2 * F, Hd, T)
         return act["dX"]
 
+    @_on_device
     def update(self):
         for k in ("W_gu", "W_down"):
             if self.optimizer == "muon":

@@ -33,7 +33,7 @@ and RHT chunks never cross a group.
 
 import torch
 
-from . import (_check, _ptr, _stream, block_norm, block_norm_backward, bs_gemm_grouped,
+from . import (_check, _on_device, _ptr, _stream, block_norm, block_norm_backward, bs_gemm_grouped,
                bs_gemm_grouped_wgrad, lib, master_weight_update, moe_combine, moe_combine_backward,
                moe_gather, moe_route, moe_route_backward, muon_update, quantize_transpose,
                quantize_transpose_amax, swiglu, swiglu_backward)
@@ -87,6 +87,7 @@ class MoELayer:
         u = muon_update(v(w), v(self.momentum[n]), v(self.grad[n]), self.lr, w_bf16=v(self.wbf[n]), **self.muon)
         self.wamax[n] = u["amax"]
 
+    @_on_device
     def _update(self, n, lr):
         u = master_weight_update(self.w32[n], self.grad[n], lr, w_bf16=self.wbf[n])
         self.wamax[n] = u["amax"]
@@ -116,6 +117,7 @@ class MoELayer:
         bs_gemm_grouped_wgrad("nvfp4", qa["col_codes"], qa["col_scales"], qb["col_codes"], qb["col_scales"],
                               self.route["offsets"], qa["col_amax"], qb["col_amax"], out=self.grad[n])
 
+    @_on_device
     def open(self, x, o=None):
         """(r, h): the residual after the block before (its output o), and this
         block's normalised input."""
@@ -125,6 +127,7 @@ class MoELayer:
         self.saved = dict(f, r=f["r"] if o is not None else x, o=o, kw=kw)
         return self.saved["r"], f["h"]
 
+    @_on_device
     def forward(self, h, logits):
         """y [T, hidden] (bfloat16) of h [T, hidden] and the router's logits [T, E]."""
         self.logits = logits
@@ -139,6 +142,7 @@ class MoELayer:
         self.y_down = self._product(self.qh, "W_down", "r")
         return moe_combine(self.y_down, self.route["row_of"], self.route["weights"])
 
+    @_on_device
     def backward(self, d_y):
         """(d_h, d_logits); the experts' weight gradients are left in grad."""
         r, off = self.route, 2 * self.it
@@ -153,12 +157,14 @@ class MoELayer:
         self._wgrad(self.qg, self.qx, "W_gu")
         return moe_combine(d_xp, r["row_of"]), d_logits
 
+    @_on_device
     def close(self, d_r, d_h):
         """block_norm_backward's gradients from those of open's r and h."""
         s = self.saved
         return block_norm_backward(s["r"], o=s["o"], d_r=d_r, d_h=d_h, w_pre=self.norm["w_pre"],
                                    rstd_pre=s["rstd_pre"], rstd_post=s["rstd_post"], **s["kw"])
 
+    @_on_device
     def update(self):
         for n in self.w32:
             if self.optimizer == "muon":
