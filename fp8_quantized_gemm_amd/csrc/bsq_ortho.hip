@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256) void k_ns_scale(NsSource src, int64_t rows, in
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float x0 = ns_scaled(u[2 * j], norm), x1 = ns_scaled(u[2 * j + 1], norm);
-        v[j] = pack_f16x2(x0, x1);
+        v[j] = pack_f16x2_stored(x0, x1);
         l[j] = pack_f16x2((x0 - f16_lo(v[j])) * kLo, (x1 - f16_hi(v[j])) * kLo);
       }
       *reinterpret_cast<ntu4*>(a + pad + r * cols64 + col) = v;
@@ -361,7 +361,7 @@ struct EpiNsNext {
   __device__ __forceinline__ ntu2 pack4(int i, int j, const Row& a, const Col& b, const Add& o, ntf4 v) const {
     float y[4];
     x.sums(a, b, o, v, y);
-    const ntu2 h = {pack_f16x2(y[0], y[1]), pack_f16x2(y[2], y[3])};
+    const ntu2 h = {pack_f16x2_stored(y[0], y[1]), pack_f16x2_stored(y[2], y[3])};
     if (x.p.inside(i, j)) {
       float l[4];
 #pragma unroll

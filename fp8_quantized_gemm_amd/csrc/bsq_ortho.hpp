@@ -14,6 +14,15 @@ constexpr float kS = 1024.0f;
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, halfx2{(_Float16)lo, (_Float16)hi});
 }
+// The same, as the bits that are stored: what is computed from them next goes by these.
+// (Otherwise the compiler may round a product or an fma to FP16 in one step where it packs and
+// in two where it goes on with the value, which differ next to a tie: the rest of such an
+// entry was taken from its other neighbour, a whole FP16 step off.)
+__device__ __forceinline__ uint32_t pack_f16x2_stored(float lo, float hi) {
+  uint32_t w = pack_f16x2(lo, hi);
+  asm("" : "+v"(w));
+  return w;
+}
 __device__ __forceinline__ float f16_lo(uint32_t w) { return (float)__builtin_bit_cast(halfx2, w).x; }
 __device__ __forceinline__ float f16_hi(uint32_t w) { return (float)__builtin_bit_cast(halfx2, w).y; }
 

@@ -41,3 +41,21 @@ def test_update_without_a_gradient_under_a_tiny_epsilon(shape):
     keep = np.float32(1) - np.float32(1e-2) * np.float32(0.1)
     assert np.array_equal(wd.cpu().numpy(), keep * w.numpy()) and bool((m == 0).all())
     assert torch.equal(u["w_bf16"], wd.bfloat16()) and float(u["amax"]) == float(u["w_bf16"].float().abs().max())
+
+
+@pytest.mark.parametrize("steps", [1, 4])
+@pytest.mark.parametrize("shape", [*SHAPES, (320, 320), (640, 700)])
+def test_entries_next_to_a_tie(shape, steps):
+    """Steps that multiply X (a = 1.25, b = c = 0), read in FP32 from an update of zero
+    weights: each entry is the scaled one to 22 bits (2^-22 a step, as much for the scaling
+    and the norm), rounded to FP16 once (2^-11 of it, or 2^-25 below FP16's normal range, under
+    the scale of 1,024).  An entry next to a tie of FP16 whose parts do not fit together is off
+    by a whole FP16 step before that, 1.25 after."""
+    announce("muon_update, steps that multiply", shape, steps)
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(3))
+    w, m = torch.zeros(shape, device="cuda"), x.cuda()
+    bsq.muon_update(w, m, torch.zeros(shape, dtype=torch.bfloat16, device="cuda"), 1.0, mu=1.0, nesterov=False, scale=1.0,
+                    steps=steps, coefs=(1.25, 0.0, 0.0))
+    e = 1.25 ** steps * x.double() / (x.double().square().sum().sqrt() + float(np.float32(1e-7)))
+    err = (-w.double().cpu() - e).abs() - (2.0 ** -11 + (steps + 2) * 2.0 ** -22) * e.abs() - 2.0 ** -35
+    assert float(err.max()) <= 0, (shape, int((err > 0).sum()), float((err / e.abs()).max()))
