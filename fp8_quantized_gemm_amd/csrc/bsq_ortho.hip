@@ -5,14 +5,23 @@
 // The products run on the FP16 MFMA (FP32 sums), and what they leave is held so that the
 // result stays near the 64-bit one, where small roundings near singular value zero are
 // multiplied by a in every step:
-//  * X as an FP16 matrix and the FP16 rest of its rounding (22 bits): the product takes the
-//    first, and the diagonal of the polynomial, nearly all of it at small singular values,
-//    multiplies both in the epilogue.
+//  * X as an FP16 matrix X' and the FP16 rest x of its rounding (22 bits).  With D the diagonal
+//    of the polynomial P and O the rest of it, the MFMAs form O X', the epilogue adds D X' and,
+//    in place of P x, a multiple of x: a x (a the step's leading coefficient, the product of
+//    both of a pair), but D x in the last two phases.
+//    What that leaves out is (P - a) x, or (P - D) x.  P is a I where singular values are near
+//    zero, which each later step multiplies by its a again (3.4^4 in all, and 3.4^7 of eight
+//    steps): there the first form leaves out nothing, the second a - D, which is not small
+//    unless the matrix has full rank.  Where they are not, nothing grows, and D is the nearer
+//    one.  (D x in every phase: a matrix of rank 1 of 16 x 16 is 2e-2 from the 64-bit result
+//    after five steps, 6e-1 after eight; so 1e-3 and 2e-3.  a x in every phase: full rank 1.1e-3
+//    for 7e-4.)
 //  * the symmetric matrices (A, the polynomials) as their diagonal in FP32 and the rest in
 //    FP16, so that the largest entries are not rounded.
-// On gradients of 512 x 1,792 five steps are 4e-4 (relative, Frobenius) from the 64-bit
-// result; with everything in FP16 1.0e-3, in BF16 1.3e-2; on a matrix of rank 8 over a floor
-// of 1e-2 2e-4, 2e-2 and 2e-1.
+// Five steps, relative to the 64-bit result (Frobenius), by these roundings: gradients 3e-4 to
+// 1e-3, any rank from 1 to full and singular values over e^5 and e^9 at most 1.5e-3, in pairs of
+// steps 3.8e-3 (at rank m / 3), and 5e-3 for fewer than 16 rows; everything in FP16 2e-2, in BF16
+// 2e-1 on a matrix of rank 8 over a floor of 1e-2.
 //
 // Everything is computed on the smaller side m of the matrix, padded with zeros to
 // multiples of 64 in both directions (zero rows and columns stay zero), so that the
@@ -292,17 +301,19 @@ struct EpiNsSquare {
 };
 
 // What the products P X (X in the matrix's own orientation, rows x cols) add to the MFMAs'
-// sum of P's FP16 part and X's: P's diagonal times X, whole.  In units of X under kS.
-// WIDE: rows <= cols, the diagonal runs along the rows.
+// sum of P's FP16 part and X's: P's diagonal times X's, and its rest times own d + lead, d
+// being the diagonal's entry: a number (own 0), or the diagonal itself (own 1, lead 0).  In
+// units of X under kS.  WIDE: rows <= cols, the diagonal runs along the rows.
 template <bool WIDE>
 struct NsApply {
   const uint16_t* hi;
   const uint16_t* lo;
   const float* d;
   int rows, cols;
+  float own, lead;               // both over kLo
   NsPart p;
   int r16, c4;
-  struct Row { float d; };
+  struct Row { float d, e; };
   struct Col { ntf4 d; };
   struct Add { ntu2 hi, lo; };
   __device__ __forceinline__ int64_t at(int e, int64_t m0, int64_t n0, int r16_, int c4_) {
@@ -315,7 +326,11 @@ struct NsApply {
     c4 = c4_;
     return o;
   }
-  __device__ __forceinline__ Row row(int i) const { return Row{WIDE ? d[min(16 * i, p.M - 16) + r16] : 0.0f}; }
+  __device__ __forceinline__ Row row(int i) const {
+    if constexpr (!WIDE) return Row{0.0f, 0.0f};
+    const float v = d[min(16 * i, p.M - 16) + r16];
+    return Row{v, __builtin_fmaf(own, v, lead)};
+  }
   __device__ __forceinline__ Col col(int j) const {
     if constexpr (WIDE) return Col{ntf4{0.0f, 0.0f, 0.0f, 0.0f}};
     else return Col{*reinterpret_cast<const ntf4*>(d + min(16 * j, p.N - 16) + c4)};
@@ -330,8 +345,8 @@ struct NsApply {
     for (int i = 0; i < 4; ++i) {
       const float h = i & 1 ? f16_hi(o.hi[i >> 1]) : f16_lo(o.hi[i >> 1]);
       const float l = i & 1 ? f16_hi(o.lo[i >> 1]) : f16_lo(o.lo[i >> 1]);
-      const float x = __builtin_fmaf(l, 1.0f / kLo, h);
-      y[i] = __builtin_fmaf(v[i], 1.0f / kS, (WIDE ? a.d : b.d[i]) * x);
+      const float x = WIDE ? __builtin_fmaf(l, a.e, a.d * h) : __builtin_fmaf(l, __builtin_fmaf(own, b.d[i], lead), b.d[i] * h);
+      y[i] = __builtin_fmaf(v[i], 1.0f / kS, x);
     }
   }
 };
@@ -528,7 +543,7 @@ bool ns_sizes(int64_t batch, int64_t rows, int64_t cols, NsSizes* z) {
 }
 
 // P X in the matrix's own orientation, X being x [m][n] and its transpose xt: the next X
-// (x, its transpose xn, the rest lo), or the result.
+// (x, its transpose xn, the rest lo), or the result.  own, lead: NsApply's, in units of X.
 struct NsBuffers {
   uint16_t* x;
   uint16_t* xt;
@@ -537,9 +552,9 @@ struct NsBuffers {
   NsSquare p;
 };
 template <bool WIDE>
-hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool more, hipStream_t s) {
+hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, float own, float lead, bool more, hipStream_t s) {
   const uint16_t *l = WIDE ? b.p.e : b.xt, *r = WIDE ? b.xt : b.p.e;
-  const NsApply<WIDE> a{WIDE ? b.x : b.xt, b.lo, b.p.d, (int)z.rows64, (int)z.cols64};
+  const NsApply<WIDE> a{WIDE ? b.x : b.xt, b.lo, b.p.d, (int)z.rows64, (int)z.cols64, own / kLo, lead / kLo};
   const auto run = [&](const auto& epi) { return product(o, l, r, z.rows64, z.cols64, z.m, false, epi, s); };
   if (more) return run(EpiNsNext<WIDE>{a, WIDE ? b.x : b.xn, b.lo, WIDE ? b.xn : b.x});
   if (o.w)
@@ -556,10 +571,10 @@ hipError_t apply(const OrthoArgs& o, const NsSizes& z, const NsBuffers& b, bool 
 // a^2 until A is formed afresh, so a pair is followed by a single step, and is taken
 // where the matrix is far enough from square to have few singular values near zero and
 // the a's are small (at most 12; the usual ones 11.9).  Simulated distance from the 64-bit
-// result one by one / in pairs with singles between: gradients of 512 x 1,792 4.1e-4,
-// 2.9e-4 (2 and 3 steps at once: 6.4e-4), 600 x 800 5.2e-4, 7.2e-4, 1,024 x 1,024 5.8e-4,
-// 1.4e-3 (4.1e-3); singular values spread over e^5 at 600 x 800 6.9e-4, 2.2e-3; all five at
-// once infinity.  16 x 1,408 x 2,048: 1,981 us one by one, 1,788 in pairs;
+// result one by one / in pairs with singles between: gradients of 512 x 1,792 4.2e-4,
+// 2.9e-4 (2 and 3 steps at once: 6.4e-4), 600 x 800 5.5e-4, 8.0e-4, 1,024 x 1,024 5.9e-4,
+// 1.4e-3 (4.1e-3); singular values spread over e^5 at 600 x 800 6.1e-4, 1.9e-3 (9.7e-3; all five
+// at once 2.6e-2); rank 128 at 320 x 512 1e-3, 3.8e-3.  16 x 1,408 x 2,048: 1,981 us one by one, 1,788 in pairs;
 // but a pair is 7 launches, two steps 6, which is what a small matrix costs (192 x 256: 79 us
 // one by one, 93 in pairs).
 int phase_steps(const OrthoArgs& o, const NsSizes& z, int i, int before) {
@@ -626,8 +641,12 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
     epi.alpha = k[2] / kS, epi.k0 = 0.5f * k[1], epi.k1 = k[2], epi.q0 = k[0], epi.q1 = k[1], epi.q2 = k[2];
     return product(o, l.e, l.e, z.m, z.m, z.m, true, epi, s);
   };
-  for (int i = 0, r = 0; i < o.steps;) {
+  int phases = 0;
+  for (int i = 0, r = 0; i < o.steps; i += r, ++phases) r = phase_steps(o, z, i, r);
+  for (int i = 0, r = 0; i < o.steps; --phases) {
     r = phase_steps(o, z, i, r);
+    const bool last = phases <= 2;                         // of two
+    const float own = last ? 1.0f : 0.0f, lead = last ? 0.0f : o.coefs[3 * i] * (r == 2 ? o.coefs[3 * i + 3] : 1.0f);
     EpiNsSquare<kNsGram> gram{ga, nullptr, nullptr, nullptr, nullptr, (int)z.m};
     gram.alpha = 1.0f / kS;
     e = product(o, x, x, z.m, z.m, z.n, true, gram, s);
@@ -641,7 +660,7 @@ hipError_t launch_ortho(const OrthoArgs& o, hipStream_t s) {
     }
     i += r;
     const NsBuffers b{x, xt, xn, lo, pp};
-    if (e == hipSuccess) e = wide ? apply<true>(o, z, b, i < o.steps, s) : apply<false>(o, z, b, i < o.steps, s);
+    if (e == hipSuccess) e = wide ? apply<true>(o, z, b, own, lead, i < o.steps, s) : apply<false>(o, z, b, own, lead, i < o.steps, s);
     if (e != hipSuccess) return e;
     std::swap(xt, xn);
   }

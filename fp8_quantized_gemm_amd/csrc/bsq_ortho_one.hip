@@ -3,8 +3,9 @@
 // in how many bits as in bsq_ortho.hip, X itself in FP32).
 //
 // What bounds small matrices is the launches: 15 products of 4 to 6 us each (200 x 136: 79
-// us; 55 here, an update's 70; 256 of 128 x 128: 150, 39).  Here a workgroup of eight waves holds a matrix in its compute unit: X in FP32 in
-// the registers of the waves that compute its tiles, and in LDS the symmetric matrix E and
+// us; 63 here, an update's 78; 256 of 128 x 128: 150, 41).  Here a workgroup of eight waves
+// holds a matrix in its compute unit: X in FP32 in the registers of the waves that compute its
+// tiles, and in LDS the symmetric matrix E and
 // X's FP16 form, by rows for the Gram matrix and then by columns for the product with the
 // polynomial, as the MFMA takes operands with K running along a row.  The reads of LDS
 // bound the products, so a wave computes 32 x 32 entries at a time of the symmetric ones,
@@ -385,11 +386,16 @@ __global__ __launch_bounds__(kOneWaves * 64) void k_ns_one(NsOne o) {
           acc[0] = nt_mfma<kNtF16>(f[0][k], e[i & 1][k], acc[0]);
           acc[1] = nt_mfma<kNtF16>(f[1][k], e[i & 1][k], acc[1]);
         }
-        const float di = D[16 * i + r16];
+        // P's diagonal times X's FP16 form, and the rest of X's rounding times the leading
+        // coefficient, or the diagonal in the last two steps (see bsq_ortho.hip)
+        const float di = D[16 * i + r16], rest = s + 2 < o.steps ? a : di;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[j][i][h][k] = __builtin_fmaf(acc[h][k], 1.0f / kS, di * x[j][i][h][k]);
+          for (int k = 0; k < 4; ++k) {
+            const float y = x[j][i][h][k], half = (float)(_Float16)y;
+            x[j][i][h][k] = __builtin_fmaf(acc[h][k], 1.0f / kS, __builtin_fmaf(y - half, rest, di * half));
+          }
       }
     }
     __syncthreads();

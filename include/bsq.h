@@ -602,10 +602,13 @@ bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, in
  * (on the transpose where rows > cols, which is the same).  The products take FP16
  * matrices under a power of two (each rounding at most 2^-11 of the value) and sum in
  * FP32; X itself is held to 22 bits, the diagonals of A and the polynomials in FP32,
- * the norm in FP64: five steps are about 5e-4 (relative, Frobenius) from the exact
- * result on gradients, 2e-3 where singular values are spread over two decades. 
- * Coefficients must keep singular values below 8.  A zero matrix gives zeros; a matrix
- * with NaN or infinities gives NaN of its own.
+ * the norm in FP64.  Five steps of the usual coefficients are 3e-4 to 1e-3 (relative,
+ * Frobenius) from the exact result on gradients, and at most 2e-3 on a matrix of any rank
+ * and any spread of its singular values; 5e-3 for fewer than 16 rows or columns, and where
+ * steps are taken in pairs (the smaller side, in multiples of 64, above 256, and the larger
+ * at least 4/3 of it).  More steps add up in proportion.  Coefficients must keep singular
+ * values below 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of
+ * its own.
  *   x     : in, [batch, rows, cols] of type.   out : out, BF16 [batch, rows, cols].
  *   coefs : in, HOST array of 3 * steps floats, 1 <= steps <= 32.   eps > 0.
  *   workspace : device memory, 256-byte aligned.
@@ -619,7 +622,7 @@ bsq_status orthogonalize(const void* x, bsq_dtype type, int64_t batch, int64_t r
  *   momentum <- mu * momentum + grad;   u = grad + mu * momentum (nesterov) or momentum
  *   w32 <- (1 - lr * weight_decay) * w32 - lr * scale * orthogonalize(u)
  *   w_bf16 <- BF16_RNE(w32);  amax <- max|w_bf16| over the stack
- * (FP32; orthogonalize's result rounded to FP16 here).  amax is the per-tensor amax of
+ * (FP32; orthogonalize's result in FP32, or rounded to FP16 here).  amax is the per-tensor amax of
  * the next weight quantization, as for master_weight_update.
  *   w32, momentum : in/out, FP32 [batch, rows, cols].  grad : in, BF16.
  *   w_bf16 : out, BF16.  amax : out, device FP32 or NULL.  No two may overlap.

@@ -4,7 +4,12 @@ include/bsq.h).
 orthogonalize: the definition in FP64.  orthogonalize_f16: the same with what is held
 between products rounded as the kernels hold it (X as an FP16 matrix and the FP16 rest
 of its rounding, symmetric matrices as an FP32 diagonal and an FP16 rest), for the size
-of error that these roundings cause; sums are FP64 here, FP32 in the kernels."""
+of error that these roundings cause; sums are FP64 here, FP32 in the kernels.
+
+The rest of X's rounding is multiplied by the phase's leading coefficient (the product of a
+pair's), in the last two phases by the polynomial's diagonal, in place of the polynomial
+P = a I + b A + c A^2.  What that leaves out, (P - a) lo, is zero on directions with singular
+value zero, the only ones along which it would grow (by a in each step that follows)."""
 
 import numpy as np
 
@@ -74,9 +79,10 @@ def orthogonalize_f16(x, steps=5, coefs=COEFS, eps=1e-7, plan=None):
     eye, c = np.eye(t.shape[0]), _steps(steps, coefs)
     plan = [1] * steps if plan is None else plan
     i = 0
-    for r in plan:
+    for phase, r in enumerate(plan):
         hi = half(t * S) / S
-        whole = hi + half((t - hi) * S * LO) / (S * LO)
+        lo = half((t - hi) * S * LO) / (S * LO)
+        lead = np.prod([c[i + j][0] for j in range(r)])
         g, p = split(hi @ hi.T), None
         for j in range(r):
             q = split(c[i][0] * eye + c[i][1] * (np.diag(g[0]) + g[1]) + c[i][2] * times(g, g))
@@ -84,7 +90,7 @@ def orthogonalize_f16(x, steps=5, coefs=COEFS, eps=1e-7, plan=None):
                 g = split(times(split(times(q, g)), q))
             p = q if p is None else split(times(q, p))
             i += 1
-        t = p[0][:, None] * whole + p[1] @ hi
+        t = p[0][:, None] * hi + (lead if phase + 2 < len(plan) else p[0][:, None]) * lo + p[1] @ hi
     return t.T if x.shape[0] > x.shape[1] else t
 
 
