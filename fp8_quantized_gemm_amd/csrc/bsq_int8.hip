@@ -12,8 +12,11 @@ namespace {
 
 // ---------------------------------------------------------------- encode
 
-// (A comparison, not fminf: a NaN stays one, and the scale is the only place that can carry
-// it to the product.  Under an infinity s_enc is 0, the codes too, and the scale infinite.)
+// (A reciprocal and a product, as tensor programs compute 127.0 / amax, so that their codes
+// are met bit for bit; at most 1.5 2^-24 from the quotient, 4 2^-24 above 2^126, where the
+// reciprocal is subnormal.  A comparison, not fminf: a NaN stays one, and the scale is the only
+// place that can carry it to the product.  Under an infinity s_enc is 0, the codes too, and the
+// scale infinite.)
 __device__ __forceinline__ float i8_enc(uint32_t amax_bits) {
   const float amax = u2f(amax_bits), s = 127.0f * (1.0f / amax);
   return amax == 0.0f ? 1.0f : s > kFltMax ? kFltMax : s;
@@ -432,8 +435,8 @@ bool i8_few_rows(const Int8Args& a) {
   if (a.M > kFewRows || a.K <= 0 || a.K % 16 != 0 || a.K > 8192) return false;
   // few pieces of x cost little beside the weights; more of them pay only where every
   // workgroup runs at once, and there by the launch that the host saves (us on the GPU by this
-  // launch / by two: 1 x 28,672 x 4,096 25.9 / 29.8, 1 x 4,096 x 4,096 7.1 / 13.2, 3 x 1,000 x
-  // 512 4.3 / 7.9; 48 x 2,048 x 2,048 9.3 / 9.3, 37 x 2,048 x 1,408 10.2 / 8.1 but 10.4 / 13.1
+  // launch / by two: 1 x 28,672 x 4,096 25.6 / 29.8, 1 x 4,096 x 4,096 7.1 / 13.2, 3 x 1,000 x
+  // 512 4.3 / 7.9; 48 x 2,048 x 2,048 9.3 / 9.3, 37 x 2,048 x 1,408 11.0 / 8.1 but 11.0 / 13.1
   // a call from Python; 8 x 28,672 x 4,096 45.7 / 30.0)
   const int64_t pieces = a.M * ((a.K + 511) / 512);
   return pieces <= 2 * kFewWaves || (pieces <= kFewPieces && (a.N + 15) / 16 <= 256);

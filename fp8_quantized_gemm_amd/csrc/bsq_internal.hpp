@@ -271,7 +271,7 @@ hipError_t launch_i8_qt(const void* x, int64_t rows, int64_t cols, uint8_t* code
                         uint8_t* codes_col, float* scales_col, uint32_t* amax, hipStream_t s);
 
 struct Int8Args {
-  int64_t M, N, K;                // 0 < K < 2^17
+  int64_t M, N, K;                // 0 <= K < 2^17
   const uint8_t* ac;              // [M, K]
   const float* as;                // [M]
   const uint8_t* bc;              // [N, K]

@@ -1,5 +1,5 @@
 // The LDS-staged kernel of the plain products (bsq_nt.hpp): C = A . B^T of 8-bit
-// integers or FP16 on square tiles of 256, 192, 128 or 64.
+// integers or FP16 on square tiles of 256, 192, 128, 96 or 64.
 //
 // A workgroup of four waves (one per SIMD) per tile of 32 NT rows and columns; wave w
 // owns the quarter (w >> 1, w & 1) as NT x NT accumulators of 16 x 16, pinned in
@@ -22,8 +22,12 @@
 // of one parity start on the same bank.
 //
 // Smaller tiles read more bytes per operation (256: 64 KB of LDS fill per 2^23
-// multiply-adds of FP16; 192: 1.33, 128: 2 times as much) and exist for shapes whose
-// 256 tiles would leave compute units idle.
+// multiply-adds of 8-bit integers, per 2^22 of FP16; 192: 1.33, 128: 2 times as much) and
+// exist for shapes whose 256 tiles would leave compute units idle.
+//
+// On tiles of 256 the epilogues of the orthogonalisation's polynomial and product need more
+// registers than a wave has: 33 and 71 VGPRs go to scratch memory (136 and 288 bytes a lane),
+// the next X of tall matrices 1 VGPR (8 bytes).
 #pragma once
 
 #include "bsq_nt.hpp"
@@ -479,8 +483,10 @@ void k_nt_ring(NtArgs g, NtGrid d, Epi epi) {
 // FP16 takes 1.2 times as long): a unit of 128 bytes of K when all compute units are busy
 // and when few are, a tile besides its units, and what the epilogue of a polynomial of the
 // orthogonalisation takes on top (Epi::kWork: how many times that another one takes).
-// `per_cu` workgroups share a compute unit at that cost.  Fitted to 210 kernel times of 22
-// sizes, 8% root mean square; the choice is at most 3% behind the best kernel on each but one (7%).
+// `per_cu` workgroups share a compute unit at that cost.  On 80 random sizes that none of these
+// numbers was fitted to (M 1 to 22,000, N 64 to 32,000, K 128 to 22,000) the call is within 10% of
+// the best kernel on 73, at most 18% behind (37 x 21,539 x 14,464), at best 7% ahead, on two
+// kernels; profiles/int8_kernel_choice.txt has each.
 struct NtCost {
   int kernel, side_m, side_n, per_cu;
   float full, few, tile, work;

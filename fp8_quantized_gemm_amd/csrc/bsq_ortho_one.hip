@@ -5,11 +5,13 @@
 // What bounds small matrices is the launches: 15 products of 4 to 6 us each (200 x 136: 79
 // us; 63 here, an update's 78; 256 of 128 x 128: 150, 41).  Here a workgroup of eight waves
 // holds a matrix in its compute unit: X in FP32 in the registers of the waves that compute its
-// tiles, and in LDS the symmetric matrix E and
-// X's FP16 form, by rows for the Gram matrix and then by columns for the product with the
-// polynomial, as the MFMA takes operands with K running along a row.  The reads of LDS
-// bound the products, so a wave computes 32 x 32 entries at a time of the symmetric ones,
-// and 32 columns of X under every row of the polynomial.
+// tiles, and in LDS the symmetric matrix E and X's FP16 form, by rows for the Gram matrix and
+// then by columns for the product with the polynomial, as the MFMA takes operands with K
+// running along a row.  The products read LDS more than they multiply, so a wave computes 32 x
+// 32 entries at a time of the symmetric ones, and 32 columns of X under every row of the
+// polynomial.  What bounds it is latency: of 200 x 136 LDS is busy for 41% of the time, the
+// VALU 40%, the matrix pipe 18%, and the waves, two a SIMD, wait for half of theirs in phases
+// that depend on each other.
 #include "bsq_ortho.hpp"
 #include "bsq_wave.hpp"
 

@@ -538,13 +538,14 @@ bsq_status bs_gemm_grouped_wgrad(bsq_format fmt, int experts, const int32_t* off
 
 /*
  * Codes of the rows of x[rows, cols] (BF16), one scale per row:
- *   amax = max|x| of the row; s_enc = 127 * (1/amax) (1 if amax == 0; <= FLT_MAX);
+ *   amax = max|x| of the row; s_enc = 127 * (1/amax), two roundings (1 if amax == 0;
+ *   <= FLT_MAX);
  *   scale = 1/s_enc; code = RNE(x * s_enc), in [-127, 127]
  * (FP32 IEEE RNE at every step).  NaN and infinities touch their own row only: a row
  * with NaN has scale NaN, one with infinities and no NaN scale infinity and codes 0, so
  * that either's products are NaN.
  *   codes  : out, int8 [rows, cols].  scales : out, FP32 [rows].
- * Any rows, any cols.
+ * Any rows, any cols (cols == 0: scales of 1).
  */
 bsq_status int8_quantize(const void* x, int64_t rows, int64_t cols, int8_t* codes, float* scales,
                          void* stream);
