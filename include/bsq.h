@@ -607,9 +607,10 @@ bsq_status orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols, in
  * Frobenius) from the exact result on gradients, and at most 2e-3 on a matrix of any rank
  * and any spread of its singular values; 5e-3 for fewer than 16 rows or columns, and where
  * steps are taken in pairs (the smaller side, in multiples of 64, above 256, and the larger
- * at least 4/3 of it).  More steps add up in proportion.  Coefficients must keep singular
- * values below 8.  A zero matrix gives zeros; a matrix with NaN or infinities gives NaN of
- * its own.
+ * at least 4/3 of it).  Each further step multiplies what the last bits of X and of the
+ * sums leave along singular values of zero by its a: eight steps are at most 8e-3 up to
+ * 4,096 rows.  Coefficients must keep singular values below 8.  A zero matrix gives zeros; a
+ * matrix with NaN or infinities gives NaN of its own.
  *   x     : in, [batch, rows, cols] of type.   out : out, BF16 [batch, rows, cols].
  *   coefs : in, HOST array of 3 * steps floats, 1 <= steps <= 32.   eps > 0.
  *   workspace : device memory, 256-byte aligned.

@@ -27,9 +27,12 @@ def matrices(m, n, seed=0):
 def stated(m, n, steps=5):
     """The accuracy of include/bsq.h: five steps 2e-3 one at a time, 5e-3 for fewer than 16
     rows (columns) and in pairs.  Every step rounds as many values to as many bits, and what one
-    leaves does not grow in those after it (along singular values near zero, where all would
-    grow, nothing is left; elsewhere the step's polynomial brings singular values together), so
-    the roundings of k steps add up to at most k / 5 of those of five."""
+    leaves of FP16's bits does not grow in those after it (along singular values near zero, where
+    all would grow, nothing is left; elsewhere the step's polynomial brings singular values
+    together), so the roundings of k steps add up to at most k / 5 of those of five.  (The last
+    bits of X, 2^-24, do grow: to 2^-24 3.44^8 = 1.2e-3 after eight steps, within the 3.2e-3 that
+    this gives for one at a time.  FP32 sums add as much again for each doubling of the square
+    root of their length, so smaller sides above 512 are left out for eight steps.)"""
     return (5e-3 if min(m, n) < 16 or 2 in OM.plan(m, n, steps) else 2e-3) * max(1.0, steps / 5)
 
 

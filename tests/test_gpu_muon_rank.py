@@ -37,6 +37,17 @@ def test_any_rank(shape, steps):
         assert d <= stated(*shape, steps) + 2.0 ** -11, (shape, steps, name, d)
 
 
+@pytest.mark.parametrize("shape,rank", [((1408, 2048), 1), ((1408, 2048), 176), ((1408, 2048), 469), ((2048, 2048), 1),
+                                        ((2048, 2048), 682), ((4096, 1024), 341)])
+def test_sizes_of_layers(shape, rank):
+    """Rank 1, m / 8 and m / 3 (where pairs of steps are furthest off)."""
+    announce("muon_update, rank", shape, rank)
+    g = torch.Generator().manual_seed(5)
+    t = torch.randn(shape[0], rank, generator=g) @ torch.randn(rank, shape[1], generator=g)
+    d = distance(_orthogonal(t, 5), OM.orthogonalize(t.double().numpy()))
+    assert d <= stated(*shape) + 2.0 ** -11, d
+
+
 @pytest.mark.parametrize("shape", [(64, 128), (200, 330), (320, 512)])
 def test_one_token(shape):
     """A weight's gradient after one token (rank 1), through orthogonalize and its BF16 output."""
