@@ -483,9 +483,9 @@ void k_nt_ring(NtArgs g, NtGrid d, Epi epi) {
 // FP16 takes 1.2 times as long): a unit of 128 bytes of K when all compute units are busy
 // and when few are, a tile besides its units, and what the epilogue of a polynomial of the
 // orthogonalisation takes on top (Epi::kWork: how many times that another one takes).
-// `per_cu` workgroups share a compute unit at that cost.  On 80 random sizes that none of these
+// `per_cu` workgroups share a compute unit at that cost.  On 79 random sizes that none of these
 // numbers was fitted to (M 1 to 22,000, N 64 to 32,000, K 128 to 22,000) the call is within 10% of
-// the best kernel on 73, at most 18% behind (37 x 21,539 x 14,464), at best 7% ahead, on two
+// the best kernel on 72, at most 18% behind (37 x 21,539 x 14,464), at best 7% ahead, on two
 // kernels; profiles/int8_kernel_choice.txt has each.
 struct NtCost {
   int kernel, side_m, side_n, per_cu;
