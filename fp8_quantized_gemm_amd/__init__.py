@@ -175,6 +175,12 @@ def _check_out(out, M, N, dtype):
         raise ValueError(f"out must be a {dtype} [{M}, {N}] tensor")
 
 
+def _row_stride(out):
+    """ldc of a checked out [M, N].  Rows that overlap (an expanded tensor) give a stride
+    below N, which the library refuses; a single row's stride means nothing."""
+    return out.stride(0) if out.shape[0] > 1 else out.shape[1]
+
+
 def _check_input(x):
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype == torch.bfloat16 and x.dim() == 2):
         raise ValueError("x must be a 2-D bfloat16 CUDA tensor")
@@ -732,7 +738,7 @@ def bs_gemm_grouped(fmt, a_codes, a_scales, b_codes, b_scales, offsets, a_amax=N
         _check_out(out, M, N, torch.bfloat16)
     st = lib().bs_gemm_grouped(FORMATS[fmt], E, _ptr(offsets), M, N, K, _ptr(a_codes), _ptr(a_scales),
                                _ptr(a_amax), _ptr(b_codes), _ptr(b_scales), _ptr(b_amax), bn, _ptr(out),
-                               max(out.stride(0), N), _stream(out.device))
+                               _row_stride(out), _stream(out.device))
     _check("bs_gemm_grouped", st)
     return out
 
@@ -851,7 +857,7 @@ def int8_gemm(a_codes, a_scales, b_codes, b_scales, bias=None, out=None):
     if out is None:
         out = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
     _call("int8_gemm", dev, M, N, K, _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), _ptr(bias), _ptr(out),
-          max(out.stride(0), N))
+          _row_stride(out))
     return out
 
 
@@ -871,7 +877,7 @@ def int8_linear(x, w_codes, w_scales, bias=None, out=None):
     need = _size("int8_linear_workspace", M, K)
     ws = _u8(need, dev)
     _call("int8_linear", dev, _ptr(x), M, N, K, _ptr(w_codes), _ptr(w_scales), _ptr(bias), _ptr(out),
-          max(out.stride(0), N), _ptr(ws), need)
+          _row_stride(out), _ptr(ws), need)
     return out
 
 
